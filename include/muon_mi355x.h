@@ -1,5 +1,6 @@
 /*
- * muon_mi355x.h - C ABI of the MI355X (gfx950) Muon + AdamW optimizer step.
+ * muon_mi355x.h - C ABI of the MI355X (gfx950) Muon + AdamW optimizer step and
+ * of what a training loop computes to feed it.
  *
  * The library updates optimizer state and parameters that the caller owns, on
  * the caller's HIP stream, with hand-written CDNA4 kernels. It never allocates
@@ -53,10 +54,14 @@
  * A device fault inside a kernel is asynchronous and surfaces at the caller's
  * next synchronisation. Calls that share a workspace must not overlap in time.
  * Streams are passed as void* and must be hipStream_t values (0 = null stream).
- * Calls cannot be captured into a HIP graph: on a capturing stream every
- * entry point returns MU_ERR_INVALID_ARG without enqueuing anything (each
- * call stages its descriptor table through pinned host memory that later
- * calls reuse, so a replayed capture would read another call's table).
+ * The optimizer steps, mu_muon_orthogonalize and mu_qk_clip cannot be captured
+ * into a HIP graph: on a capturing stream they return MU_ERR_INVALID_ARG
+ * without enqueuing anything (each call stages its descriptor table through
+ * pinned host memory that later calls reuse, so a replayed capture would read
+ * another call's table). mu_grad_norm, mu_clip_grads, mu_embedding,
+ * mu_embedding_grad and mu_qk_max_logits carry their lists in the kernels'
+ * arguments and can be captured; a replay works on the buffers of the captured
+ * call, the workspace among them, which must live as long as the graph.
  */
 #ifndef MUON_MI355X_H
 #define MUON_MI355X_H
@@ -245,6 +250,147 @@ int mu_qk_clip_workspace_size(const mu_qk_pair* pairs, int32_t n, size_t* bytes)
 int mu_qk_clip(const mu_qk_pair* pairs, int32_t n, float tau, void* workspace, size_t workspace_bytes,
                void* stream);
 
+/*
+ * Global gradient norm and clipping over a list of tensors of mixed types:
+ *   norm = sqrt(sum over all elements of g^2)
+ *   c    = min(1, max_norm / (norm + eps)), rounded to float32
+ * The squares and their sum are float64 in a fixed order: no overflow or
+ * underflow for any finite gradient, and the same list gives the same bits.
+ * NaN anywhere makes norm and c NaN; an infinity makes norm infinite and c 0.
+ *
+ * grad      [numel] dtype, read only unless out is the same buffer
+ * out       mu_clip_grads: [numel] out_dtype receiving c * g (the float32
+ *           product rounded to nearest even), with any mix of the two types;
+ *           the same pointer and dtype as grad scales in place (then nothing
+ *           is written where c is 1). mu_grad_norm ignores it.
+ */
+typedef struct mu_grad {
+    const void* grad;
+    void* out;
+    int64_t numel;
+    int32_t dtype;
+    int32_t out_dtype;
+} mu_grad;
+
+/* Workspace bytes of mu_grad_norm and mu_clip_grads for this list. */
+int mu_grad_norm_workspace_size(const mu_grad* gs, int32_t n, size_t* bytes);
+
+/* norm_out, scale_out: device float32, either may be NULL (not both). scale_out
+ * receives c, which needs max_norm >= 0 (finite or +inf) and eps >= 0. Buffers
+ * of the list may overlap each other (they are only read). */
+int mu_grad_norm(const mu_grad* gs, int32_t n, float max_norm, float eps, float* norm_out, float* scale_out,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* The norm and the scaled gradients; norm_out and scale_out are optional. */
+int mu_clip_grads(const mu_grad* gs, int32_t n, float max_norm, float eps, float* norm_out, float* scale_out,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mu_muon_step and mu_adamw_step with every gradient multiplied by *grad_scale
+ * (device float32, read when the kernels run; mu_grad_norm's scale_out) as it
+ * is read, in float32 and unrounded: a clipped step without a pass that writes
+ * the scaled gradients. NULL is the plain step.
+ */
+int mu_muon_step_scaled(const mu_matrix* mats, int32_t n, const mu_muon_hparams* hp, const float* grad_scale,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int mu_adamw_step_scaled(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, const float* grad_scale,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Embedding lookup: out[t, :] = scale * weight[tokens[t], :], the float32
+ * product rounded to nearest even (scale 1 copies the rows bit for bit). A
+ * token outside [0, vocab) reads nothing and its row becomes NaN.
+ * tokens [n_tokens] int32 or int64 (token_bits 32 | 64); weight [vocab, dim]
+ * and out [n_tokens, dim] share dtype.
+ */
+typedef struct mu_lookup {
+    const void* tokens;
+    const void* weight;
+    void* out;
+    int64_t n_tokens;
+    int64_t vocab;
+    int64_t dim;
+    int32_t token_bits;
+    int32_t dtype;
+    float scale;
+    int32_t pad0;
+} mu_lookup;
+int mu_embedding(const mu_lookup* e, void* stream);
+
+/*
+ * The gradient of an embedding from the gradients of its looked-up rows:
+ *   grad[v, :] = scale * sum over t with tokens[t] == v of rows[t, :]
+ * (accumulate = 1: added to what grad holds, in float32, rounded once). Each
+ * row's sum is float32 in an order fixed by the tokens alone, so the same call
+ * gives the same bits. Rows no token names become zero (accumulate: stay).
+ * Tokens outside [0, vocab) and tokens equal to padding_idx (-1: none) add
+ * nothing. rows [n_tokens, dim] row_dtype, grad [vocab, dim] grad_dtype, any
+ * mix of the two types. n_tokens < 2^31, vocab < 2^31.
+ */
+typedef struct mu_rowgrad {
+    const void* tokens;
+    const void* rows;
+    void* grad;
+    int64_t n_tokens;
+    int64_t vocab;
+    int64_t dim;
+    int64_t padding_idx;
+    int32_t token_bits;
+    int32_t row_dtype;
+    int32_t grad_dtype;
+    int32_t accumulate;
+    float scale;
+    int32_t pad0;
+} mu_rowgrad;
+int mu_embedding_grad_workspace_size(const mu_rowgrad* e, size_t* bytes);
+int mu_embedding_grad(const mu_rowgrad* e, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The largest attention logit magnitude of each query head, which mu_qk_clip
+ * takes as max_logit:
+ *   max_logit[h] = |scale| * max over sequences b and visible pairs (i, j) of
+ *                  |sum_d q[b, i, h, d] * k[b, j, h / G, d]|,  G = q_heads / k_heads
+ * float32 accumulation (bfloat16 products are exact); 0 for a head without a
+ * visible pair. A NaN logit at a visible pair makes the result NaN; what
+ * invisible positions hold does not matter. causal = 1: query i of a sequence
+ * with nq queries and nk keys sees keys j <= i + nk - nq.
+ *
+ * q, k      element (b, s, h, d) at b * stride_b + s * stride_s + h * stride_h
+ *           + d (strides in elements, >= 0); dtype MU_F32 | MU_BF16; dim 1..256
+ * padded    cu_q == NULL: batch sequences of q_len queries and k_len keys; with
+ *           q_lengths (k_lengths; device int32 [batch], NULL: all of them) only
+ *           the first so many of each, clamped to [0, q_len]
+ * packed    cu_q != NULL: device int32 [batch + 1], sequence b holds rows
+ *           cu_q[b] .. cu_q[b+1] - 1 of q and cu_k[b] .. of k (cu_k NULL: cu_q);
+ *           q_len and k_len are the packed buffers' row counts, to which the
+ *           entries are clamped; stride_b and the lengths are not used
+ * max_logit device float32 [q_heads]; accumulate = 1 keeps what is larger there
+ *           (values >= 0, as this call writes), over micro-batches of a step
+ */
+#define MU_QK_MAX_DIM 256
+typedef struct mu_qk_logits {
+    const void* q;
+    const void* k;
+    int64_t q_stride_b, q_stride_s, q_stride_h;
+    int64_t k_stride_b, k_stride_s, k_stride_h;
+    int64_t q_len;
+    int64_t k_len;
+    int32_t batch;
+    int32_t q_heads;
+    int32_t k_heads;
+    int32_t dim;
+    const int32_t* q_lengths;
+    const int32_t* k_lengths;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int32_t dtype;
+    int32_t causal;
+    int32_t accumulate;
+    float scale;
+    float* max_logit;
+} mu_qk_logits;
+int mu_qk_max_logits(const mu_qk_logits* a, void* stream);
+
 /* Workspace bytes mu_muon_step needs for this list (n == 0 gives 0). */
 int mu_muon_workspace_size(const mu_matrix* mats, int32_t n, const mu_muon_hparams* hp, size_t* bytes);
 
@@ -313,7 +459,12 @@ int mu_version(void);
 #define MU_K_FUSED 8     /* every step but the last apply of mp == 128 problems (>= 256 in a call) */
 #define MU_K_RESCALE 9   /* exact 2^e rescale of X0 where ||U||_F is outside [2^-24, 2^24] */
 #define MU_K_TILEMAP 10  /* per call: each GEMM tile's problem and coordinates, resolved once */
-#define MU_K_COUNT 11
+#define MU_K_GRADNORM 11 /* global gradient norm: squares, and the final sum */
+#define MU_K_CLIP 12     /* scaled gradients */
+#define MU_K_LOOKUP 13   /* embedding lookup */
+#define MU_K_ROWGRAD 14  /* embedding gradient: token sort, row sums, joins */
+#define MU_K_QKMAX 15    /* attention max logits */
+#define MU_K_COUNT 16
 int mu_profile_enable(int on);
 int mu_profile_read(int kernel, double* total_ms, int64_t* launches, double* flops, double* bytes);
 const char* mu_kernel_name(int kernel);

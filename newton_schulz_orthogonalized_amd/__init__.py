@@ -1,16 +1,20 @@
 """MI355X-native Muon optimizer step (momentum, Frobenius normalisation,
 Newton-Schulz orthogonalisation, decoupled-weight-decay update) and fused
-AdamW, on hand-written gfx950 HIP kernels behind a C ABI.
+AdamW, on hand-written gfx950 HIP kernels behind a C ABI, with what a training
+loop computes to feed the step: gradient norm and clipping, the embedding and
+its gradient, and the attention max logits of QK-Clip.
 
 The HIP library is loaded on first use of any compute entry point; a missing
 library raises ImportError (there is no CPU fallback).
 """
 
-__all__ = ["muon_step", "orthogonalize", "adamw_step", "qk_clip", "muon_workspace_bytes", "MuonAdamW", "split_params"]
+_CALLS = ("muon_step", "orthogonalize", "adamw_step", "qk_clip", "muon_workspace_bytes", "grad_norm", "clip_grads",
+          "embedding", "embedding_grad", "qk_max_logits")
+__all__ = [*_CALLS, "MuonAdamW", "split_params"]
 
 
 def __getattr__(name):
-    if name in ("muon_step", "orthogonalize", "adamw_step", "qk_clip", "muon_workspace_bytes"):
+    if name in _CALLS:
         from . import api
         return getattr(api, name)
     if name in ("MuonAdamW", "split_params"):

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -31,13 +32,15 @@ MU_ERR_WORKSPACE = 4
 MU_ERR_HIP = 5
 
 (MU_K_PREP, MU_K_NORM, MU_K_GRAM, MU_K_GRAM2, MU_K_APPLY, MU_K_FINISH, MU_K_ADAMW, MU_K_QKCLIP, MU_K_FUSED,
- MU_K_RESCALE, MU_K_TILEMAP) = range(11)
-MU_K_COUNT = 11
+ MU_K_RESCALE, MU_K_TILEMAP, MU_K_GRADNORM, MU_K_CLIP, MU_K_LOOKUP, MU_K_ROWGRAD, MU_K_QKMAX) = range(16)
+MU_K_COUNT = 16
 
 EXPORTED = (
     "mu_muon_workspace_size", "mu_muon_step", "mu_muon_step_noalloc", "mu_ortho_workspace_size",
     "mu_muon_orthogonalize",
     "mu_adamw_workspace_size", "mu_adamw_step", "mu_qk_clip_workspace_size", "mu_qk_clip",
+    "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm", "mu_clip_grads",
+    "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad", "mu_qk_max_logits",
     "mu_status_string", "mu_last_error", "mu_version", "mu_profile_enable", "mu_profile_read", "mu_kernel_name",
 )
 
@@ -90,6 +93,37 @@ class MuQkPair(ctypes.Structure):
     ]
 
 
+class MuGrad(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class MuLookup(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("token_bits", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("pad0", ctypes.c_int32)]
+
+
+class MuRowgrad(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("n_tokens", ctypes.c_int64), ("vocab", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("padding_idx", ctypes.c_int64), ("token_bits", ctypes.c_int32), ("row_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("pad0", ctypes.c_int32)]
+
+
+class MuQkLogits(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_stride_b", ctypes.c_int64), ("q_stride_s", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k_stride_b", ctypes.c_int64), ("k_stride_s", ctypes.c_int64), ("k_stride_h", ctypes.c_int64),
+                ("q_len", ctypes.c_int64), ("k_len", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("q_lengths", ctypes.c_void_p), ("k_lengths", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float), ("max_logit", ctypes.c_void_p)]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{_status_text(status)} (status {status}): {detail}")
@@ -115,6 +149,16 @@ def _load() -> ctypes.CDLL:
                                   ctypes.c_void_p]
     lib.mu_qk_clip_workspace_size.argtypes = [P(MuQkPair), ctypes.c_int32, P(sz)]
     lib.mu_qk_clip.argtypes = [P(MuQkPair), ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, sz, ctypes.c_void_p]
+    vp = ctypes.c_void_p
+    lib.mu_muon_step_scaled.argtypes = [P(MuMatrix), ctypes.c_int32, P(MuMuonHparams), vp, vp, sz, vp]
+    lib.mu_adamw_step_scaled.argtypes = [P(MuTensor), ctypes.c_int32, P(MuAdamwHparams), vp, vp, sz, vp]
+    lib.mu_grad_norm_workspace_size.argtypes = [vp, ctypes.c_int32, P(sz)]   # mu_grad lists are packed bytes (gradients())
+    for name in ("mu_grad_norm", "mu_clip_grads"):
+        getattr(lib, name).argtypes = [vp, ctypes.c_int32, ctypes.c_float, ctypes.c_float, vp, vp, vp, sz, vp]
+    lib.mu_embedding.argtypes = [P(MuLookup), vp]
+    lib.mu_embedding_grad_workspace_size.argtypes = [P(MuRowgrad), P(sz)]
+    lib.mu_embedding_grad.argtypes = [P(MuRowgrad), vp, sz, vp]
+    lib.mu_qk_max_logits.argtypes = [P(MuQkLogits), vp]
     lib.mu_status_string.argtypes = [ctypes.c_int]
     lib.mu_status_string.restype = ctypes.c_char_p
     lib.mu_last_error.argtypes = []
@@ -127,7 +171,10 @@ def _load() -> ctypes.CDLL:
     lib.mu_kernel_name.restype = ctypes.c_char_p
     for name in ("mu_muon_workspace_size", "mu_muon_step", "mu_muon_step_noalloc", "mu_ortho_workspace_size",
                  "mu_muon_orthogonalize",
-                 "mu_adamw_workspace_size", "mu_adamw_step", "mu_profile_enable", "mu_profile_read"):
+                 "mu_adamw_workspace_size", "mu_adamw_step", "mu_profile_enable", "mu_profile_read",
+                 "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm",
+                 "mu_clip_grads", "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad",
+                 "mu_qk_max_logits"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -222,6 +269,24 @@ def mu_muon_step(mats, n, hp, workspace: Optional[torch.Tensor], stream=None) ->
     _check(LIB.mu_muon_step(mats, n, ctypes.byref(hp), ws, nb, _stream(stream)))
 
 
+def grad_scale_ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    """Address of a clip factor: one float32 on the GPU (None: the plain step)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise TypeError("grad_scale must be one float32 element")
+    if not t.is_cuda:
+        raise ValueError("grad_scale must be a GPU tensor (it is read when the kernels run)")
+    return t.data_ptr()
+
+
+def mu_muon_step_scaled(mats, n, hp, grad_scale: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                        stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_muon_step_scaled(mats, n, ctypes.byref(hp), grad_scale_ptr(grad_scale), ws, nb, _stream(stream)))
+
+
 MU_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -285,6 +350,176 @@ def mu_adamw_step(ts, n, beta1: float, beta2: float, eps: float, step: int,
     ws = 0 if workspace is None else workspace.data_ptr()
     nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(LIB.mu_adamw_step(ts, n, ctypes.byref(hp), ws, nb, _stream(stream)))
+
+
+def mu_adamw_step_scaled(ts, n, beta1: float, beta2: float, eps: float, step: int,
+                         grad_scale: Optional[torch.Tensor], workspace: Optional[torch.Tensor], stream=None) -> None:
+    hp = MuAdamwHparams(beta1, beta2, eps, step)
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_adamw_step_scaled(ts, n, ctypes.byref(hp), grad_scale_ptr(grad_scale), ws, nb, _stream(stream)))
+
+
+def device_of(tensors, what: str) -> torch.device:
+    """The one GPU that all of `tensors` (None entries aside) live on."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+            if dev.type != "cuda":
+                raise ValueError(f"{what} must be on a GPU (got a tensor on {dev})")
+        elif t.device != dev:
+            raise ValueError(f"{what} must share one device (got {dev} and {t.device})")
+    return dev
+
+
+_CODES = {torch.float32: MU_F32, torch.bfloat16: MU_BF16}
+
+
+def gradients(grads, outs=None):
+    """(mu_grad list as packed bytes, n): a list of hundreds of tensors is
+    described in one pass, without a ctypes object each."""
+    n = len(grads)
+    if outs is not None and len(outs) != n:
+        raise ValueError("outs must have one tensor for each gradient")
+    vals = []
+    for i, g in enumerate(grads):
+        code = _CODES.get(g.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {g.dtype}")
+        if not g.is_contiguous():
+            raise ValueError("gradient must be contiguous (the library takes dense row-major buffers)")
+        if outs is None:
+            vals += (g.data_ptr(), 0, g.numel(), code, code)
+            continue
+        o = outs[i]
+        oc = _CODES.get(o.dtype)
+        if oc is None:
+            raise TypeError(f"unsupported dtype {o.dtype}")
+        if not o.is_contiguous():
+            raise ValueError("output must be contiguous (the library takes dense row-major buffers)")
+        if o.shape != g.shape:
+            raise ValueError("each output must have its gradient's shape")
+        vals += (g.data_ptr(), o.data_ptr(), g.numel(), code, oc)
+    return struct.pack("=" + "QQqii" * n, *vals), n
+
+
+def mu_grad_norm_workspace_size(gs, n) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_grad_norm_workspace_size(gs, n, ctypes.byref(out)))
+    return out.value
+
+
+def mu_grad_norm(gs, n, max_norm: float, eps: float, norm_out, scale_out, workspace, stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_grad_norm(gs, n, max_norm, eps, _ptr(norm_out), _ptr(scale_out), ws, nb, _stream(stream)))
+
+
+def mu_clip_grads(gs, n, max_norm: float, eps: float, norm_out, scale_out, workspace, stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_clip_grads(gs, n, max_norm, eps, _ptr(norm_out), _ptr(scale_out), ws, nb, _stream(stream)))
+
+
+def _token_bits(t: torch.Tensor) -> int:
+    if t.dtype == torch.int64:
+        return 64
+    if t.dtype == torch.int32:
+        return 32
+    raise TypeError(f"tokens must be int32 or int64 (got {t.dtype})")
+
+
+def lookup(tokens, weight, out, scale: float) -> MuLookup:
+    for t, what in ((tokens, "tokens"), (weight, "weight"), (out, "out")):
+        _require(t, what)
+    if weight.dim() != 2:
+        raise ValueError("weight must be 2-D")
+    if out.shape != tokens.shape + weight.shape[1:]:
+        raise ValueError("out must have the tokens' shape and the weight's row length")
+    if out.dtype != weight.dtype:
+        raise TypeError("out must share the weight's dtype")
+    return MuLookup(_ptr(tokens), _ptr(weight), _ptr(out), tokens.numel(), weight.shape[0], weight.shape[1],
+                    _token_bits(tokens), _dtype_code(weight), float(scale), 0)
+
+
+def mu_embedding(e: MuLookup, stream=None) -> None:
+    _check(LIB.mu_embedding(ctypes.byref(e), _stream(stream)))
+
+
+def rowgrad(tokens, rows, grad, scale: float, padding_idx: Optional[int], accumulate: bool) -> MuRowgrad:
+    for t, what in ((tokens, "tokens"), (rows, "rows"), (grad, "grad")):
+        _require(t, what)
+    if grad.dim() != 2:
+        raise ValueError("grad must be 2-D")
+    if rows.shape != tokens.shape + grad.shape[1:]:
+        raise ValueError("rows must have the tokens' shape and the gradient's row length")
+    if padding_idx is not None and not 0 <= padding_idx < grad.shape[0]:
+        raise ValueError("padding_idx must name a row of the gradient")
+    return MuRowgrad(_ptr(tokens), _ptr(rows), _ptr(grad), tokens.numel(), grad.shape[0], grad.shape[1],
+                     -1 if padding_idx is None else int(padding_idx), _token_bits(tokens), _dtype_code(rows),
+                     _dtype_code(grad), 1 if accumulate else 0, float(scale), 0)
+
+
+def mu_embedding_grad_workspace_size(e: MuRowgrad) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_embedding_grad_workspace_size(ctypes.byref(e), ctypes.byref(out)))
+    return out.value
+
+
+def mu_embedding_grad(e: MuRowgrad, workspace: Optional[torch.Tensor], stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_embedding_grad(ctypes.byref(e), ws, nb, _stream(stream)))
+
+
+def qk_logits(q, k, out, scale: float, causal: bool, lengths, k_lengths, cu_seqlens, cu_seqlens_k,
+              accumulate: bool) -> MuQkLogits:
+    packed = cu_seqlens is not None
+    nd = 3 if packed else 4
+    if q.dim() != nd or k.dim() != nd:
+        raise ValueError("q and k must be [batch, length, heads, dim], or [rows, heads, dim] with cu_seqlens")
+    if k.dtype != q.dtype:
+        raise TypeError("k must share q's dtype")
+    if q.shape[-1] != k.shape[-1] or (not packed and q.shape[0] != k.shape[0]):
+        raise ValueError("q and k must agree in dim and batch")
+    for t, what in ((q, "q"), (k, "k")):
+        if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {what} must be contiguous")
+    if out.dtype != torch.float32 or out.shape != (q.shape[-2],):
+        raise ValueError("out must be float32 with one element for each query head")
+    _require(out, "out")
+    if packed and (lengths is not None or k_lengths is not None):
+        raise ValueError("packed sequences (cu_seqlens) take no lengths")
+    if cu_seqlens_k is not None and not packed:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    batch = cu_seqlens.numel() - 1 if packed else q.shape[0]
+    if packed and batch < 0:
+        raise ValueError("cu_seqlens must have at least one element")
+    for t, what, size in ((lengths, "lengths", batch), (k_lengths, "k_lengths", batch),
+                          (cu_seqlens, "cu_seqlens", batch + 1), (cu_seqlens_k, "cu_seqlens_k", batch + 1)):
+        if t is None:
+            continue
+        if t.dtype != torch.int32:
+            raise TypeError(f"{what} must be int32")
+        if t.dim() != 1 or t.numel() != size:
+            raise ValueError(f"{what} must have {size} elements")
+        _require(t, what)
+    if packed:
+        qs, ks = (0,) + q.stride()[:2], (0,) + k.stride()[:2]
+        q_len, k_len = q.shape[0], k.shape[0]
+    else:
+        qs, ks = q.stride()[:3], k.stride()[:3]
+        q_len, k_len = q.shape[1], k.shape[1]
+    return MuQkLogits(_ptr(q), _ptr(k), *qs, *ks, q_len, k_len, batch, q.shape[-2], k.shape[-2], q.shape[-1],
+                      _ptr(lengths), _ptr(k_lengths), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _dtype_code(q),
+                      1 if causal else 0, 1 if accumulate else 0, float(scale), _ptr(out))
+
+
+def mu_qk_max_logits(a: MuQkLogits, stream=None) -> None:
+    _check(LIB.mu_qk_max_logits(ctypes.byref(a), _stream(stream)))
 
 
 def qk_pairs(wqs, wks, max_logits, q_heads, k_heads, gamma_outs=None):

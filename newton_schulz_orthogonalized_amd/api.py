@@ -1,4 +1,6 @@
-"""Tensor-level calls over the C ABI: one Muon step, orthogonalise-only, AdamW.
+"""Tensor-level calls over the C ABI: one Muon step, orthogonalise-only, AdamW,
+QK-Clip, and what feeds them (gradient norm and clipping, the embedding and its
+gradient, attention max logits).
 
 Each function marshals torch tensors into the library's descriptor lists,
 allocates the workspace the library asks for (unless one is passed in) and
@@ -10,6 +12,8 @@ kernels still read it. Nothing here computes.
 
 from __future__ import annotations
 
+import contextlib
+import math
 from typing import Optional, Sequence
 
 import torch
@@ -24,13 +28,15 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
               norm_outs: Optional[Sequence[torch.Tensor]] = None,
               ortho_outs: Optional[Sequence[Optional[torch.Tensor]]] = None,
               workspace: Optional[torch.Tensor] = None, stream=None, noalloc: bool = False,
-              cautious_wd: bool = False) -> None:
+              cautious_wd: bool = False, grad_scale: Optional[torch.Tensor] = None) -> None:
     """In-place Muon step over 2-D params (momentum fp32, grads in the param dtype).
 
     noalloc=True runs mu_muon_step_noalloc: no workspace is allocated, the
     library's static per-GPU scratch (MU_NOALLOC_SCRATCH_BYTES) is used, and
     calls on one GPU must not overlap in time. cautious_wd=True applies the
-    decay only where it agrees in sign with the update (see the header)."""
+    decay only where it agrees in sign with the update (see the header).
+    grad_scale (one float32 on the GPU, grad_norm's factor) multiplies every
+    gradient as it is read: a clipped step that writes no scaled gradients."""
     mats, n = _lib.matrices(params, grads, moms, heads, scales, norm_outs, ortho_outs)
     hp, keep = _lib.muon_hparams(lr, weight_decay, mu, nesterov, norm_eps, ns_steps, coeffs, precision, cautious_wd)
     if n == 0:
@@ -38,13 +44,15 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
     if noalloc:
         if workspace is not None:
             raise ValueError("noalloc=True takes no workspace")
+        if grad_scale is not None:
+            raise ValueError("noalloc=True takes no grad_scale")
         _lib.mu_muon_step_noalloc(mats, n, hp, stream)
         del keep
         return
     if workspace is None:
         workspace = _lib.workspace(_lib.mu_muon_workspace_size(mats, n, hp), params[0].device)
         _lib.tie_to_stream(workspace, stream)
-    _lib.mu_muon_step(mats, n, hp, workspace, stream)
+    _lib.mu_muon_step_scaled(mats, n, hp, grad_scale, workspace, stream)
     del keep
 
 
@@ -77,8 +85,10 @@ def orthogonalize(inputs: Sequence[torch.Tensor], *, heads: Optional[Sequence[in
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, weight_decay, beta1: float = 0.9,
                beta2: float = 0.95, eps: float = 1e-8, step: int = 1,
-               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
-    """In-place AdamW step over a flat list; lr and weight_decay may be per-tensor lists."""
+               workspace: Optional[torch.Tensor] = None, stream=None,
+               grad_scale: Optional[torch.Tensor] = None) -> None:
+    """In-place AdamW step over a flat list; lr and weight_decay may be per-tensor lists.
+    grad_scale as in muon_step."""
     n = len(params)
     lrs = list(lr) if isinstance(lr, (list, tuple)) else [lr] * n
     wds = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
@@ -88,7 +98,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, weight_decay, beta1:
     if workspace is None:
         workspace = _lib.workspace(_lib.mu_adamw_workspace_size(n), params[0].device)
         _lib.tie_to_stream(workspace, stream)
-    _lib.mu_adamw_step(ts, n, beta1, beta2, eps, step, workspace, stream)
+    _lib.mu_adamw_step_scaled(ts, n, beta1, beta2, eps, step, grad_scale, workspace, stream)
 
 
 def qk_clip(wqs, wks, max_logits, *, q_heads, k_heads, tau: float = 100.0, gamma_outs=None,
@@ -106,3 +116,156 @@ def qk_clip(wqs, wks, max_logits, *, q_heads, k_heads, tau: float = 100.0, gamma
         workspace = _lib.workspace(_lib.mu_qk_clip_workspace_size(pairs, n), wqs[0].device)
         _lib.tie_to_stream(workspace, stream)
     _lib.mu_qk_clip(pairs, n, tau, workspace, stream)
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """Make the tensors' device current and give the stream to launch on: the
+    caller's, or the current one of that device."""
+    if device.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream(device) if stream is None else stream
+    else:
+        with torch.cuda.device(device):
+            yield torch.cuda.current_stream(device) if stream is None else stream
+
+
+def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float = math.inf, eps: float = 1e-6,
+              norm_out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The global 2-norm of a list of float32 and bfloat16 tensors, as a float32
+    scalar on the GPU (no synchronisation). scale_out receives the factor
+    min(1, max_norm / (norm + eps)), which muon_step and adamw_step take as
+    grad_scale."""
+    return _norm(grads, None, max_norm, eps, norm_out, scale_out, workspace, stream)
+
+
+def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, outs: Optional[Sequence[torch.Tensor]] = None,
+               eps: float = 1e-6, norm_out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scale gradients to a global norm of at most max_norm: in place, or into
+    `outs` (of either type, e.g. float32 accumulation buffers into the bfloat16
+    gradients the steps take). Returns the norm before scaling, as grad_norm."""
+    return _norm(grads, grads if outs is None else outs, max_norm, eps, norm_out, scale_out, workspace, stream)
+
+
+def _norm(grads, outs, max_norm, eps, norm_out, scale_out, workspace, stream):
+    grads = list(grads)
+    gs, n = _lib.gradients(grads, outs)
+    for t in (norm_out, scale_out):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise TypeError("norm_out and scale_out must be one float32 element")
+    known = grads + ([] if outs is None or outs is grads else list(outs)) + [norm_out, scale_out, workspace]
+    device = _lib.device_of(known, "gradients and outputs")
+    if device is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on(device, stream) as st:
+        if norm_out is None:
+            norm_out = torch.empty((), dtype=torch.float32, device=device)
+            _lib.tie_to_stream(norm_out, st)
+        if workspace is None:
+            workspace = _lib.workspace(_lib.mu_grad_norm_workspace_size(gs, n), device)
+            _lib.tie_to_stream(workspace, st)
+        call = _lib.mu_grad_norm if outs is None else _lib.mu_clip_grads
+        call(gs, n, float(max_norm), float(eps), norm_out, scale_out, workspace, st)
+    return norm_out
+
+
+def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0, padding_idx: Optional[int] = None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """scale * weight[tokens] for int32 or int64 tokens of any shape. A token
+    outside the table reads nothing and gives a row of NaN. Differentiable in
+    weight (embedding_grad; the row padding_idx gets no gradient) unless `out`
+    is given."""
+    if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
+        raise ValueError("padding_idx must name a row of the weight")
+    if torch.is_grad_enabled() and weight.requires_grad:
+        if out is not None:
+            raise ValueError("out takes no gradient: call under torch.no_grad()")
+        return _Embedding.apply(tokens, weight, float(scale), padding_idx, stream)
+    return _lookup(tokens, weight, scale, out, stream)
+
+
+def _lookup(tokens, weight, scale, out, stream):
+    device = _lib.device_of((tokens, weight, out), "tokens, weight and out")
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty(tokens.shape + weight.shape[1:], dtype=weight.dtype, device=device)
+            _lib.tie_to_stream(out, st)
+        _lib.mu_embedding(_lib.lookup(tokens, weight, out, scale), st)
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale, padding_idx, stream):
+        ctx.save_for_backward(tokens)
+        ctx.spec = (weight.shape[0], weight.dtype, scale, padding_idx)
+        return _lookup(tokens, weight, scale, None, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, rows):
+        (tokens,) = ctx.saved_tensors
+        vocab, dtype, scale, padding_idx = ctx.spec
+        # autograd hands in expanded or transposed gradients too
+        grad = embedding_grad(tokens, rows.contiguous(), vocab, scale=scale, padding_idx=padding_idx, dtype=dtype)
+        return None, grad, None, None, None
+
+
+def embedding_grad(tokens: torch.Tensor, rows: torch.Tensor, num_embeddings: int, *, scale: float = 1.0,
+                   padding_idx: Optional[int] = None, dtype: Optional[torch.dtype] = None,
+                   out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dense gradient [num_embeddings, dim] of an embedding from its rows'
+    gradients: row v is scale times the float32 sum of rows[t] over tokens[t] ==
+    v, in a fixed order. Tokens outside the table and padding_idx add nothing.
+    `out` receives it (accumulate=True: added to it); dtype is that of a new
+    one (default: the rows')."""
+    if accumulate and out is None:
+        raise ValueError("accumulate=True needs out")
+    if out is not None and (out.dim() != 2 or out.shape[0] != num_embeddings):
+        raise ValueError("out must be [num_embeddings, dim]")
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise TypeError("dtype differs from out's")
+    device = _lib.device_of((tokens, rows, out, workspace), "tokens, rows and out")
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty(num_embeddings, rows.shape[-1], dtype=rows.dtype if dtype is None else dtype, device=device)
+            _lib.tie_to_stream(out, st)
+        e = _lib.rowgrad(tokens, rows, out, scale, padding_idx, accumulate)
+        if workspace is None:
+            workspace = _lib.workspace(_lib.mu_embedding_grad_workspace_size(e), device)
+            _lib.tie_to_stream(workspace, st)
+        _lib.mu_embedding_grad(e, workspace, st)
+    return out
+
+
+def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = None, causal: bool = True,
+                  lengths: Optional[torch.Tensor] = None, k_lengths: Optional[torch.Tensor] = None,
+                  cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """The largest |scale * q.k| of each query head over the visible pairs of a
+    batch, float32 [q_heads]: the max_logits that qk_clip takes.
+
+    q [batch, length, q_heads, dim] and k [batch, length, k_heads, dim] may be
+    strided views (of a fused projection) with a contiguous last dimension;
+    `lengths` and `k_lengths` (int32 [batch]; k_lengths defaults to lengths) cut
+    padded rows short. With cu_seqlens (int32 [sequences + 1]; cu_seqlens_k
+    defaults to it) they are packed, [rows, heads, dim]. scale defaults to
+    dim ** -0.5. causal: query i of a sequence sees keys j <= i + (keys -
+    queries). A head without a visible pair gets 0. accumulate=True keeps what
+    is larger in `out`, over the micro-batches of a step."""
+    if accumulate and out is None:
+        raise ValueError("accumulate=True needs out")
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if k_lengths is None:
+        k_lengths = lengths
+    device = _lib.device_of((q, k, lengths, k_lengths, cu_seqlens, cu_seqlens_k, out), "q, k, lengths and out")
+    with _on(device, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape[-2], dtype=torch.float32, device=device)
+            _lib.tie_to_stream(out, st)
+        _lib.mu_qk_max_logits(_lib.qk_logits(q, k, out, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k,
+                                             accumulate), st)
+    return out

@@ -16,7 +16,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon_mi355x.so")
-SOURCES = ["capi.hip", "elementwise.hip", "ns_gemm.hip"]
+SOURCES = ["capi.hip", "elementwise.hip", "ns_gemm.hip", "grads.hip", "embedding.hip", "qkmax.hip"]
 # The benchmark's ceiling probe (an MFMA loop with clock stamps), a library of
 # its own so that the optimizer library holds only the optimizer.
 PROBE_LIB = os.path.join(HERE, "libmuon_probe.so")

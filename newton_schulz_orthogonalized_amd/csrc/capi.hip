@@ -26,14 +26,17 @@
 #include <vector>
 
 #include "../../include/muon_mi355x.h"
+#include "capi_common.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 
 using namespace mu;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace mu {
 
 int fail(int code, const char* fmt, ...) {
     char buf[512];
@@ -49,19 +52,7 @@ int hip_fail(hipError_t e, const char* what) {
     return fail(MU_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-constexpr size_t ALIGN = 256;
-inline size_t align_up(size_t x, size_t a = ALIGN) { return (x + a - 1) / a * a; }
-inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-size_t dtype_size(int dt) { return dt == MU_BF16 ? 2 : 4; }
-
-// ---------------------------------------------------------------------------
-// Buffer overlap check over all device ranges of one call.
-// ---------------------------------------------------------------------------
-struct Range {
-    uintptr_t lo, hi;
-    int owner;
-};
+void clear_error() { g_err.clear(); }
 
 bool ranges_overlap(std::vector<Range>& r) {
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
@@ -69,6 +60,14 @@ bool ranges_overlap(std::vector<Range>& r) {
         if (r[i].lo < r[i - 1].hi) return true;
     return false;
 }
+
+}  // namespace mu
+
+namespace {
+
+inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+size_t dtype_size(int dt) { return dt == MU_BF16 ? 2 : 4; }
 
 // ---------------------------------------------------------------------------
 // Coefficients
@@ -456,7 +455,7 @@ void build_plan(const std::vector<Item>& items, int ns_dt, const std::vector<Coe
 }
 
 // The per-call scalars, at the head of the table (kernels read them there).
-CallScalars call_scalars(const mu_muon_hparams* hp) {
+CallScalars call_scalars(const mu_muon_hparams* hp, const float* gscale) {
     CallScalars c{};
     c.lr = hp->lr;
     c.wd = hp->weight_decay;
@@ -464,6 +463,7 @@ CallScalars call_scalars(const mu_muon_hparams* hp) {
     c.nesterov = hp->nesterov ? 1 : 0;
     c.eps = hp->norm_eps;
     c.cautious = hp->cautious_wd ? 1 : 0;
+    c.gscale = gscale;
     return c;
 }
 
@@ -746,13 +746,21 @@ hipEvent_t get_event() {
     return e;
 }
 
-template <typename F>
-int timed_launch(int kernel, double flops, double bytes, hipStream_t s, F&& fn, const char* what) {
+}  // namespace
+
+namespace mu {
+
+int timed_launch(int kernel, double flops, double bytes, hipStream_t s, const std::function<hipError_t()>& fn,
+                 const char* what) {
     hipEvent_t a = nullptr, b = nullptr;
     bool prof;
     {
         std::lock_guard<std::mutex> lk(g_prof_mu);
         prof = g_prof_on;
+        if (prof) {   // events recorded into a capture would become graph nodes
+            hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+            prof = hipStreamIsCapturing(s, &st) == hipSuccess && st == hipStreamCaptureStatusNone;
+        }
         if (prof) {
             a = get_event();
             b = get_event();
@@ -789,6 +797,10 @@ int cu_count(int* out) {
     *out = n;
     return MU_OK;
 }
+
+}  // namespace mu
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // The NS pipeline shared by mu_muon_step and mu_muon_orthogonalize.
@@ -1230,8 +1242,6 @@ int capture_call(CachedCall& c, char* ws, const mu_muon_hparams* hp, int src_dt,
     return MU_OK;
 }
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // Calls are not capturable: each call stages its descriptor table through a
 // ring of pinned host slots that later calls overwrite, so a captured graph
 // would replay a table copy from memory that no longer holds its table.
@@ -1343,9 +1353,9 @@ int check_ws(const Plan& pl, void* ws, size_t ws_bytes) {
 // The table of one call: the carved table with this call's scalars in its
 // header and each problem's scale from its list entry.
 void table_for_call(const Plan& pl, const std::vector<char>& carved, const std::vector<Item>& items,
-                    const mu_muon_hparams* hp, std::vector<char>& out) {
+                    const mu_muon_hparams* hp, const float* gscale, std::vector<char>& out) {
     out = carved;
-    const CallScalars cs = call_scalars(hp);
+    const CallScalars cs = call_scalars(hp, gscale);
     std::memcpy(out.data() + pl.off_scalars, &cs, sizeof(cs));
     for (size_t i = 0; i < pl.probs.size(); ++i) {
         NsProb* d = (NsProb*)(out.data() + pl.off_table + i * sizeof(NsProb));
@@ -1358,7 +1368,7 @@ int run_eager(Plan& pl, const std::vector<Item>& items, char* ws, const mu_muon_
               bool step_mode, hipStream_t s, NoallocDev* na_dev) {
     std::vector<char> carved, table;
     carve(pl, ws, carved);
-    table_for_call(pl, carved, items, hp, table);
+    table_for_call(pl, carved, items, hp, nullptr, table);
     int rc = na_dev ? upload_noalloc(*na_dev, table, ws, s) : upload(table.data(), table.size(), ws, s);
     if (rc) return rc;
     return launch_sequence(pl, ws, hp, src_dt, step_mode, s);
@@ -1366,7 +1376,7 @@ int run_eager(Plan& pl, const std::vector<Item>& items, char* ws, const mu_muon_
 
 // A call through the cache of repeated calls (see CachedCall).
 int run_call(const std::vector<Item>& items, const mu_muon_hparams* hp, int src_dt, bool step_mode, void* ws,
-             size_t ws_bytes, hipStream_t s) {
+             size_t ws_bytes, const float* gscale, hipStream_t s) {
     std::lock_guard<std::mutex> lk(g_call_mu);
     std::vector<unsigned char> key = call_key(items, hp, src_dt, step_mode, ws, ws_bytes);
     // A key seen before (on any device) has passed the workspace check; a new
@@ -1408,7 +1418,7 @@ int run_call(const std::vector<Item>& items, const mu_muon_hparams* hp, int src_
     int rc = check_not_capturing(s);
     if (rc) return rc;
     std::vector<char> table;
-    table_for_call(c->plan, c->table, items, hp, table);
+    table_for_call(c->plan, c->table, items, hp, gscale, table);
     rc = upload(table.data(), table.size(), ws, s);
     if (rc) return rc;
     if (graphs_enabled() && !profiling_on()) {
@@ -1465,7 +1475,13 @@ int mu_muon_workspace_size(const mu_matrix* m, int32_t n, const mu_muon_hparams*
 }
 
 int mu_muon_step(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, void* ws, size_t ws_bytes, void* stream) {
+    return mu_muon_step_scaled(m, n, hp, nullptr, ws, ws_bytes, stream);
+}
+
+int mu_muon_step_scaled(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, const float* grad_scale, void* ws,
+                        size_t ws_bytes, void* stream) {
     g_err.clear();
+    if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
     int rc = check_hparams(hp, true);
     if (rc) return rc;
     std::vector<Item> items;
@@ -1473,7 +1489,7 @@ int mu_muon_step(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, void*
     rc = validate_mats(m, n, items, dt);
     if (rc) return rc;
     if (n == 0) return MU_OK;
-    return run_call(items, hp, dt, true, ws, ws_bytes, (hipStream_t)stream);
+    return run_call(items, hp, dt, true, ws, ws_bytes, grad_scale, (hipStream_t)stream);
 }
 
 int mu_muon_step_noalloc(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, void* stream) {
@@ -1524,7 +1540,7 @@ int mu_muon_orthogonalize(const mu_ortho* xs, int32_t n, const mu_muon_hparams* 
     rc = validate_ortho(xs, n, items, dt);
     if (rc) return rc;
     if (n == 0) return MU_OK;
-    return run_call(items, hp, dt, false, ws, ws_bytes, (hipStream_t)stream);
+    return run_call(items, hp, dt, false, ws, ws_bytes, nullptr, (hipStream_t)stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -1625,7 +1641,13 @@ int mu_adamw_workspace_size(int32_t n, size_t* bytes) {
 }
 
 int mu_adamw_step(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, void* ws, size_t ws_bytes, void* stream) {
+    return mu_adamw_step_scaled(ts, n, hp, nullptr, ws, ws_bytes, stream);
+}
+
+int mu_adamw_step_scaled(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, const float* grad_scale, void* ws,
+                         size_t ws_bytes, void* stream) {
     g_err.clear();
+    if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
     if (!hp) return fail(MU_ERR_INVALID_ARG, "hparams is null");
     if (n < 0) return fail(MU_ERR_INVALID_ARG, "n must be >= 0");
     if (n > 0 && !ts) return fail(MU_ERR_INVALID_ARG, "tensor list is null");
@@ -1686,6 +1708,7 @@ int mu_adamw_step(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, vo
     a.eps = hp->eps;
     a.bc1 = (float)(1.0 - std::pow((double)hp->beta1, (double)hp->step));
     a.bc2 = (float)(1.0 - std::pow((double)hp->beta2, (double)hp->step));
+    a.gscale = grad_scale;
     double bytes = 0;
     for (int i = 0; i < n; ++i) bytes += (double)ts[i].numel * (3.0 * dtype_size(ts[i].dtype) + 16.0);
     return timed_launch(MU_K_ADAMW, 0.0, bytes, s, [&] { return launch_adamw(a, s); }, "adamw launch");
@@ -1747,6 +1770,11 @@ const char* mu_kernel_name(int k) {
         case MU_K_FUSED: return "ns_fused";
         case MU_K_RESCALE: return "rescale";
         case MU_K_TILEMAP: return "tile_map";
+        case MU_K_GRADNORM: return "grad_norm";
+        case MU_K_CLIP: return "clip_grads";
+        case MU_K_LOOKUP: return "embedding";
+        case MU_K_ROWGRAD: return "embedding_grad";
+        case MU_K_QKMAX: return "qk_max_logits";
         default: return "unknown";
     }
 }

@@ -178,6 +178,7 @@ __global__ __launch_bounds__(NTHR) void k_prep(PrepArgs A) {
     const bool with_m = A.with_momentum != 0;
     const bool nest = gp(A.cs)->nesterov != 0;
     const float mu = gp(A.cs)->mu;
+    const float* gscale = gp(A.cs)->gscale;
     float gk[4][4], mk[4][4];
     // a tile wholly inside the head block, on vector-capable buffers, loads
     // without per-lane range checks (no divergent branches between the loads)
@@ -209,6 +210,13 @@ __global__ __launch_bounds__(NTHR) void k_prep(PrepArgs A) {
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) load_gm<TS>(P, ti * TR + rr + RSTEP * k, tj * TC + cc, with_m, gk[k], mk[k]);
+    }
+    if (gscale) {   // a clipped step: the gradient times its factor, unrounded
+        const float c = *gp(gscale);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) gk[k][e] *= c;
     }
     // sum of squares in float64: squares of float32 values are exact there and
     // neither overflow nor underflow, whatever the magnitude of U
@@ -448,6 +456,11 @@ __device__ inline void adamw8(const AdamWDesc& D, int64_t i0, int cnt, const Ada
             else { pv[e] = gv[e] = mv[e] = vv[e] = 0.f; }
         }
     }
+    if (A.gscale) {
+        const float c = *gp(A.gscale);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) gv[e] *= c;
+    }
     const float lr = D.lr, decay = D.lr * D.wd;
 #pragma unroll
     for (int e = 0; e < 8; ++e) adamw1(pv[e], gv[e], mv[e], vv[e], A, lr, decay);
@@ -544,6 +557,13 @@ __device__ __forceinline__ void adamw_band_tile(const AdamWDesc& D, int64_t q, c
         }
         mq[k] = *(const MU_GLOBAL f32x4*)(D.m + i0);
         vq[k] = *(const MU_GLOBAL f32x4*)(D.v + i0);
+    }
+    if (A.gscale) {   // a clipped step: the gradient times its factor, unrounded
+        const float c = *gp(A.gscale);
+#pragma unroll
+        for (int k = 0; k < RUNS; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) gv[k][e] *= c;
     }
     const float lr = D.lr, decay = D.lr * D.wd;
 #pragma unroll

@@ -26,7 +26,7 @@ struct CallScalars {
     int32_t nesterov;
     float eps;
     int32_t cautious;   // cautious weight decay: decay only where W * (lr scale O) >= 0
-    int32_t pad[2];
+    const float* gscale;   // gradients are multiplied by *gscale as they are read (null: not)
 };
 
 struct PrepArgs {
@@ -180,6 +180,7 @@ struct AdamWArgs {
     int64_t total_chunks;
     float beta1, beta2, eps;
     float bc1, bc2;         // 1 - beta^t
+    const float* gscale;    // gradients are multiplied by *gscale as they are read (null: not)
 };
 constexpr int ADAMW_CHUNK = 8192;  // elements per workgroup
 hipError_t launch_adamw(const AdamWArgs& a, hipStream_t s);

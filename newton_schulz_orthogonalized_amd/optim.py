@@ -15,11 +15,11 @@ any torch optimizer. The library holds no state between calls.
 
 from __future__ import annotations
 
-from typing import Dict, Iterable, List, Tuple
+from typing import Dict, Iterable, List, Optional, Tuple
 
 import torch
 
-from . import _lib
+from . import _lib, api
 
 NON_HIDDEN_NAME_PARTS = ("embed", "wte", "wpe", "lm_head", "unembed", "output_head")
 
@@ -55,12 +55,25 @@ class MuonAdamW(torch.optim.Optimizer):
     AdamW group options: lr, weight_decay, betas, eps.
     Tensors with more than two dimensions are orthogonalised as
     [shape[0], prod(shape[1:])] matrices.
+
+    max_grad_norm clips the gradients of all groups together: the step uses
+    them times min(1, max_grad_norm / (norm + 1e-6)), applied as they are read
+    (p.grad keeps its values), and grad_norm holds the norm of the last step
+    before clipping, a float32 scalar on the GPU. The norm is over this
+    process's gradients.
+
+    An AdamW parameter may have a sparse gradient over its rows (that of
+    nn.Embedding(sparse=True)): its rows are summed into a dense gradient
+    (api.embedding_grad) and the step is that of the dense gradient.
     """
 
     def __init__(self, param_groups: List[Dict], *, lr: float = 0.02, weight_decay: float = 0.0,
                  momentum: float = 0.95, nesterov: bool = True, ns_steps: int = 5, coeffs=None,
                  precision: str = "bf16", norm_eps: float = 1e-7, num_heads=1, scale=1.0, cautious_wd: bool = False,
-                 adamw_lr: float = 3e-4, betas=(0.9, 0.95), eps: float = 1e-8, adamw_weight_decay: float = 0.0):
+                 adamw_lr: float = 3e-4, betas=(0.9, 0.95), eps: float = 1e-8, adamw_weight_decay: float = 0.0,
+                 max_grad_norm: Optional[float] = None):
+        if max_grad_norm is not None and not max_grad_norm >= 0:
+            raise ValueError("max_grad_norm must be >= 0")
         groups = []
         for g in param_groups:
             g = dict(g)
@@ -80,6 +93,10 @@ class MuonAdamW(torch.optim.Optimizer):
             groups.append(g)
         super().__init__(groups, {})
         self._workspaces: Dict[tuple, torch.Tensor] = {}
+        self.max_grad_norm = max_grad_norm
+        self.grad_norm: Optional[torch.Tensor] = None
+        self._grads: Dict[torch.Tensor, torch.Tensor] = {}   # during a step: each parameter's dense gradient
+        self._scale: Optional[torch.Tensor] = None           # during a step: the clip factor
 
     # float32 state of both rules (the library reads and writes it as float32)
     _F32_STATE = ("momentum_buffer", "exp_avg", "exp_avg_sq")
@@ -113,12 +130,47 @@ class MuonAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
-        for g in self.param_groups:
-            if g["kind"] == "muon":
-                self._step_muon(g)
-            else:
-                self._step_adamw(g)
+        try:
+            self._gather_grads()
+            for g in self.param_groups:
+                if g["kind"] == "muon":
+                    self._step_muon(g)
+                else:
+                    self._step_adamw(g)
+        finally:
+            self._grads, self._scale = {}, None
         return loss
+
+    def _gather_grads(self):
+        """Dense contiguous gradients of all parameters, and with max_grad_norm
+        their norm and clip factor."""
+        for g in self.param_groups:
+            for p in g["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.layout == torch.strided:
+                    self._grads[p] = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
+                elif g["kind"] == "adamw" and p.grad.layout == torch.sparse_coo and p.grad.sparse_dim() == 1 and p.dim() == 2:
+                    self._grads[p] = self._dense_rows(p)
+                else:
+                    raise ValueError("a gradient is dense, or sparse over the rows of a 2-D AdamW parameter")
+        if self.max_grad_norm is None or not self._grads:
+            return
+        grads = list(self._grads.values())
+        gs, n = _lib.gradients(grads)
+        dev = _lib.device_of(grads, "gradients")
+        self._scale = torch.empty((), dtype=torch.float32, device=dev)
+        self.grad_norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = self._ws(("norm",), _lib.mu_grad_norm_workspace_size(gs, n), dev)
+        _lib.mu_grad_norm(gs, n, float(self.max_grad_norm), 1e-6, self.grad_norm, self._scale, ws)
+
+    def _dense_rows(self, p):
+        rows = p.grad._values().contiguous()
+        key = ("rows", id(p))
+        buf = self._workspaces.get(key)
+        if buf is None or buf.shape != p.shape or buf.dtype != p.dtype or buf.device != p.device:
+            buf = self._workspaces[key] = torch.empty(p.shape, dtype=p.dtype, device=p.device)
+        return api.embedding_grad(p.grad._indices()[0].contiguous(), rows, p.shape[0], out=buf)
 
     def _step_muon(self, g):
         ps, gs, ms, heads, scales = [], [], [], [], []
@@ -131,9 +183,8 @@ class MuonAdamW(torch.optim.Optimizer):
             if "momentum_buffer" not in st:
                 st["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
             w2 = p.view(p.shape[0], -1)
-            grad = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
             ps.append(w2)
-            gs.append(grad.view(p.shape[0], -1))
+            gs.append(self._grads[p].view(p.shape[0], -1))
             ms.append(st["momentum_buffer"].view(p.shape[0], -1))
             h = g["num_heads"]
             heads.append(int(h(p) if callable(h) else h))
@@ -146,7 +197,7 @@ class MuonAdamW(torch.optim.Optimizer):
                                      g["ns_steps"], g["coeffs"], g["precision"], g.get("cautious_wd", False))
         need = _lib.mu_muon_workspace_size(mats, n, hp)
         ws = self._ws(("muon", id(g)), need, ps[0].device)
-        _lib.mu_muon_step(mats, n, hp, ws)
+        _lib.mu_muon_step_scaled(mats, n, hp, self._scale, ws)
         del keep
 
     def _step_adamw(self, g):
@@ -160,11 +211,10 @@ class MuonAdamW(torch.optim.Optimizer):
                 st["exp_avg"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
                 st["exp_avg_sq"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
             st["step"] += 1
-            grad = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
-            batches.setdefault(int(st["step"]), []).append((p, grad, st["exp_avg"], st["exp_avg_sq"]))
+            batches.setdefault(int(st["step"]), []).append((p, self._grads[p], st["exp_avg"], st["exp_avg_sq"]))
         b1, b2 = g["betas"]
         for t, items in batches.items():
             ts, n = _lib.tensors([x[0] for x in items], [x[1] for x in items], [x[2] for x in items],
                                  [x[3] for x in items], [g["lr"]] * len(items), [g["weight_decay"]] * len(items))
             ws = self._ws(("adamw", id(g), len(items)), _lib.mu_adamw_workspace_size(n), items[0][0].device)
-            _lib.mu_adamw_step(ts, n, b1, b2, g["eps"], t, ws)
+            _lib.mu_adamw_step_scaled(ts, n, b1, b2, g["eps"], t, self._scale, ws)
