@@ -389,7 +389,8 @@ typedef struct mu_qk_logits {
     float scale;
     float* max_logit;
 } mu_qk_logits;
-int mu_qk_max_logits(const mu_qk_logits* a, void* stream);
+int mu_qk_max_logits_workspace_size(const mu_qk_logits* a, size_t* bytes);
+int mu_qk_max_logits(const mu_qk_logits* a, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Workspace bytes mu_muon_step needs for this list (n == 0 gives 0). */
 int mu_muon_workspace_size(const mu_matrix* mats, int32_t n, const mu_muon_hparams* hp, size_t* bytes);

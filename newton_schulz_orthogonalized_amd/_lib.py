@@ -40,7 +40,8 @@ EXPORTED = (
     "mu_muon_orthogonalize",
     "mu_adamw_workspace_size", "mu_adamw_step", "mu_qk_clip_workspace_size", "mu_qk_clip",
     "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm", "mu_clip_grads",
-    "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad", "mu_qk_max_logits",
+    "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad", "mu_qk_max_logits_workspace_size",
+    "mu_qk_max_logits",
     "mu_status_string", "mu_last_error", "mu_version", "mu_profile_enable", "mu_profile_read", "mu_kernel_name",
 )
 
@@ -158,7 +159,8 @@ def _load() -> ctypes.CDLL:
     lib.mu_embedding.argtypes = [P(MuLookup), vp]
     lib.mu_embedding_grad_workspace_size.argtypes = [P(MuRowgrad), P(sz)]
     lib.mu_embedding_grad.argtypes = [P(MuRowgrad), vp, sz, vp]
-    lib.mu_qk_max_logits.argtypes = [P(MuQkLogits), vp]
+    lib.mu_qk_max_logits_workspace_size.argtypes = [P(MuQkLogits), P(sz)]
+    lib.mu_qk_max_logits.argtypes = [P(MuQkLogits), vp, sz, vp]
     lib.mu_status_string.argtypes = [ctypes.c_int]
     lib.mu_status_string.restype = ctypes.c_char_p
     lib.mu_last_error.argtypes = []
@@ -174,7 +176,7 @@ def _load() -> ctypes.CDLL:
                  "mu_adamw_workspace_size", "mu_adamw_step", "mu_profile_enable", "mu_profile_read",
                  "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm",
                  "mu_clip_grads", "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad",
-                 "mu_qk_max_logits"):
+                 "mu_qk_max_logits_workspace_size", "mu_qk_max_logits"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -518,8 +520,16 @@ def qk_logits(q, k, out, scale: float, causal: bool, lengths, k_lengths, cu_seql
                       1 if causal else 0, 1 if accumulate else 0, float(scale), _ptr(out))
 
 
-def mu_qk_max_logits(a: MuQkLogits, stream=None) -> None:
-    _check(LIB.mu_qk_max_logits(ctypes.byref(a), _stream(stream)))
+def mu_qk_max_logits_workspace_size(a: MuQkLogits) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_qk_max_logits_workspace_size(ctypes.byref(a), ctypes.byref(out)))
+    return out.value
+
+
+def mu_qk_max_logits(a: MuQkLogits, workspace: Optional[torch.Tensor], stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_qk_max_logits(ctypes.byref(a), ws, nb, _stream(stream)))
 
 
 def qk_pairs(wqs, wks, max_logits, q_heads, k_heads, gamma_outs=None):

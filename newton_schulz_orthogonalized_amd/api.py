@@ -243,7 +243,8 @@ def embedding_grad(tokens: torch.Tensor, rows: torch.Tensor, num_embeddings: int
 def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = None, causal: bool = True,
                   lengths: Optional[torch.Tensor] = None, k_lengths: Optional[torch.Tensor] = None,
                   cu_seqlens: Optional[torch.Tensor] = None, cu_seqlens_k: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None) -> torch.Tensor:
+                  out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The largest |scale * q.k| of each query head over the visible pairs of a
     batch, float32 [q_heads]: the max_logits that qk_clip takes.
 
@@ -261,11 +262,14 @@ def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = 
         scale = q.shape[-1] ** -0.5
     if k_lengths is None:
         k_lengths = lengths
-    device = _lib.device_of((q, k, lengths, k_lengths, cu_seqlens, cu_seqlens_k, out), "q, k, lengths and out")
+    device = _lib.device_of((q, k, lengths, k_lengths, cu_seqlens, cu_seqlens_k, out, workspace), "q, k, lengths and out")
     with _on(device, stream) as st:
         if out is None:
             out = torch.empty(q.shape[-2], dtype=torch.float32, device=device)
             _lib.tie_to_stream(out, st)
-        _lib.mu_qk_max_logits(_lib.qk_logits(q, k, out, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k,
-                                             accumulate), st)
+        a = _lib.qk_logits(q, k, out, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k, accumulate)
+        if workspace is None:
+            workspace = _lib.workspace(_lib.mu_qk_max_logits_workspace_size(a), device)
+            _lib.tie_to_stream(workspace, st)
+        _lib.mu_qk_max_logits(a, workspace, st)
     return out

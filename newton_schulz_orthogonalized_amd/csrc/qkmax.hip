@@ -23,9 +23,21 @@ namespace {
 
 constexpr int NTHR = 256;
 
-__global__ __launch_bounds__(NTHR) void k_qk_init(float* out, int n) {
-    for (int i = threadIdx.x; i < n; i += NTHR) gp(out)[i] = 0.f;
-}
+#define LDSP __attribute__((address_space(3)))
+// s_waitcnt with vmcnt(n) and lgkmcnt(0) (gfx9 encoding)
+#define MU_WAIT_VMCNT_LGKM0(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (0 << 8) | (((n) >> 4) << 14))
+constexpr int BUF_RAW32 = 0x00020000;   // word 3 of a raw buffer resource
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// A unit of work is a tile of BM queries of one head against KC keys of its
+// sequence. Units of a sequence are counted key chunk by key chunk (chunk c is
+// seen by the query tiles t >= tmin(c)), those of one key head together.
+struct QkMaxArgs {
+    mu_qk_logits p;
+    const int64_t* prefix;   // [batch + 1] units of one query head before sequence b
+    int64_t key_chunk;       // KC, a multiple of the key tile
+};
 
 struct Seq {
     int64_t q0, k0;   // element offset of its first row (without the head)
@@ -34,7 +46,7 @@ struct Seq {
 
 __device__ inline int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-__device__ inline Seq seq_of(const mu_qk_logits& A, int b) {
+__device__ inline Seq seq_of(const mu_qk_logits& A, int64_t b) {
     Seq s;
     if (A.cu_q) {
         const MU_GLOBAL int32_t* cq = (const MU_GLOBAL int32_t*)A.cu_q;
@@ -53,41 +65,333 @@ __device__ inline Seq seq_of(const mu_qk_logits& A, int b) {
     return s;
 }
 
-// One query of one sequence and head a workgroup, one key a thread at a time.
-template <typename T>
-__global__ __launch_bounds__(NTHR) void k_qkmax(mu_qk_logits A) {
-    __shared__ float qs[MU_QK_MAX_DIM];
-    __shared__ int red[4];
-    const int h = blockIdx.y, b = blockIdx.z;
-    const Seq S = seq_of(A, b);
-    const int64_t i = blockIdx.x;
-    if (i >= S.nq) return;
-    const MU_GLOBAL T* q = (const MU_GLOBAL T*)A.q + S.q0 + i * A.q_stride_s + h * A.q_stride_h;
-    const MU_GLOBAL T* k = (const MU_GLOBAL T*)A.k + S.k0 + (h / (A.q_heads / A.k_heads)) * A.k_stride_h;
-    for (int d = threadIdx.x; d < A.dim; d += NTHR) qs[d] = to_f32<T>(q[d]);
-    __syncthreads();
-    const int64_t last = A.causal ? min<int64_t>(S.nk, i + S.nk - S.nq + 1) : S.nk;
-    int best = 0;
-    for (int64_t j = threadIdx.x; j < last; j += NTHR) {
-        float s = 0.f;
-        for (int d = 0; d < A.dim; ++d) s = fmaf(qs[d], to_f32<T>(k[j * A.k_stride_s + d]), s);
-        best = max(best, __float_as_int(s) & 0x7fffffff);
+// First query tile that sees key chunk c: its last row sees key c * KC.
+__device__ inline int64_t tile_min(const Seq& S, int causal, int64_t kc, int bm, int64_t c) {
+    const int64_t x = c * kc - (S.nk - S.nq);
+    return causal && x > 0 ? x / bm : 0;
+}
+
+__device__ inline int64_t units_of(const Seq& S, int causal, int64_t kc, int bm) {
+    if (S.nq <= 0 || S.nk <= 0) return 0;
+    const int64_t tq = (S.nq + bm - 1) / bm, nc = (S.nk + kc - 1) / kc;
+    int64_t n = 0;
+    for (int64_t c = 0; c < nc; ++c) n += tq - tile_min(S, causal, kc, bm, c);
+    return n;
+}
+
+// One workgroup: the units before each sequence, and zeros to take maxima from.
+__global__ __launch_bounds__(NTHR) void k_qk_plan(QkMaxArgs A, int64_t* prefix, int bm) {
+    __shared__ int64_t wsum[4];
+    if (!A.p.accumulate)
+        for (int i = threadIdx.x; i < A.p.q_heads; i += NTHR) gp(A.p.max_logit)[i] = 0.f;
+    int64_t carry = 0;
+    for (int64_t b0 = 0; b0 < A.p.batch; b0 += NTHR) {
+        const int64_t b = b0 + threadIdx.x;
+        int64_t n = b < A.p.batch ? units_of(seq_of(A.p, b), A.p.causal, A.key_chunk, bm) : 0;
+        for (int off = 1; off < 64; off <<= 1) {
+            const int64_t up = __shfl_up(n, off, 64);
+            if ((int)(threadIdx.x & 63) >= off) n += up;
+        }
+        if ((threadIdx.x & 63) == 63) wsum[threadIdx.x >> 6] = n;
+        __syncthreads();
+        int64_t before = carry;
+        for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) before += wsum[w];
+        if (b < A.p.batch) gp(prefix)[b + 1] = before + n;
+        carry += wsum[0] + wsum[1] + wsum[2] + wsum[3];
+        __syncthreads();
     }
-    for (int off = 32; off >= 1; off >>= 1) best = max(best, __shfl_xor(best, off, 64));
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = best;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        best = max(max(red[0], red[1]), max(red[2], red[3]));
-        atomicMax((int*)A.max_logit + h, __float_as_int(fabsf(A.scale) * __int_as_float(best)) & 0x7fffffff);
+    if (threadIdx.x == 0) gp(prefix)[0] = 0;
+}
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// 16-byte pieces ("chunks") of a row: EPC elements each. A pair of chunks, one
+// for each half of the wave, feeds one bf16 or four float32 matrix
+// instructions: lane l of a 32 x 32 operand holds row l % 32 and half l / 32 of
+// the instruction's k, and which k an instruction multiplies is free as long as
+// both operands agree.
+template <typename T> struct Frag;
+template <> struct Frag<bf16> {
+    typedef bf16x8 V;
+    static constexpr int EPC = 8;
+    static __device__ __forceinline__ f32x16 mma(V a, V b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Frag<float> {
+    typedef f32x4 V;
+    static constexpr int EPC = 4;
+    static __device__ __forceinline__ f32x16 mma(V a, V b, f32x16 c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+        return c;
+    }
+};
+
+// Chunk c of a row of dim elements, zeros from element dim on. VEC: rows are
+// whole 16-byte chunks; otherwise element by element at any alignment.
+template <typename T, bool VEC>
+__device__ __forceinline__ typename Frag<T>::V load_chunk(const MU_GLOBAL T* row, int c, int dim) {
+    typename Frag<T>::V v;
+    constexpr int EPC = Frag<T>::EPC;
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) v[e] = (T)0.f;
+    if constexpr (VEC) {
+        if (c * EPC < dim) v = *(const MU_GLOBAL typename Frag<T>::V*)(row + c * EPC);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EPC; ++e)
+            if (c * EPC + e < dim) v[e] = row[c * EPC + e];
+    }
+    return v;
+}
+
+// max(|a|, |b|, m) that keeps NaN
+__device__ __forceinline__ float absmax3(float a, float b, float m) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b)), m);
+}
+
+// Logits of a query tile against a stream of key tiles. Four waves of MT * 32
+// queries each keep their queries in registers (the left operand of every
+// product); the keys pass through a ring of NS LDS slots of BN rows, read as
+// right operands by all four. Nothing but a running maximum leaves the matrix
+// instructions, one max3 for two logits.
+//
+// A slot holds BN rows of NC chunks; chunk c of row r lies at position
+// c ^ ((r >> SH) & (GR - 1)) of its row, which spreads the 16 lanes that read
+// one chunk column of 16 rows over all 16 positions of 256 bytes: no bank
+// conflicts at any NC. DIRECT: rows go from memory straight into the slot (the
+// lane's address carries the permutation; chunks beyond dim are zeroed once and
+// never written). Otherwise (rows that are not 16-byte aligned, ragged dim)
+// they pass through registers.
+//
+// Rows past the end of a sequence read its last row again, which cannot change
+// a maximum; only tiles that the causal border crosses test each pair.
+template <typename T, int DP, int BN, int MT, int NS, bool DIRECT>
+__global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
+    typedef typename Frag<T>::V V;
+    constexpr int EPC = Frag<T>::EPC, NC = DP / EPC, NK = NC / 2, ROWB = NC * 16, BM = 4 * MT * 32;
+    constexpr int GR = NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : NC % 4 == 0 ? 4 : 2;
+    constexpr int SH = GR == 16 ? 0 : GR == 8 ? 1 : GR == 4 ? 2 : 3;
+    constexpr int SLOTS = BN * NC;                     // chunks of a tile
+    constexpr int NL = (SLOTS / 64 + 3) / 4;           // direct loads of a wave and tile
+    static_assert(SLOTS % 64 == 0, "whole loads");
+    constexpr int TB = BN * ROWB;
+    __shared__ __align__(256) char s0[TB], s1[TB], s2[NS > 2 ? TB : 16];
+    __shared__ int red[4];
+    const mu_qk_logits& P = A.p;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), l32 = lane & 31, half = lane >> 5;
+    const int G = P.q_heads / P.k_heads;
+
+    // chunk positions of this lane's reads: RA of them, then a multiple of GR * 16 bytes further
+    constexpr int RA = GR / 2 < NK ? GR / 2 : NK;
+    int rd[RA];
+    const int sw = (l32 >> SH) & (GR - 1);
+#pragma unroll
+    for (int k = 0; k < RA; ++k) rd[k] = l32 * ROWB + (((2 * k + half) ^ sw) * 16);
+    // this lane's part of each load: row and chunk
+    int lrow[NL], lchk[NL], lpos[NL];
+#pragma unroll
+    for (int j = 0; j < NL; ++j) {
+        lpos[j] = uni(min(wave + 4 * j, SLOTS / 64 - 1));   // a last odd load is done twice
+        const int q = lpos[j] * 64 + lane;
+        lrow[j] = q / NC;
+        lchk[j] = (q % NC) ^ ((lrow[j] >> SH) & (GR - 1));
+    }
+    if (DIRECT && P.dim < DP) {
+        for (int i = tid; i < TB / 16; i += NTHR) {
+            ((LDSP f32x4*)(LDSP char*)s0)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            ((LDSP f32x4*)(LDSP char*)s1)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (NS > 2) ((LDSP f32x4*)(LDSP char*)s2)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        __syncthreads();
+    }
+
+    const int64_t per_head = gp(A.prefix)[P.batch], total = per_head * P.q_heads;
+    // XCD x works on units [x * total / 8, (x + 1) * total / 8)
+    const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
+    const int64_t u_end = total * (xcd + 1) / 8;
+    for (int64_t u = total * xcd / 8 + (blockIdx.x >> 3); u < u_end; u += stride) {
+        // unit -> sequence, key head, key chunk, query tile, query head
+        int64_t lo = 0, hi = P.batch - 1;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi + 1) >> 1;
+            if (gp(A.prefix)[mid] * P.q_heads <= u) lo = mid; else hi = mid - 1;
+        }
+        const Seq S = seq_of(P, lo);
+        int64_t r = u - gp(A.prefix)[lo] * P.q_heads;
+        const int64_t n_u = gp(A.prefix)[lo + 1] - gp(A.prefix)[lo];
+        const int hk = (int)(r / (n_u * G));
+        r -= hk * n_u * G;
+        const int g = (int)(r % G);
+        r /= G;
+        const int64_t tq = (S.nq + BM - 1) / BM;
+        int64_t c = 0, t0 = 0;
+        for (;;) {
+            t0 = tile_min(S, P.causal, A.key_chunk, BM, c);
+            if (r < tq - t0) break;
+            r -= tq - t0;
+            ++c;
+        }
+        const int64_t t = t0 + r;
+        const int h = hk * G + g;
+        const int64_t off = S.nk - S.nq;
+        const int64_t row_last = min<int64_t>((t + 1) * BM, S.nq) - 1;
+        const int64_t k_lo = c * A.key_chunk;
+        const int64_t k_hi = min<int64_t>(k_lo + A.key_chunk, P.causal ? min<int64_t>(S.nk, row_last + 1 + off) : S.nk);
+        const int nkeys = (int)(k_hi - k_lo);   // >= 1
+        const MU_GLOBAL T* kbase = (const MU_GLOBAL T*)P.k + S.k0 + hk * P.k_stride_h + k_lo * P.k_stride_s;
+        const int ntiles = (nkeys + BN - 1) / BN;
+
+        auto stage = [&](char* slot, int kt) {
+            const int rem = nkeys - kt * BN;   // rows left from this tile on
+            const MU_GLOBAL T* base = kbase + (int64_t)kt * BN * P.k_stride_s;
+            if constexpr (DIRECT) {
+                const int sb = (int)P.k_stride_s * (int)sizeof(T);
+                const __amdgpu_buffer_rsrc_t rs =
+                    __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (BN - 1) * sb + P.dim * (int)sizeof(T), BUF_RAW32);
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const int vo = min(lrow[j], rem - 1) * sb + lchk[j] * 16;
+                    if (lchk[j] * EPC < P.dim)
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDSP void*)(slot + lpos[j] * 1024), 16, vo, 0, 0, 0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < NL; ++j) {
+                    const MU_GLOBAL T* row = base + (int64_t)min(lrow[j], rem - 1) * P.k_stride_s;
+                    *(LDSP V*)((LDSP char*)slot + lpos[j] * 1024 + lane * 16) = load_chunk<T, false>(row, lchk[j], P.dim);
+                }
+            }
+        };
+
+        // this wave's queries
+        const int64_t w_row = t * BM + wave * (MT * 32);
+        const bool live = w_row < S.nq;
+        const int64_t w_last = min<int64_t>(w_row + MT * 32, S.nq) - 1;
+        // keys of this chunk that the wave's last row sees, and that its first row sees
+        const int see_last = !live ? 0 : P.causal ? (int)clamp64(w_last + 1 + off - k_lo, 0, nkeys) : nkeys;
+        const int see_all = !live ? 0 : P.causal ? (int)clamp64(w_row + 1 + off - k_lo, 0, nkeys) : nkeys;
+        stage(s0, 0);
+        if constexpr (NS > 2) {
+            if (ntiles > 1) stage(s1, 1);
+        }
+        V qf[MT][NK];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int64_t i = min<int64_t>(w_row + m * 32 + l32, S.nq - 1);
+            const MU_GLOBAL T* row = (const MU_GLOBAL T*)P.q + S.q0 + i * P.q_stride_s + h * P.q_stride_h;
+#pragma unroll
+            for (int k = 0; k < NK; ++k) qf[m][k] = load_chunk<T, DIRECT>(row, 2 * k + half, P.dim);
+        }
+
+        float best = 0.f;
+        auto compute = [&](const char* slot, int kt) {
+            if (kt * BN >= see_last) return;
+            const bool border = min((kt + 1) * BN, nkeys) > see_all;
+#pragma unroll
+            for (int n = 0; n < BN / 32; ++n) {
+                f32x16 acc[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[m][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    const V kf = *(const LDSP V*)((const LDSP char*)slot + rd[k % RA] + n * 32 * ROWB + k / RA * (RA * 32));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) acc[m] = Frag<T>::mma(qf[m][k], kf, acc[m]);
+                }
+                if (border) {
+                    const int64_t j = min<int64_t>(kt * BN + n * 32 + l32, nkeys - 1) + k_lo;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int64_t i = min<int64_t>(w_row + m * 32 + 8 * (e / 4) + 4 * half + e % 4, S.nq - 1);
+                            acc[m][e] = j <= i + off ? acc[m][e] : 0.f;
+                        }
+                }
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) best = absmax3(acc[m][e], acc[m][e + 1], best);
+            }
+        };
+        // Tile kt in slot kt % NS. The wait leaves the loads of the tiles
+        // behind it in flight; past the barrier every wave has finished tile
+        // kt - 1, whose slot the next loads take.
+        auto step = [&](char* cur, char* nxt, int kt) {
+            if (NS > 2 && kt + 1 < ntiles && DIRECT && P.dim == DP) MU_WAIT_VMCNT_LGKM0(NL);
+            else MU_WAIT_VMCNT_LGKM0(0);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (kt + NS - 1 < ntiles) stage(nxt, kt + NS - 1);
+            compute(cur, kt);
+        };
+        for (int kt = 0; kt < ntiles; kt += NS) {
+            if constexpr (NS > 2) {
+                step(s0, s2, kt);
+                if (kt + 1 < ntiles) step(s1, s0, kt + 1);
+                if (kt + 2 < ntiles) step(s2, s1, kt + 2);
+            } else {
+                step(s0, s1, kt);
+                if (kt + 1 < ntiles) step(s1, s0, kt + 1);
+            }
+        }
+        int bits = __float_as_int(best) & 0x7fffffff;
+        for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
+        if (lane == 0) red[wave] = bits;
+        __syncthreads();   // also: every wave is done with the slots
+        if (tid == 0) {
+            bits = max(max(red[0], red[1]), max(red[2], red[3]));
+            if (bits) atomicMax((int*)P.max_logit + h, __float_as_int(__builtin_fabsf(P.scale) * __int_as_float(bits)) & 0x7fffffff);
+        }
+    }
+}
+
+template <typename T, int DP, int BN, int MT, int NS>
+hipError_t launch(const QkMaxArgs& a, bool direct, int grid, hipStream_t s) {
+    if (direct) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, NS, true>), dim3(grid), dim3(NTHR), 0, s, a);
+    else hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, NS, false>), dim3(grid), dim3(NTHR), 0, s, a);
+    return hipGetLastError();
+}
+
+// Instances by padded head width.
+struct Shape {
+    int dp, bn, bm;
+};
+Shape shape_of(int dtype, int dim) {
+    const int dp = dim <= 32 ? 32 : dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256;
+    if (dtype == MU_BF16) return {dp, dp <= 128 ? 64 : 32, 256};
+    return {dp, 32, dp <= 128 ? 256 : 128};
+}
+hipError_t launch_shape(const QkMaxArgs& a, int dp, bool direct, int grid, hipStream_t s) {
+    if (a.p.dtype == MU_BF16) switch (dp) {
+        case 32: return launch<bf16, 32, 64, 2, 3>(a, direct, grid, s);
+        case 64: return launch<bf16, 64, 64, 2, 3>(a, direct, grid, s);
+        case 96: return launch<bf16, 96, 64, 2, 3>(a, direct, grid, s);
+        case 128: return launch<bf16, 128, 64, 2, 3>(a, direct, grid, s);
+        case 192: return launch<bf16, 192, 32, 2, 3>(a, direct, grid, s);
+        default: return launch<bf16, 256, 32, 2, 3>(a, direct, grid, s);
+    }
+    switch (dp) {
+        case 32: return launch<float, 32, 32, 2, 3>(a, direct, grid, s);
+        case 64: return launch<float, 64, 32, 2, 3>(a, direct, grid, s);
+        case 96: return launch<float, 96, 32, 2, 3>(a, direct, grid, s);
+        case 128: return launch<float, 128, 32, 2, 3>(a, direct, grid, s);
+        case 192: return launch<float, 192, 32, 1, 3>(a, direct, grid, s);
+        default: return launch<float, 256, 32, 1, 3>(a, direct, grid, s);
     }
 }
 
 int check(const mu_qk_logits* a) {
     if (!a) return fail(MU_ERR_INVALID_ARG, "argument is null");
     if (a->dtype != MU_F32 && a->dtype != MU_BF16) return fail(MU_ERR_DTYPE, "unknown dtype %d", a->dtype);
-    if (a->batch < 0 || a->batch > 65535 || a->q_len < 0 || a->k_len < 0 || a->q_len > 0x7fffff00LL || a->k_len > 0x7fffff00LL)
+    if (a->batch < 0 || a->batch > (1 << 24) || a->q_len < 0 || a->k_len < 0 || a->q_len > 0x7fffff00LL || a->k_len > 0x7fffff00LL)
         return fail(MU_ERR_INVALID_ARG, "bad batch or length");
-    if (a->q_heads < 1 || a->q_heads > 65535 || a->k_heads < 1 || a->q_heads % a->k_heads != 0)
+    if (a->q_heads < 1 || a->q_heads > (1 << 20) || a->k_heads < 1 || a->q_heads % a->k_heads != 0)
         return fail(MU_ERR_INVALID_ARG, "head counts must be >= 1 and k_heads divide q_heads");
     if (a->dim < 1 || a->dim > MU_QK_MAX_DIM) return fail(MU_ERR_INVALID_ARG, "dim must be in [1, %d]", MU_QK_MAX_DIM);
     if ((a->causal != 0 && a->causal != 1) || (a->accumulate != 0 && a->accumulate != 1))
@@ -108,32 +412,60 @@ int check(const mu_qk_logits* a) {
     return MU_OK;
 }
 
+size_t qk_workspace(const mu_qk_logits* a) { return align_up(sizeof(int64_t) * ((size_t)a->batch + 1)); }
+
 }  // namespace
 
 extern "C" {
 
-int mu_qk_max_logits(const mu_qk_logits* a, void* stream) {
+int mu_qk_max_logits_workspace_size(const mu_qk_logits* a, size_t* bytes) {
+    return guarded([&]() -> int {
+        if (!bytes) return fail(MU_ERR_INVALID_ARG, "bytes is null");
+        int rc = check(a);
+        if (rc) return rc;
+        *bytes = qk_workspace(a);
+        return MU_OK;
+    });
+}
+
+int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* stream) {
     return guarded([&]() -> int {
         int rc = check(a);
         if (rc) return rc;
+        const bool empty = a->batch == 0 || a->q_len == 0 || a->k_len == 0;
+        if (empty && a->accumulate) return MU_OK;
+        const size_t need = qk_workspace(a);
+        if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
+        if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
         hipStream_t s = (hipStream_t)stream;
-        if (!a->accumulate) {
-            rc = timed_launch(MU_K_QKMAX, 0.0, 4.0 * a->q_heads, s, [&] {
-                hipLaunchKernelGGL(k_qk_init, dim3(1), dim3(NTHR), 0, s, a->max_logit, a->q_heads);
-                return hipGetLastError();
-            }, "max logits init");
-            if (rc) return rc;
-        }
-        if (a->batch == 0 || a->q_len == 0 || a->k_len == 0) return MU_OK;
-        const double es = a->dtype == MU_BF16 ? 2 : 4, nb = a->cu_q ? 1 : a->batch;
+        const Shape sh = shape_of(a->dtype, a->dim);
+        const int es = a->dtype == MU_BF16 ? 2 : 4;
+        // rows as whole 16-byte chunks, a tile of them within 32-bit offsets
+        const int64_t mix = a->q_stride_b | a->q_stride_s | a->q_stride_h | a->k_stride_b | a->k_stride_s | a->k_stride_h | a->dim;
+        const bool direct = (mix * es) % 16 == 0 && aligned(a->q, 16) && aligned(a->k, 16) &&
+                            a->k_stride_s * es < ((int64_t)1 << 30) / sh.bn;
+        int cus = 0;
+        rc = cu_count(&cus);
+        if (rc) return rc;
+        // Key chunk: a few units for each workgroup slot, between 256 and 4096 keys.
+        const int64_t seqs = std::max<int64_t>(1, a->batch), slots = 2 * (int64_t)cus;
+        const int64_t tiles = (a->cu_q ? a->q_len / sh.bm + seqs : seqs * ((a->q_len + sh.bm - 1) / sh.bm)) * a->q_heads;
+        const int64_t keys = a->cu_q ? (a->k_len + seqs - 1) / seqs : a->k_len;
+        QkMaxArgs q{*a, (const int64_t*)ws, 4096};
+        while (q.key_chunk > 256 && tiles * ((keys + q.key_chunk - 1) / q.key_chunk) < 8 * slots) q.key_chunk /= 2;
+        rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, s, [&] {
+            hipLaunchKernelGGL(k_qk_plan, dim3(1), dim3(NTHR), 0, s, q, (int64_t*)ws, sh.bm);
+            return hipGetLastError();
+        }, "max logits plan");
+        if (rc || empty) return rc;
+        const double nb = a->cu_q ? 1 : a->batch;
         const double bytes = nb * a->dim * es * ((double)a->q_len * a->q_heads + (double)a->k_len * a->k_heads);
         const double flops = 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
-        return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] {
-            const dim3 grid((unsigned)a->q_len, (unsigned)a->q_heads, (unsigned)a->batch);
-            if (a->dtype == MU_BF16) hipLaunchKernelGGL(k_qkmax<bf16>, grid, dim3(NTHR), 0, s, *a);
-            else hipLaunchKernelGGL(k_qkmax<float>, grid, dim3(NTHR), 0, s, *a);
-            return hipGetLastError();
-        }, "max logits launch");
+        const double most = (double)tiles * (double)((a->k_len + q.key_chunk - 1) / q.key_chunk);
+        const int grid = (int)std::min<double>((double)slots, 8.0 * std::ceil(most / 8.0));
+        return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch_shape(q, sh.dp, direct, grid, s); },
+                            "max logits launch");
     });
 }
 

@@ -112,11 +112,11 @@ def test_empty_accumulation_is_nothing(lib):
     assert _rowgrad(lib, n_tokens=0, tokens=None, rows=None, accumulate=1) == lib.MU_OK
 
 
-def _qk(lib, **kw):
+def _qk(lib, ws=A + (3 << 30), nb=1 << 20, **kw):
     d = dict(q=A, k=A + (1 << 30), q_stride_b=4096, q_stride_s=256, q_stride_h=64, k_stride_b=4096, k_stride_s=256,
              k_stride_h=64, q_len=16, k_len=16, batch=2, q_heads=4, k_heads=2, dim=64, q_lengths=None, k_lengths=None,
              cu_q=None, cu_k=None, dtype=lib.MU_BF16, causal=1, accumulate=0, scale=0.125, max_logit=A + (2 << 30))
-    return lib.LIB.mu_qk_max_logits(ctypes.byref(lib.MuQkLogits(**{**d, **kw})), None)
+    return lib.LIB.mu_qk_max_logits(ctypes.byref(lib.MuQkLogits(**{**d, **kw})), ws, nb, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -128,6 +128,11 @@ def _qk(lib, **kw):
 ])
 def test_bad_qk_rejected(lib, kw, code):
     assert _qk(lib, **kw) == code
+
+
+def test_qk_workspace_rejected(lib):
+    for kw in (dict(ws=None), dict(ws=A + 8), dict(nb=16)):
+        assert _qk(lib, **kw) == lib.MU_ERR_WORKSPACE, kw
 
 
 def test_empty_accumulating_qk_is_nothing(lib):
