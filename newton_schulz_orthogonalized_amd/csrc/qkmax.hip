@@ -30,21 +30,15 @@ constexpr int BUF_RAW32 = 0x00020000;   // word 3 of a raw buffer resource
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// A unit of work is a tile of BM queries of one head against at most KC keys of
-// its sequence. The units of one query head are the same for every head: the
-// plan kernel writes them as records, sequence by sequence, key chunk by key
-// chunk (chunk c is seen by the query tiles t >= tmin(c)).
-struct Unit {
-    int64_t q_off, k_off;   // elements before its first query and key row (without the head)
-    int32_t rows, keys;     // of this unit, both >= 1
-    int32_t see;            // row i sees the unit's keys j < see + i (all of them where not causal)
-    int32_t pad;
-};
+// The work is key tiles: query tile t (BM rows) of a sequence and head passes
+// over the tiles of BN keys that its last row sees. All of them are laid out on
+// one line (head slowest, then sequence, query tile, key tile), each query tile
+// with COST more places in front for what it costs to begin and to end at the
+// border, and every workgroup takes an equal run of the line, wherever that
+// starts and ends.
 struct QkMaxArgs {
     mu_qk_logits p;
-    const int64_t* count;    // units of one head
-    const Unit* units;
-    int64_t key_chunk;       // KC, a multiple of the key tile
+    const int64_t* prefix;   // [batch + 1] places of one head before each sequence
 };
 
 struct Seq {
@@ -73,88 +67,58 @@ __device__ inline Seq seq_of(const mu_qk_logits& A, int64_t b) {
     return s;
 }
 
-// First query tile that sees key chunk c: its last row sees key c * KC.
-__device__ inline int64_t tile_min(const Seq& S, int causal, int64_t kc, int bm, int64_t c) {
-    const int64_t x = c * kc - (S.nk - S.nq);
-    return causal && x > 0 ? x / bm : 0;
-}
-
-__device__ inline int64_t units_of(const Seq& S, int causal, int64_t kc, int bm) {
-    if (S.nq <= 0 || S.nk <= 0) return 0;
-    const int64_t tq = (S.nq + bm - 1) / bm, nc = (S.nk + kc - 1) / kc;
-    int64_t n = 0;
-    for (int64_t c = 0; c < nc; ++c) n += tq - tile_min(S, causal, kc, bm, c);
-    return n;
-}
-
-// The units of chunk c of a sequence that follow record `at`, every `step`-th from `first` on.
-__device__ inline void put_units(const Seq& S, const QkMaxArgs& A, int bm, int64_t c, Unit* at, int first, int step) {
-    const int64_t kc = A.key_chunk, tq = (S.nq + bm - 1) / bm, t0 = tile_min(S, A.p.causal, kc, bm, c);
-    const int64_t off = S.nk - S.nq, k_lo = c * kc;
-    for (int64_t t = t0 + first; t < tq; t += step) {
-        Unit u;
-        u.q_off = S.q0 + t * bm * A.p.q_stride_s;
-        u.k_off = S.k0 + k_lo * A.p.k_stride_s;
-        u.rows = (int32_t)min<int64_t>(bm, S.nq - t * bm);
-        const int64_t k_hi = A.p.causal ? min<int64_t>(S.nk, t * bm + u.rows + off) : S.nk;
-        u.keys = (int32_t)min<int64_t>(kc, k_hi - k_lo);
-        // beyond the keys on one side and below the first row's reach on the other any value does
-        u.see = A.p.causal ? (int32_t)clamp64(t * bm + 1 + off - k_lo, -bm, u.keys) : u.keys;
-        u.pad = 0;
-        at[t - t0] = u;
+// Key tiles of a sequence and head. Query tile t < last sees (t + 1) BM + nk - nq
+// keys (causal), so (t + 1) BM / BN + o tiles with o = ceil((nk - nq) / BN) from
+// the first t that sees any; the last one sees all keys.
+constexpr int COST = 6;
+template <int BM, int BN>
+struct Tiles {
+    int64_t t0, last, all;   // first and last query tile with keys, tiles of all keys
+    int64_t o;
+    bool causal;
+    __device__ Tiles(const Seq& S, bool c) : causal(c) {
+        last = (S.nq + BM - 1) / BM - 1;
+        all = (S.nk + BN - 1) / BN;
+        const int64_t off = S.nk - S.nq;
+        o = off >= 0 ? (off + BN - 1) / BN : -(-off / BN);
+        t0 = causal && off < 0 ? (BM - off) / BM - 1 : 0;   // ceil((1 - off) / BM) - 1
+        if (S.nq <= 0 || S.nk <= 0) t0 = 0, last = -1;
     }
-}
+    __device__ int64_t of(int64_t t) const { return causal && t < last ? (t + 1) * (BM / BN) + o : all; }
+    // places of the query tiles before t, t0 <= t <= last
+    __device__ int64_t before(int64_t t) const {
+        return (t - t0) * COST + (causal ? (t - t0) * o + (BM / BN) * (t * (t + 1) / 2 - t0 * (t0 + 1) / 2) : t * all);
+    }
+    __device__ int64_t total() const { return last < 0 ? 0 : before(last) + COST + all; }
+};
 
-// One workgroup: the units of every sequence, and zeros to take maxima from.
-// Sequences of few units are written by a thread each, others by a wave.
-constexpr int PLAN_THR = 1024, PLAN_FEW = 4;
-__global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* count, Unit* units, int bm) {
-    __shared__ int64_t wsum[PLAN_THR / 64], base[PLAN_THR];
-    __shared__ int many;
-    const int tid = threadIdx.x, wave = tid >> 6;
+// One workgroup: the places before each sequence, and zeros to take maxima from.
+constexpr int PLAN_THR = 1024;
+template <int BM, int BN>
+__global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* prefix) {
+    __shared__ int64_t wsum[PLAN_THR / 64];
+    const int tid = threadIdx.x;
     if (!A.p.accumulate)
         for (int i = tid; i < A.p.q_heads; i += PLAN_THR) gp(A.p.max_logit)[i] = 0.f;
     int64_t carry = 0;
     for (int64_t b0 = 0; b0 < A.p.batch; b0 += PLAN_THR) {
         const int64_t b = b0 + tid;
-        Seq S{0, 0, 0, 0};
-        if (b < A.p.batch) S = seq_of(A.p, b);
-        const int64_t mine = units_of(S, A.p.causal, A.key_chunk, bm);
-        if (tid == 0) many = 0;
-        int64_t n = mine;
+        int64_t n = b < A.p.batch ? Tiles<BM, BN>(seq_of(A.p, b), A.p.causal != 0).total() : 0;
         for (int off = 1; off < 64; off <<= 1) {
             const int64_t up = __shfl_up(n, off, 64);
             if ((tid & 63) >= off) n += up;
         }
-        if ((tid & 63) == 63) wsum[wave] = n;
+        if ((tid & 63) == 63) wsum[tid >> 6] = n;
         __syncthreads();
-        int64_t before = carry + n - mine;
+        int64_t before = carry;
         for (int w = 0; w < PLAN_THR / 64; ++w) {
-            if (w < wave) before += wsum[w];
+            if (w < (tid >> 6)) before += wsum[w];
             carry += wsum[w];
         }
-        base[tid] = mine > PLAN_FEW ? before : -1;
-        if (mine > PLAN_FEW) many = 1;
-        else
-            for (int64_t c = 0, at = before; at < before + mine; ++c) {
-                put_units(S, A, bm, c, units + at, 0, 1);
-                at += (S.nq + bm - 1) / bm - tile_min(S, A.p.causal, A.key_chunk, bm, c);
-            }
-        __syncthreads();
-        if (many)
-            for (int i = wave; i < PLAN_THR && b0 + i < A.p.batch; i += PLAN_THR / 64) {
-                int64_t at = base[i];
-                if (at < 0) continue;
-                const Seq T = seq_of(A.p, b0 + i);
-                const int64_t tq = (T.nq + bm - 1) / bm, nc = (T.nk + A.key_chunk - 1) / A.key_chunk;
-                for (int64_t c = 0; c < nc; ++c) {
-                    put_units(T, A, bm, c, units + at, tid & 63, 64);
-                    at += tq - tile_min(T, A.p.causal, A.key_chunk, bm, c);
-                }
-            }
+        if (b < A.p.batch) gp(prefix)[b + 1] = before + n;
         __syncthreads();
     }
-    if (tid == 0) *gp(count) = carry;
+    if (tid == 0) gp(prefix)[0] = 0;
 }
 
 __device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -214,7 +178,7 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 
 // Logits of a query tile against a stream of key tiles. Four waves of MT * 32
 // queries each keep their queries in registers (the left operand of every
-// product); the keys pass through a ring of NS LDS slots of BN rows, read as
+// product); the keys pass through a ring of three LDS slots of BN rows, read as
 // right operands by all four. Nothing but a running maximum leaves the matrix
 // instructions, one max3 for two logits.
 //
@@ -227,8 +191,8 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 //
 // Rows past the end of a sequence read its last row again, which cannot change
 // a maximum; only tiles that the causal border crosses test each pair.
-template <typename T, int DP, int BN, int MT, int NS, int ROWS>
-__global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
+template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
+__global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     typedef typename Frag<T>::V V;
     constexpr bool DIRECT = ROWS != RAGGED;
     constexpr int EPC = Frag<T>::EPC, NC = DP / EPC, NK = NC / 2, ROWB = NC * 16, BM = 4 * MT * 32;
@@ -237,12 +201,18 @@ __global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
     constexpr int SLOTS = BN * NC;                     // chunks of a tile
     constexpr int NL = (SLOTS / 64 + 3) / 4;           // direct loads of a wave and tile
     static_assert(SLOTS % 64 == 0, "whole loads");
-    constexpr int TB = BN * ROWB;
+    constexpr int TB = BN * ROWB, NB = BN / 32;
+    constexpr int PD = NK <= 8 ? NK : NK % 8 == 0 ? 8 : 6;
+    static_assert(NK % PD == 0, "a column block is whole rounds of the operand ring");
     __shared__ __align__(256) char s0[TB], s1[TB], s2[TB];
-    static_assert(NS == 3, "three slots");
     __shared__ int red[4];
     const mu_qk_logits& P = A.p;
-    const int tid = threadIdx.x, lane = tid & 63, wave = uni(tid >> 6), l32 = lane & 31, half = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
+    int wave = uni(tid >> 6);
+    // its range is hidden: where the compiler can tell a read of the upper rows
+    // of a slot from the slot's first direct load, it no longer connects it to
+    // the slot's others and waits for every load in flight
+    asm("" : "+s"(wave));
     const int G = P.q_heads / P.k_heads;
 
     // chunk positions of this lane's reads: RA of them, then a multiple of GR * 16 bytes further
@@ -255,7 +225,7 @@ __global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
     int lrow[NL], lchk[NL], lpos[NL];
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
-        lpos[j] = uni(min(wave + 4 * j, SLOTS / 64 - 1));   // a last odd load is done twice
+        lpos[j] = SLOTS % 256 == 0 ? wave + 4 * j : uni(min(wave + 4 * j, SLOTS / 64 - 1));   // a last odd load is done twice
         const int q = lpos[j] * 64 + lane;
         lrow[j] = q / NC;
         lchk[j] = (q % NC) ^ ((lrow[j] >> SH) & (GR - 1));
@@ -269,24 +239,54 @@ __global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
         __syncthreads();
     }
 
-    const int64_t per_head = *gp(A.count), total = per_head * P.q_heads;
-    // XCD x works on units [x * total / 8, (x + 1) * total / 8) of the order
-    // key head, record, query head: what runs together there shares its keys
-    const int xcd = blockIdx.x & 7, stride = gridDim.x >> 3;
-    const int64_t u_end = total * (xcd + 1) / 8;
-    int64_t u = total * xcd / 8 + (blockIdx.x >> 3);
-    auto record = [&](int64_t x) { return (x < u_end ? x : u_end - 1) % (per_head * G) / G; };
+    const int64_t per_head = uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
+    // XCD x takes places [x * total / 8, (x + 1) * total / 8), so few key heads
+    const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3, w_in = blockIdx.x >> 3;
+    const int64_t x_lo = total * xcd / 8, x_n = total * (xcd + 1) / 8 - x_lo;
+    int64_t u = x_lo + x_n * w_in / wgs;
+    const int64_t u_end = x_lo + x_n * (w_in + 1) / wgs;
     if (u >= u_end) return;
-    Unit nxt = A.units[record(u)];
-    for (; u < u_end; u += stride) {
-        const int64_t q_off = uni64(nxt.q_off), k_off = uni64(nxt.k_off);
-        const int nrows = uni(nxt.rows), nkeys = uni(nxt.keys), see = uni(nxt.see);
-        nxt = A.units[record(u + stride)];   // needed a unit later
-        const int hk = (int)(u / (per_head * G)), h = hk * G + (int)(u % G);
-        const MU_GLOBAL T* kbase = (const MU_GLOBAL T*)P.k + k_off + hk * P.k_stride_h;
-        const int ntiles = (nkeys + BN - 1) / BN;
+    int h = (int)(u / per_head);
+    int64_t r = u - h * per_head;   // place in the head
+    // its sequence: the last one that starts at or before r, 64 candidates at a time
+    int64_t b = 0;
+    for (int64_t n = P.batch; n > 1;) {
+        const int64_t st = (n + 63) / 64, at = b + min<int64_t>(st * lane, n - 1);
+        const int k = __popcll(__ballot(lane * st < n && gp(A.prefix)[at] <= r));   // >= 1
+        b += (k - 1) * st;
+        n = min<int64_t>(st, n - (k - 1) * st);
+    }
+    b = uni64(b);
+    Seq S = seq_of(P, b);
+    Tiles<BM, BN> tl(S, P.causal != 0);
+    r -= uni64(gp(A.prefix)[b]);
+    int64_t t = tl.t0;
+    for (int64_t n = tl.last - tl.t0 + 1; n > 1;) {   // its query tile
+        const int64_t half_n = n / 2;
+        if (tl.before(t + half_n) <= r) t += half_n, n -= half_n;
+        else n = half_n;
+    }
+    r -= tl.before(t);
+    for (; u < u_end; r = 0) {
+        // key tiles first .. first + ntiles - 1 of query tile t, from its place r on
+        const int64_t places = min<int64_t>(COST + tl.of(t) - r, u_end - u);
+        u += places;
+        const int first = (int)max<int64_t>(r - COST, 0), ntiles = (int)max<int64_t>(r + places - COST, 0) - first;
+        if (ntiles <= 0) break;   // the run ends before the first tile
+        const int hk = h / G;
+        const int64_t k_lo = (int64_t)first * BN, off = S.nk - S.nq;
+        const int nrows = (int)min<int64_t>(BM, S.nq - t * BM);
+        const int64_t k_hi = P.causal ? min<int64_t>(S.nk, t * BM + nrows + off) : S.nk;
+        const int nkeys = (int)min<int64_t>(k_hi - k_lo, (int64_t)ntiles * BN);
+        // row i sees the run's keys j < see + i; not causal, all of them
+        const int see = P.causal ? (int)clamp64(t * BM + 1 + off - k_lo, -BM, nkeys) : nkeys;
+        const int64_t q_off = S.q0 + t * BM * P.q_stride_s;
+        const MU_GLOBAL T* kbase = (const MU_GLOBAL T*)P.k + S.k0 + hk * P.k_stride_h + k_lo * P.k_stride_s;
 
+        // Tiles past the last one are the last one again: every wave then has
+        // the same number of loads in flight at every wait.
         auto stage = [&](char* slot, int kt) {
+            kt = min(kt, ntiles - 1);
             const int rem = nkeys - kt * BN;   // rows left from this tile on
             const MU_GLOBAL T* base = kbase + (int64_t)kt * BN * P.k_stride_s;
             if constexpr (DIRECT) {
@@ -308,13 +308,12 @@ __global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
             }
         };
 
-        // this wave's queries; how many of the keys its last and its first row see
+        // this wave's queries; how many of the keys its last row sees
         const int w_row = wave * (MT * 32);
         const bool live = w_row < nrows;
         const int see_last = !live ? 0 : min(nkeys, see + min(w_row + MT * 32, nrows) - 1);
-        const int see_all = see + w_row;
-        stage(s0, 0);
-        if (ntiles > 1) stage(s1, 1);
+                stage(s0, 0);
+        stage(s1, 1);
         V qf[MT][NK];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -325,101 +324,193 @@ __global__ __launch_bounds__(NTHR, 2) void k_qkmax(QkMaxArgs A) {
         }
 
         float best = 0.f;
-        auto compute = [&](const char* slot, int kt) {
-            if (kt * BN >= see_last) return;
-            const bool border = min((kt + 1) * BN, nkeys) > see_all;
+        // The stream of right operands: tile after tile, 32 keys (a column
+        // block) after 32 keys, chunk pair after chunk pair. f holds the next
+        // PD of them; each place is read again as soon as its matrix
+        // instructions have issued, so a read has PD * MT of those to arrive.
+        // Accumulators alternate between column blocks, and the maximum of one
+        // block is taken while the next is multiplied.
+        V f[PD];
+        f32x16 acc[2][MT];
 #pragma unroll
-            for (int n = 0; n < BN / 32; ++n) {
-                f32x16 acc[MT];
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[m][e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    const V kf = *(const LDSP V*)((const LDSP char*)slot + rd[k % RA] + n * 32 * ROWB + k / RA * (RA * 32));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) acc[m] = Frag<T>::mma(qf[m][k], kf, acc[m]);
-                }
-                if (border) {
-                    const int j = min(kt * BN + n * 32 + l32, nkeys - 1) - see;
-#pragma unroll
-                    for (int m = 0; m < MT; ++m)
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int i = min(w_row + m * 32 + 8 * (e / 4) + 4 * half + e % 4, nrows - 1);
-                            acc[m][e] = j < i ? acc[m][e] : 0.f;
-                        }
-                }
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) best = absmax3(acc[m][e], acc[m][e + 1], best);
-            }
+            for (int e = 0; e < 16; ++e) acc[0][m][e] = acc[1][m][e] = 0.f;
+        auto operand = [&](const char* slot, int n, int k) {
+            return *(const LDSP V*)((const LDSP char*)slot + rd[k % RA] + n * 32 * ROWB + k / RA * (RA * 32));
         };
-        // Tile kt in slot kt % 3. The wait leaves the loads of the tile behind
-        // it in flight (counted where every wave issues the same number); past
-        // the barrier every wave has finished tile kt - 1, whose slot the next
-        // loads take.
-        auto step = [&](char* cur, char* nxt_slot, int kt) {
-            if (ROWS == FULL && kt + 1 < ntiles) MU_WAIT_VMCNT_LGKM0(NL);
-            else MU_WAIT_VMCNT_LGKM0(0);
+        auto take = [&](f32x16 (&c)[MT]) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) best = absmax3(c[m][e], c[m][e + 1], best);
+        };
+        // Makes tile kt readable (slot kt % 3) and sends for tile kt + 2, whose
+        // slot tile kt - 1 has left: past the barrier every wave holds what it
+        // read there. The wait leaves the loads of tile kt + 1 in flight
+        // (counted where every wave issues the same number).
+        auto advance = [&](char* slot2, int kt) {
+            MU_WAIT_VMCNT_LGKM0(ROWS == FULL ? NL : 0);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            if (kt + 2 < ntiles) stage(nxt_slot, kt + 2);
-            compute(cur, kt);
+            stage(slot2, kt + 2);
         };
-        for (int kt = 0; kt < ntiles; kt += 3) {
-            step(s0, s2, kt);
-            if (kt + 1 < ntiles) step(s1, s0, kt + 1);
-            if (kt + 2 < ntiles) step(s2, s1, kt + 2);
+        // tiles that all of the workgroup's rows see whole (a last tile's
+        // repeated rows count as keys)
+        const int nwhole = see >= nkeys ? ntiles : max(see, 0) / BN;
+        auto whole = [&](const char* cur, const char* nxt_slot, char* slot2, int kt) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                f32x16 (&c)[MT] = acc[NB == 1 ? 0 : n & 1];
+                f32x16 (&prev)[MT] = acc[NB == 1 ? 1 : (n & 1) ^ 1];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[m][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    if (n == NB - 1 && k == NK - PD) advance(slot2, kt + 1);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) c[m] = Frag<T>::mma(qf[m][k], f[k % PD], c[m]);
+                    const bool far = k + PD >= NK;
+                    f[k % PD] = operand(n == NB - 1 && far ? nxt_slot : cur, far ? (n + 1) % NB : n, (k + PD) % NK);
+                }
+                if constexpr (NB > 1) {
+                    take(prev);
+                    // the maxima spread behind matrix instructions, from the
+                    // second round on (the first waits for prev's last ones)
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        __builtin_amdgcn_sched_group_barrier(0x008, MT * (sizeof(T) == 2 ? 1 : 4), 0);
+                        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                        if (k > 0) __builtin_amdgcn_sched_group_barrier(0x002, (8 * MT + NK - 2) / (NK - 1), 0);
+                    }
+                } else {
+                    take(c);
+                }
+            }
+        };
+        // Any other tile: one that the causal border crosses, or that some
+        // waves do not see, or left over from the threes.
+        auto border = [&](const char* cur, int kt) {
+            if (kt * BN >= see_last) return;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                f32x16 (&c)[MT] = acc[0];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[m][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < NK; ++k) {
+                    const V kf = operand(cur, n, k);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) c[m] = Frag<T>::mma(qf[m][k], kf, c[m]);
+                }
+                const int j = min(kt * BN + n * 32 + l32, nkeys - 1) - see;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int i = min(w_row + m * 32 + 8 * (e / 4) + 4 * half + e % 4, nrows - 1);
+                        c[m][e] = j < i ? c[m][e] : 0.f;
+                    }
+                take(c);
+            }
+        };
+        // Whole tiles three at a time without a branch in between, the others
+        // one by one. (Where paths meet the compiler forgets which slot a load
+        // in flight goes to and waits for all of them before the next read: once
+        // in three tiles here, and there the youngest load is half a tile old.)
+        advance(s2, 0);
+        int kt = 0;
+        if (nwhole >= 3) {
+#pragma unroll
+            for (int k = 0; k < PD; ++k) f[k] = operand(s0, 0, k);
+            do {
+                whole(s0, s1, s0, kt);
+                whole(s1, s2, s1, kt + 1);
+                whole(s2, s0, s2, kt + 2);
+                kt += 3;
+            } while (kt + 3 <= nwhole);
         }
+        while (kt < ntiles) {
+            border(s0, kt);
+            if (++kt >= ntiles) break;
+            advance(s0, kt);
+            border(s1, kt);
+            if (++kt >= ntiles) break;
+            advance(s1, kt);
+            border(s2, kt);
+            if (++kt >= ntiles) break;
+            advance(s2, kt);
+        }
+        if constexpr (NB > 1) take(acc[1]);
         int bits = __float_as_int(best) & 0x7fffffff;
         for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
         if (lane == 0) red[wave] = bits;
         __syncthreads();   // also: every wave is done with the slots
         if (tid == 0) {
             bits = max(max(red[0], red[1]), max(red[2], red[3]));
-            if (bits) atomicMax((int*)P.max_logit + h, __float_as_int(__builtin_fabsf(P.scale) * __int_as_float(bits)) & 0x7fffffff);
+            if (bits > 0) atomicMax((int*)P.max_logit + h, __float_as_int(__builtin_fabsf(P.scale) * __int_as_float(bits)) & 0x7fffffff);
         }
+        // the next query tile, sequence or head
+        if (++t <= tl.last || u >= u_end) continue;
+        do {
+            if (++b == P.batch) b = 0, ++h;
+            S = seq_of(P, b);
+            tl = Tiles<BM, BN>(S, P.causal != 0);
+        } while (tl.last < 0);   // a later sequence has tiles: u < u_end
+        t = tl.t0;
     }
 }
 
-template <typename T, int DP, int BN, int MT, int NS>
+template <typename T, int DP, int BN, int MT, int WPE>
 hipError_t launch(const QkMaxArgs& a, bool direct, int grid, hipStream_t s) {
-    if (!direct) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, NS, RAGGED>), dim3(grid), dim3(NTHR), 0, s, a);
-    else if (a.p.dim < DP) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, NS, PADDED>), dim3(grid), dim3(NTHR), 0, s, a);
-    else hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, NS, FULL>), dim3(grid), dim3(NTHR), 0, s, a);
+    if (!direct) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, RAGGED>), dim3(grid), dim3(NTHR), 0, s, a);
+    else if (a.p.dim < DP) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, PADDED>), dim3(grid), dim3(NTHR), 0, s, a);
+    else hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, FULL>), dim3(grid), dim3(NTHR), 0, s, a);
     return hipGetLastError();
 }
 
-// Instances by padded head width.
-struct Shape {
-    int dp, bn, bm;
-};
-Shape shape_of(int dtype, int dim) {
-    const int dp = dim <= 32 ? 32 : dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : dim <= 192 ? 192 : 256;
-    if (dtype == MU_BF16) return {dp, dp <= 128 ? 64 : 32, 256};
-    return {dp, 32, dp <= 128 ? 256 : 128};
+// An instance: padded head width, keys and queries of a tile.
+template <typename T, int DP, int BN, int MT, int WPE>
+int run(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, double bytes, hipStream_t s) {
+    const QkMaxArgs q{*a, prefix};
+    constexpr int BM = 4 * MT * 32;
+    int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, s, [&] {
+        hipLaunchKernelGGL((k_qk_plan<BM, BN>), dim3(1), dim3(PLAN_THR), 0, s, q, prefix);
+        return hipGetLastError();
+    }, "max logits plan");
+    if (rc || flops == 0.0) return rc;
+    int cus = 0;
+    rc = cu_count(&cus);
+    if (rc) return rc;
+    // two workgroups a compute unit; fewer where there cannot be as many tiles
+    const int64_t seqs = a->cu_q ? 1 : a->batch, more = a->cu_q ? a->batch : 0;
+    const double tiles = ((double)seqs * ((a->q_len + BM - 1) / BM) + (double)more) * (double)((a->k_len + BN - 1) / BN) * a->q_heads;
+    const int grid = (int)std::min<double>((double)WPE * cus, 8.0 * std::ceil(tiles / 8.0));
+    return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch<T, DP, BN, MT, WPE>(q, direct, grid, s); },
+                        "max logits launch");
 }
-hipError_t launch_shape(const QkMaxArgs& a, int dp, bool direct, int grid, hipStream_t s) {
-    if (a.p.dtype == MU_BF16) switch (dp) {
-        case 32: return launch<bf16, 32, 64, 2, 3>(a, direct, grid, s);
-        case 64: return launch<bf16, 64, 64, 2, 3>(a, direct, grid, s);
-        case 96: return launch<bf16, 96, 64, 2, 3>(a, direct, grid, s);
-        case 128: return launch<bf16, 128, 64, 2, 3>(a, direct, grid, s);
-        case 192: return launch<bf16, 192, 32, 2, 3>(a, direct, grid, s);
-        default: return launch<bf16, 256, 32, 2, 3>(a, direct, grid, s);
+
+int run_any(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, double bytes, hipStream_t s) {
+    const int d = a->dim;
+    if (a->dtype == MU_BF16) {
+        if (d <= 32) return run<bf16, 32, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
+        if (d <= 64) return run<bf16, 64, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
+        if (d <= 96) return run<bf16, 96, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
+        if (d <= 128) return run<bf16, 128, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
+        if (d <= 192) return run<bf16, 192, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+        return run<bf16, 256, 32, 2, 1>(a, prefix, direct, flops, bytes, s);
     }
-    switch (dp) {
-        case 32: return launch<float, 32, 32, 2, 3>(a, direct, grid, s);
-        case 64: return launch<float, 64, 32, 2, 3>(a, direct, grid, s);
-        case 96: return launch<float, 96, 32, 2, 3>(a, direct, grid, s);
-        case 128: return launch<float, 128, 32, 2, 3>(a, direct, grid, s);
-        case 192: return launch<float, 192, 32, 1, 3>(a, direct, grid, s);
-        default: return launch<float, 256, 32, 1, 3>(a, direct, grid, s);
-    }
+    if (d <= 32) return run<float, 32, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 64) return run<float, 64, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 96) return run<float, 96, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 128) return run<float, 128, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 192) return run<float, 192, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
+    return run<float, 256, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
 }
 
 int check(const mu_qk_logits* a) {
@@ -448,26 +539,7 @@ int check(const mu_qk_logits* a) {
     return MU_OK;
 }
 
-// What a call launches.
-struct Plan {
-    Shape sh;
-    int64_t key_chunk;
-    int64_t most;      // units of one head at most
-    size_t bytes;      // of workspace
-};
-Plan plan_of(const mu_qk_logits* a) {
-    Plan p;
-    p.sh = shape_of(a->dtype, a->dim);
-    const int64_t seqs = std::max<int64_t>(1, a->batch), bm = p.sh.bm;
-    const int64_t tiles = a->cu_q ? a->q_len / bm + seqs : seqs * ((a->q_len + bm - 1) / bm);
-    const int64_t keys = a->cu_q ? (a->k_len + seqs - 1) / seqs : a->k_len;   // of a sequence, about
-    // Key chunk: a few units for each workgroup slot, between 256 and 4096 keys.
-    p.key_chunk = 4096;
-    while (p.key_chunk > 256 && tiles * a->q_heads * ((keys + p.key_chunk - 1) / p.key_chunk) < 8 * 2 * 256) p.key_chunk /= 2;
-    p.most = tiles * ((a->k_len + p.key_chunk - 1) / p.key_chunk);
-    p.bytes = ALIGN + align_up(sizeof(Unit) * (size_t)p.most);
-    return p;
-}
+size_t qk_workspace(const mu_qk_logits* a) { return align_up(sizeof(int64_t) * ((size_t)a->batch + 1)); }
 
 }  // namespace
 
@@ -478,7 +550,7 @@ int mu_qk_max_logits_workspace_size(const mu_qk_logits* a, size_t* bytes) {
         if (!bytes) return fail(MU_ERR_INVALID_ARG, "bytes is null");
         int rc = check(a);
         if (rc) return rc;
-        *bytes = plan_of(a).bytes;
+        *bytes = qk_workspace(a);
         return MU_OK;
     });
 }
@@ -489,34 +561,19 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* str
         if (rc) return rc;
         const bool empty = a->batch == 0 || a->q_len == 0 || a->k_len == 0;
         if (empty && a->accumulate) return MU_OK;
-        const Plan pl = plan_of(a);
-        const Shape sh = pl.sh;
-        if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", pl.bytes);
+        const size_t need = qk_workspace(a);
+        if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
         if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-        if (ws_bytes < pl.bytes) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, pl.bytes);
-        hipStream_t s = (hipStream_t)stream;
+        if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
         const int es = a->dtype == MU_BF16 ? 2 : 4;
         // rows as whole 16-byte chunks, a tile of them within 32-bit offsets
         const int64_t mix = a->q_stride_b | a->q_stride_s | a->q_stride_h | a->k_stride_b | a->k_stride_s | a->k_stride_h | a->dim;
         const bool direct = (mix * es) % 16 == 0 && aligned(a->q, 16) && aligned(a->k, 16) &&
-                            a->k_stride_s < ((int64_t)1 << 30) / (sh.bn * es);
-        int64_t* count = (int64_t*)ws;
-        Unit* units = (Unit*)((char*)ws + ALIGN);
-        const QkMaxArgs q{*a, count, units, pl.key_chunk};
-        rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, s, [&] {
-            hipLaunchKernelGGL(k_qk_plan, dim3(1), dim3(PLAN_THR), 0, s, q, count, units, sh.bm);
-            return hipGetLastError();
-        }, "max logits plan");
-        if (rc || empty) return rc;
-        int cus = 0;
-        rc = cu_count(&cus);
-        if (rc) return rc;
+                            a->k_stride_s < ((int64_t)1 << 30) / (64 * es);
         const double nb = a->cu_q ? 1 : a->batch;
         const double bytes = nb * a->dim * es * ((double)a->q_len * a->q_heads + (double)a->k_len * a->k_heads);
-        const double flops = 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
-        const int grid = (int)std::min<int64_t>(2 * (int64_t)cus, (pl.most * a->q_heads + 7) / 8 * 8);
-        return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch_shape(q, sh.dp, direct, grid, s); },
-                            "max logits launch");
+        const double flops = empty ? 0.0 : 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
+        return run_any(a, (int64_t*)ws, direct, flops, bytes, (hipStream_t)stream);
     });
 }
 
