@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/muon_mi355x.h"
@@ -43,7 +44,7 @@ struct QkMaxArgs {
 
 struct Seq {
     int64_t q0, k0;   // element offset of its first row (without the head)
-    int64_t nq, nk;
+    int32_t nq, nk;
 };
 
 __device__ inline int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -54,13 +55,13 @@ __device__ inline Seq seq_of(const mu_qk_logits& A, int64_t b) {
         const MU_GLOBAL int32_t* cq = (const MU_GLOBAL int32_t*)A.cu_q;
         const MU_GLOBAL int32_t* ck = A.cu_k ? (const MU_GLOBAL int32_t*)A.cu_k : cq;
         const int64_t a = clamp64(cq[b], 0, A.q_len), c = clamp64(ck[b], 0, A.k_len);
-        s.nq = clamp64(cq[b + 1], a, A.q_len) - a;
-        s.nk = clamp64(ck[b + 1], c, A.k_len) - c;
+        s.nq = (int32_t)(clamp64(cq[b + 1], a, A.q_len) - a);
+        s.nk = (int32_t)(clamp64(ck[b + 1], c, A.k_len) - c);
         s.q0 = a * A.q_stride_s;
         s.k0 = c * A.k_stride_s;
     } else {
-        s.nq = A.q_lengths ? clamp64(((const MU_GLOBAL int32_t*)A.q_lengths)[b], 0, A.q_len) : A.q_len;
-        s.nk = A.k_lengths ? clamp64(((const MU_GLOBAL int32_t*)A.k_lengths)[b], 0, A.k_len) : A.k_len;
+        s.nq = (int32_t)(A.q_lengths ? clamp64(((const MU_GLOBAL int32_t*)A.q_lengths)[b], 0, A.q_len) : A.q_len);
+        s.nk = (int32_t)(A.k_lengths ? clamp64(((const MU_GLOBAL int32_t*)A.k_lengths)[b], 0, A.k_len) : A.k_len);
         s.q0 = b * A.q_stride_b;
         s.k0 = b * A.k_stride_b;
     }
@@ -73,21 +74,23 @@ __device__ inline Seq seq_of(const mu_qk_logits& A, int64_t b) {
 constexpr int COST = 6;
 template <int BM, int BN>
 struct Tiles {
-    int64_t t0, last, all;   // first and last query tile with keys, tiles of all keys
-    int64_t o;
+    int t0, last, all;   // first and last query tile with keys, tiles of all keys
+    int o;
     bool causal;
     __device__ Tiles(const Seq& S, bool c) : causal(c) {
+        // (lengths are below 2^31 - 256)
         last = (S.nq + BM - 1) / BM - 1;
         all = (S.nk + BN - 1) / BN;
-        const int64_t off = S.nk - S.nq;
+        const int off = S.nk - S.nq;
         o = off >= 0 ? (off + BN - 1) / BN : -(-off / BN);
         t0 = causal && off < 0 ? (BM - off) / BM - 1 : 0;   // ceil((1 - off) / BM) - 1
         if (S.nq <= 0 || S.nk <= 0) t0 = 0, last = -1;
     }
-    __device__ int64_t of(int64_t t) const { return causal && t < last ? (t + 1) * (BM / BN) + o : all; }
+    __device__ int of(int t) const { return causal && t < last ? (t + 1) * (BM / BN) + o : all; }
     // places of the query tiles before t, t0 <= t <= last
-    __device__ int64_t before(int64_t t) const {
-        return (t - t0) * COST + (causal ? (t - t0) * o + (BM / BN) * (t * (t + 1) / 2 - t0 * (t0 + 1) / 2) : t * all);
+    __device__ int64_t before(int t) const {
+        const int64_t n = t - t0, both = (int64_t)t + t0 + 1;   // t (t + 1) - t0 (t0 + 1) = n both
+        return n * COST + (causal ? n * o + (BM / BN) * (n * both / 2) : n * all);
     }
     __device__ int64_t total() const { return last < 0 ? 0 : before(last) + COST + all; }
 };
@@ -187,7 +190,8 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 // one chunk column of 16 rows over all 16 positions of 256 bytes: no bank
 // conflicts at any NC. FULL and PADDED rows go from memory straight into the
 // slot (the lane's address carries the permutation; chunks beyond dim are zeroed
-// once and never written), RAGGED ones pass through registers.
+// once, and their loads lie outside the buffer resource, which gives zeros),
+// RAGGED ones pass through registers.
 //
 // Rows past the end of a sequence read its last row again, which cannot change
 // a maximum; only tiles that the causal border crosses test each pair.
@@ -260,9 +264,9 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     Seq S = seq_of(P, b);
     Tiles<BM, BN> tl(S, P.causal != 0);
     r -= uni64(gp(A.prefix)[b]);
-    int64_t t = tl.t0;
-    for (int64_t n = tl.last - tl.t0 + 1; n > 1;) {   // its query tile
-        const int64_t half_n = n / 2;
+    int t = tl.t0;
+    for (int n = tl.last - tl.t0 + 1; n > 1;) {   // its query tile
+        const int half_n = n / 2;
         if (tl.before(t + half_n) <= r) t += half_n, n -= half_n;
         else n = half_n;
     }
@@ -274,14 +278,14 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         const int first = (int)max<int64_t>(r - COST, 0), ntiles = (int)max<int64_t>(r + places - COST, 0) - first;
         if (ntiles <= 0) break;   // the run ends before the first tile
         const int hk = h / G;
-        const int64_t k_lo = (int64_t)first * BN, off = S.nk - S.nq;
-        const int nrows = (int)min<int64_t>(BM, S.nq - t * BM);
-        const int64_t k_hi = P.causal ? min<int64_t>(S.nk, t * BM + nrows + off) : S.nk;
-        const int nkeys = (int)min<int64_t>(k_hi - k_lo, (int64_t)ntiles * BN);
+        const int k_lo = first * BN, off = S.nk - S.nq;
+        const int nrows = min(BM, S.nq - t * BM);
+        const int k_hi = P.causal ? min(S.nk, t * BM + nrows + off) : S.nk;
+        const int nkeys = min(k_hi - k_lo, ntiles * BN);
         // row i sees the run's keys j < see + i; not causal, all of them
-        const int see = P.causal ? (int)clamp64(t * BM + 1 + off - k_lo, -BM, nkeys) : nkeys;
-        const int64_t q_off = S.q0 + t * BM * P.q_stride_s;
-        const MU_GLOBAL T* kbase = (const MU_GLOBAL T*)P.k + S.k0 + hk * P.k_stride_h + k_lo * P.k_stride_s;
+        const int see = P.causal ? min(max(t * BM + 1 + off - k_lo, -BM), nkeys) : nkeys;
+        const int64_t q_off = S.q0 + (int64_t)t * BM * P.q_stride_s;
+        const MU_GLOBAL T* kbase = (const MU_GLOBAL T*)P.k + S.k0 + hk * P.k_stride_h + (int64_t)k_lo * P.k_stride_s;
 
         // Tiles past the last one are the last one again: every wave then has
         // the same number of loads in flight at every wait.
@@ -295,9 +299,9 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
                     __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (BN - 1) * sb + P.dim * (int)sizeof(T), BUF_RAW32);
 #pragma unroll
                 for (int j = 0; j < NL; ++j) {
-                    const int vo = min(lrow[j], rem - 1) * sb + lchk[j] * 16;
-                    if (ROWS == FULL || lchk[j] * EPC < P.dim)
-                        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDSP void*)(slot + lpos[j] * 1024), 16, vo, 0, 0, 0);
+                    int vo = min(lrow[j], rem - 1) * sb + lchk[j] * 16;
+                    if (ROWS == PADDED && lchk[j] * EPC >= P.dim) vo = 0x7fffff00;   // beyond the resource: reads nothing
+                    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LDSP void*)(slot + lpos[j] * 1024), 16, vo, 0, 0, 0);
                 }
             } else {
 #pragma unroll
@@ -339,7 +343,16 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         auto operand = [&](const char* slot, int n, int k) {
             return *(const LDSP V*)((const LDSP char*)slot + rd[k % RA] + n * 32 * ROWB + k / RA * (RA * 32));
         };
-        auto take = [&](f32x16 (&c)[MT]) {
+        // The maximum over a block of logits. A lane's element e of block m is
+        // row 32 m + 8 (e / 4) + e % 4 (from a base of its own) of one key; MASK:
+        // only rows beyond `thr` see it.
+        auto take = [&](auto mask, f32x16 (&c)[MT], int thr) {
+            if constexpr (decltype(mask)::value) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) c[m][e] = thr < m * 32 + 8 * (e / 4) + e % 4 ? c[m][e] : 0.f;
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -347,19 +360,21 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         };
         // Makes tile kt readable (slot kt % 3) and sends for tile kt + 2, whose
         // slot tile kt - 1 has left: past the barrier every wave holds what it
-        // read there. The wait leaves the loads of tile kt + 1 in flight
-        // (counted where every wave issues the same number).
+        // read there. The wait leaves the loads of tile kt + 1 in flight.
         auto advance = [&](char* slot2, int kt) {
-            MU_WAIT_VMCNT_LGKM0(ROWS == FULL ? NL : 0);
+            MU_WAIT_VMCNT_LGKM0(DIRECT ? NL : 0);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             stage(slot2, kt + 2);
         };
-        // tiles that all of the workgroup's rows see whole (a last tile's
-        // repeated rows count as keys)
-        const int nwhole = see >= nkeys ? ntiles : max(see, 0) / BN;
-        auto whole = [&](const char* cur, const char* nxt_slot, char* slot2, int kt) {
+        // One tile. MASK: the causal border may cross it. (Rows past nrows and
+        // keys past nkeys repeat the last ones; the last row sees every key of
+        // the run, so neither needs a test of its own.)
+        constexpr int SEE_ALL = -(1 << 30);
+        int thr_prev = SEE_ALL;
+        const int thr_lane = l32 - see - w_row - 4 * half;
+        auto tile = [&](auto mask, const char* cur, const char* nxt_slot, char* slot2, int kt) {
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 f32x16 (&c)[MT] = acc[NB == 1 ? 0 : n & 1];
@@ -376,77 +391,50 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
                     const bool far = k + PD >= NK;
                     f[k % PD] = operand(n == NB - 1 && far ? nxt_slot : cur, far ? (n + 1) % NB : n, (k + PD) % NK);
                 }
+                const int thr = kt * BN + n * 32 + thr_lane;
                 if constexpr (NB > 1) {
-                    take(prev);
+                    take(mask, prev, thr_prev);
                     // the maxima spread behind matrix instructions, from the
                     // second round on (the first waits for prev's last ones)
 #pragma unroll
-                    for (int k = 0; k < NK; ++k) {
+                    for (int k = 0; k < NK && !decltype(mask)::value; ++k) {
                         __builtin_amdgcn_sched_group_barrier(0x008, MT * (sizeof(T) == 2 ? 1 : 4), 0);
                         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         if (k > 0) __builtin_amdgcn_sched_group_barrier(0x002, (8 * MT + NK - 2) / (NK - 1), 0);
                     }
                 } else {
-                    take(c);
+                    take(mask, c, thr);
                 }
+                if (decltype(mask)::value) thr_prev = thr;
             }
         };
-        // Any other tile: one that the causal border crosses, or that some
-        // waves do not see, or left over from the threes.
-        auto border = [&](const char* cur, int kt) {
-            if (kt * BN >= see_last) return;
-#pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                f32x16 (&c)[MT] = acc[0];
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) c[m][e] = 0.f;
-#pragma unroll
-                for (int k = 0; k < NK; ++k) {
-                    const V kf = operand(cur, n, k);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) c[m] = Frag<T>::mma(qf[m][k], kf, c[m]);
-                }
-                const int j = min(kt * BN + n * 32 + l32, nkeys - 1) - see;
-#pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int i = min(w_row + m * 32 + 8 * (e / 4) + 4 * half + e % 4, nrows - 1);
-                        c[m][e] = j < i ? c[m][e] : 0.f;
-                    }
-                take(c);
-            }
-        };
-        // Whole tiles three at a time without a branch in between, the others
-        // one by one. (Where paths meet the compiler forgets which slot a load
-        // in flight goes to and waits for all of them before the next read: once
-        // in three tiles here, and there the youngest load is half a tile old.)
+        // Tiles that all of the workgroup's rows see whole go three at a time
+        // without a branch in between, then the others. The code keeps to
+        // straight runs: where paths meet the compiler forgets which slot a
+        // load in flight goes to and waits for all of them before the next read
+        // (at the heads of the two loops here). A wave whose rows see nothing
+        // further leaves, and only takes its part in loads and barriers.
         advance(s2, 0);
-        int kt = 0;
-        if (nwhole >= 3) {
 #pragma unroll
-            for (int k = 0; k < PD; ++k) f[k] = operand(s0, 0, k);
-            do {
-                whole(s0, s1, s0, kt);
-                whole(s1, s2, s1, kt + 1);
-                whole(s2, s0, s2, kt + 2);
-                kt += 3;
-            } while (kt + 3 <= nwhole);
+        for (int k = 0; k < PD; ++k) f[k] = operand(s0, 0, k);
+        const int nwhole = see >= nkeys ? ntiles : max(see, 0) / BN;
+        int kt = 0;
+        for (; kt + 3 <= nwhole; kt += 3) {
+            tile(std::false_type{}, s0, s1, s0, kt);
+            tile(std::false_type{}, s1, s2, s1, kt + 1);
+            tile(std::false_type{}, s2, s0, s2, kt + 2);
         }
-        while (kt < ntiles) {
-            border(s0, kt);
-            if (++kt >= ntiles) break;
-            advance(s0, kt);
-            border(s1, kt);
-            if (++kt >= ntiles) break;
-            advance(s1, kt);
-            border(s2, kt);
-            if (++kt >= ntiles) break;
-            advance(s2, kt);
+        for (;;) {
+            if (kt * BN >= see_last) break;
+            tile(std::true_type{}, s0, s1, s0, kt);
+            if (++kt * BN >= see_last) break;
+            tile(std::true_type{}, s1, s2, s1, kt);
+            if (++kt * BN >= see_last) break;
+            tile(std::true_type{}, s2, s0, s2, kt);
+            ++kt;
         }
-        if constexpr (NB > 1) take(acc[1]);
+        if constexpr (NB > 1) take(std::true_type{}, acc[1], thr_prev);
+        for (; kt < ntiles; ++kt) advance(kt % 3 == 0 ? s0 : kt % 3 == 1 ? s1 : s2, kt + 1);
         int bits = __float_as_int(best) & 0x7fffffff;
         for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
         if (lane == 0) red[wave] = bits;
