@@ -4,8 +4,8 @@
 //   out[t, :]  = scale * weight[tokens[t], :]
 //   grad[v, :] = scale * sum over t with tokens[t] == v, in rising t, of rows[t, :]
 //
-// The gradient sorts the tokens (stable, by least significant digits; tokens
-// outside the table and the padding token sort behind all others), then sums
+// The gradient sorts the tokens (stable; tokens outside the table and the
+// padding token sort behind all others), then sums
 // the rows in sorted order: chunks of C consecutive entries, a wave for each
 // chunk and slice of columns, whatever the distribution of the tokens. A run
 // of equal tokens inside a chunk is a finished row; a run that crosses chunk
@@ -134,10 +134,9 @@ __global__ __launch_bounds__(NTHR) void k_lookup(LookupArgs A) {
 // ---------------------------------------------------------------------------
 // Sort. Keys are table rows, `vocab` for tokens that add nothing.
 // ---------------------------------------------------------------------------
-constexpr int STHR = 1024, SWAVES = STHR / 64;
 constexpr int DIGIT = 9, RADIX = 1 << DIGIT;      // two passes up to 2^18 - 1 rows
-constexpr int SORT_ONE = 16384;                   // tokens that one workgroup sorts by itself
-constexpr int SORT_TILE = 8192;                   // tokens of a workgroup otherwise
+constexpr int SORT_RANK = 16384;                  // tokens sorted by counting smaller ones
+constexpr int SORT_IPT = 8;                       // digit passes: tokens a thread
 
 struct SortArgs {
     mu_rowgrad e;
@@ -148,23 +147,21 @@ struct SortArgs {
     int32_t* hist;           // [RADIX][tiles] digit counts of each tile
     int n, tiles;
     int shift;               // digit of this pass
-    int passes;              // one-workgroup sort: all of them
+    int index_bits;          // counting: bits of a token's place
     // the gradient's zeros are written by further workgroups of the sorting launches
     char* fill;
     int64_t fill_bytes;
     int sorters;             // workgroups 0 .. sorters - 1 sort
 };
 
-// Zeros, FILL_WG bytes a workgroup: sorting keeps one or a few compute units
-// busy and waits on latency, so it runs beside the stores rather than before.
-constexpr int64_t FILL_WG = (int64_t)STHR * 16 * 8;
+// Zeros, FILL_WG bytes a workgroup: the sort computes and waits on latency, so
+// it runs beside the stores rather than before.
+constexpr int64_t FILL_WG = 65536;
 __device__ __forceinline__ void fill_zeros(const SortArgs& A) {
     const int64_t at = (int64_t)(blockIdx.x - A.sorters) * FILL_WG;
     MU_GLOBAL char* p = (MU_GLOBAL char*)A.fill + at;
-    const int64_t left = A.fill_bytes - at;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t o = ((int64_t)i * STHR + threadIdx.x) * 16;
+    const int64_t left = min<int64_t>(FILL_WG, A.fill_bytes - at), step = (int64_t)blockDim.x * 16;
+    for (int64_t o = (int64_t)threadIdx.x * 16; o < left; o += step) {
         if (o + 16 <= left) *(MU_GLOBAL u32x4u*)(p + o) = u32x4{0, 0, 0, 0};
         else
             for (int64_t j = o; j < left; j += 2) *(MU_GLOBAL short*)(p + j) = 0;
@@ -176,26 +173,73 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs& A, int t) {
     return v >= 0 && v < A.e.vocab && v != A.e.padding_idx ? (uint32_t)v : (uint32_t)A.e.vocab;
 }
 
+// Few tokens: a token's place is the number of tokens that sort before it. With
+// key and place in one word (the place below the key) these are the smaller
+// words. A workgroup holds all words in LDS and places RANK_ITEMS tokens, each
+// counted by eight lanes over an eighth of the words: n^2 comparisons spread
+// over the chip, one launch and no passes. 8192 tokens: the digit passes of one
+// workgroup took 22 us.
+constexpr int RANK_THR = 256, RANK_ITEMS = 32, RANK_PARTS = RANK_THR / RANK_ITEMS;
+template <typename W>
+__global__ __launch_bounds__(RANK_THR) void k_sort_rank(SortArgs A) {
+    extern __shared__ __align__(16) char raw[];
+    __shared__ int count[RANK_PARTS][RANK_ITEMS];
+    if ((int)blockIdx.x >= A.sorters) {
+        fill_zeros(A);
+        return;
+    }
+    constexpr int PER = 16 / (int)sizeof(W);   // words of one LDS read
+    typedef W WV __attribute__((ext_vector_type(PER)));
+    LDSP W* word = (LDSP W*)(LDSP char*)raw;
+    const int tid = threadIdx.x;
+    const int part = ((A.n + RANK_PARTS - 1) / RANK_PARTS + PER - 1) / PER * PER;   // words of an eighth
+    for (int i = tid; i < part * RANK_PARTS; i += RANK_THR)
+        word[i] = i < A.n ? ((W)key_of(A, i) << A.index_bits) | (W)i : ~(W)0;
+    __syncthreads();
+    const int item = blockIdx.x * RANK_ITEMS + tid % RANK_ITEMS, q = tid / RANK_ITEMS;
+    const W mine = word[min(item, A.n - 1)];
+    int n = 0;
+    const LDSP WV* from = (const LDSP WV*)(word + q * part);
+#pragma unroll 8
+    for (int i = 0; i < part / PER; ++i) {
+        const WV x = from[i];
+#pragma unroll
+        for (int k = 0; k < PER; ++k) n += x[k] < mine;
+    }
+    count[q][tid % RANK_ITEMS] = n;
+    __syncthreads();
+    if (tid >= RANK_ITEMS || item >= A.n) return;
+    n = 0;
+#pragma unroll
+    for (int k = 0; k < RANK_PARTS; ++k) n += count[k][tid];
+    gp(A.key_out)[n] = (int32_t)(mine >> A.index_bits);
+    gp(A.pos_out)[n] = item;
+}
+
+// More tokens: two launches for each digit, over tiles of THR * SORT_IPT.
+//
 // Stable rank of each lane's digit among those of its wave, counted on in
 // cnt[digit]; lanes with the same digit find each other by one ballot a bit.
 __device__ __forceinline__ int wave_rank(uint32_t d, bool on, volatile LDSP int* cnt) {
-    uint64_t same = __ballot(on);
+    const uint64_t all = __ballot(on);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
 #pragma unroll
     for (int b = 0; b < DIGIT; ++b) {
-        const bool bit = (d >> b) & 1;
-        const uint64_t m = __ballot(on && bit);
-        same &= bit ? m : ~m;
+        const uint32_t bit = (uint32_t)((int32_t)(d << (31 - b)) >> 31);   // all ones where set
+        const uint64_t m = __ballot(bit != 0);
+        lo &= ~((uint32_t)m ^ bit);
+        hi &= ~((uint32_t)(m >> 32) ^ bit);
     }
-    const int lane = threadIdx.x & 63;
-    const int below = __popcll(same & ((1ull << lane) - 1));
+    const int below = __builtin_amdgcn_mbcnt_hi(hi, __builtin_amdgcn_mbcnt_lo(lo, 0));
     int base = 0;
     if (on) base = cnt[d];
     // (a wave's LDS accesses keep their order: every read above comes first)
-    if (on && below == 0) cnt[d] = base + __popcll(same);
+    if (on && below == 0) cnt[d] = base + __popc(lo) + __popc(hi);
     return base + below;
 }
 
 // Exclusive sum over the workgroup in thread order.
+template <int THR>
 __device__ __forceinline__ int block_scan(int v, int* wsum) {
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     int s = v;
@@ -206,156 +250,101 @@ __device__ __forceinline__ int block_scan(int v, int* wsum) {
     if (lane == 63) wsum[w] = s;
     __syncthreads();
     int before = s - v;
-    for (int i = 0; i < SWAVES; ++i)
+#pragma unroll
+    for (int i = 0; i < THR / 64; ++i)
         if (i < w) before += wsum[i];
     __syncthreads();
     return before;
 }
 
-// Up to SORT_ONE tokens in one workgroup: item i * 64 + lane of wave w's run of
-// ipt * 64 items is thread (w, lane)'s i-th, so that rising (w, i, lane) is the
-// items' order and ranks taken in it are stable. All passes stay in LDS.
-// About 12 us for 8192 tokens and two passes, beside the stores of the zeros.
-__global__ __launch_bounds__(STHR) void k_sort_one(SortArgs A) {
-    __shared__ uint32_t skey[SORT_ONE];
-    __shared__ uint16_t spos[SORT_ONE];
-    __shared__ int cnt[SWAVES * RADIX];
-    __shared__ int wsum[SWAVES];
-    if ((int)blockIdx.x >= A.sorters) {
-        fill_zeros(A);
-        return;
-    }
-    constexpr int IPT = SORT_ONE / STHR;
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int ipt = (A.n + STHR - 1) / STHR, first = w * ipt * 64 + lane;
-    uint32_t key[IPT];
-    int pos[IPT], rank[IPT];
-    // behind the items: keys that sort last
+// Thread (w, lane)'s i-th item is i * 64 + lane of wave w's run: rising (w, i,
+// lane) is the items' order, and ranks taken in it are stable.
+template <int THR>
+__device__ __forceinline__ void tile_items(const SortArgs& A, uint32_t key[SORT_IPT], int pos[SORT_IPT], bool on[SORT_IPT]) {
+    const int first = blockIdx.x * (THR * SORT_IPT) + (threadIdx.x >> 6) * SORT_IPT * 64 + (threadIdx.x & 63);
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-        pos[i] = first + i * 64;
-        key[i] = i < ipt && pos[i] < A.n ? key_of(A, pos[i]) : 0xffffffffu;
-    }
-    for (int pass = 0; pass < A.passes; ++pass) {
-        for (int i = tid; i < SWAVES * RADIX; i += STHR) cnt[i] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < IPT; ++i)
-            if (i < ipt) rank[i] = wave_rank((key[i] >> (pass * DIGIT)) & (RADIX - 1), true, (volatile LDSP int*)cnt + w * RADIX);
-        __syncthreads();
-        // cnt[w][d] -> items of smaller digits, and of this digit in earlier waves
-        {
-            const int d = tid >> 1, w0 = (tid & 1) * (SWAVES / 2);
-            int c[SWAVES / 2], sum = 0;
-#pragma unroll
-            for (int k = 0; k < SWAVES / 2; ++k) {
-                c[k] = cnt[(w0 + k) * RADIX + d];
-                sum += c[k];
-            }
-            int before = block_scan(sum, wsum);
-#pragma unroll
-            for (int k = 0; k < SWAVES / 2; ++k) {
-                cnt[(w0 + k) * RADIX + d] = before;
-                before += c[k];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < IPT; ++i)
-            if (i < ipt) {
-                const int to = cnt[w * RADIX + ((key[i] >> (pass * DIGIT)) & (RADIX - 1))] + rank[i];
-                skey[to] = key[i];
-                spos[to] = (uint16_t)pos[i];
-            }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < IPT; ++i)
-            if (i < ipt) {
-                key[i] = skey[first + i * 64];
-                pos[i] = spos[first + i * 64];
-            }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-        const int j = first + i * 64;
-        if (i < ipt && j < A.n) {
-            gp(A.key_out)[j] = (int32_t)key[i];
-            gp(A.pos_out)[j] = pos[i];
-        }
-    }
-}
-static_assert(RADIX * 2 == STHR, "two threads a digit");
-
-// More tokens: two launches a pass over tiles of SORT_TILE.
-constexpr int TIPT = SORT_TILE / STHR;
-__device__ __forceinline__ void tile_items(const SortArgs& A, uint32_t key[TIPT], int pos[TIPT], bool on[TIPT]) {
-    const int first = blockIdx.x * SORT_TILE + (threadIdx.x >> 6) * TIPT * 64 + (threadIdx.x & 63);
-#pragma unroll
-    for (int i = 0; i < TIPT; ++i) {
-        const int j = first + i * 64;
-        on[i] = j < A.n;
-        key[i] = !on[i] ? 0 : A.key_in ? (uint32_t)gp(A.key_in)[j] : key_of(A, j);
-        pos[i] = !on[i] ? 0 : A.key_in ? gp(A.pos_in)[j] : j;
+    for (int i = 0; i < SORT_IPT; ++i) {
+        const int j = min(first + i * 64, A.n - 1);
+        on[i] = first + i * 64 < A.n;
+        key[i] = A.key_in ? (uint32_t)gp(A.key_in)[j] : key_of(A, j);
+        pos[i] = A.key_in ? gp(A.pos_in)[j] : j;
     }
 }
 
-__global__ __launch_bounds__(STHR) void k_sort_count(SortArgs A) {
+template <int THR>
+__global__ __launch_bounds__(THR) void k_sort_count(SortArgs A) {
     __shared__ int cnt[RADIX];
     if ((int)blockIdx.x >= A.sorters) {
         fill_zeros(A);
         return;
     }
-    for (int i = threadIdx.x; i < RADIX; i += STHR) cnt[i] = 0;
-    uint32_t key[TIPT];
-    int pos[TIPT];
-    bool on[TIPT];
-    tile_items(A, key, pos, on);
+    for (int i = threadIdx.x; i < RADIX; i += THR) cnt[i] = 0;
+    uint32_t key[SORT_IPT];
+    int pos[SORT_IPT];
+    bool on[SORT_IPT];
+    tile_items<THR>(A, key, pos, on);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TIPT; ++i)
+    for (int i = 0; i < SORT_IPT; ++i)
         if (on[i]) atomicAdd(&cnt[(key[i] >> A.shift) & (RADIX - 1)], 1);
     __syncthreads();
-    for (int i = threadIdx.x; i < RADIX; i += STHR) gp(A.hist)[(int64_t)i * A.tiles + blockIdx.x] = cnt[i];
+    for (int i = threadIdx.x; i < RADIX; i += THR) gp(A.hist)[(int64_t)i * A.tiles + blockIdx.x] = cnt[i];
 }
 
-__global__ __launch_bounds__(STHR) void k_sort_place(SortArgs A) {
-    __shared__ int cnt[SWAVES * RADIX];
-    __shared__ int wsum[SWAVES];
+template <int THR>
+__global__ __launch_bounds__(THR) void k_sort_place(SortArgs A) {
+    constexpr int WAVES = THR / 64, DPT = RADIX > THR ? RADIX / THR : 1;   // digits a thread adds up
+    __shared__ int cnt[WAVES * RADIX];
+    __shared__ int wsum[WAVES];
     if ((int)blockIdx.x >= A.sorters) {
         fill_zeros(A);
         return;
     }
     const int tid = threadIdx.x, w = tid >> 6;
-    for (int i = tid; i < SWAVES * RADIX; i += STHR) cnt[i] = 0;
-    uint32_t key[TIPT];
-    int pos[TIPT], rank[TIPT];
-    bool on[TIPT];
-    tile_items(A, key, pos, on);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < TIPT; ++i) rank[i] = wave_rank((key[i] >> A.shift) & (RADIX - 1), on[i], (volatile LDSP int*)cnt + w * RADIX);
+    for (int i = tid; i < WAVES * RADIX; i += THR) cnt[i] = 0;
+    uint32_t key[SORT_IPT];
+    int pos[SORT_IPT], rank[SORT_IPT];
+    bool on[SORT_IPT];
+    tile_items<THR>(A, key, pos, on);
     // where this tile's items of digit d go: behind all smaller digits, and
     // behind digit d of the tiles before
-    int all = 0, mine = 0;
-    if (tid < RADIX)
-        for (int t = 0; t < A.tiles; ++t) {
-            const int c = gp(A.hist)[(int64_t)tid * A.tiles + t];
-            all += c;
-            if (t < (int)blockIdx.x) mine += c;
+    int all[DPT], mine[DPT], sum = 0;
+#pragma unroll
+    for (int k = 0; k < DPT; ++k) {
+        all[k] = mine[k] = 0;
+        const int d = tid * DPT + k;
+        if (d < RADIX) {
+            const MU_GLOBAL int32_t* h = gp(A.hist) + (int64_t)d * A.tiles;
+#pragma unroll 8
+            for (int t = 0; t < A.tiles; ++t) {
+                const int c = h[t];
+                all[k] += c;
+                mine[k] += t < (int)blockIdx.x ? c : 0;
+            }
         }
-    const int to0 = block_scan(all, wsum) + mine;
-    if (tid < RADIX) {
-        int before = to0;
-        for (int k = 0; k < SWAVES; ++k) {
-            const int c = cnt[k * RADIX + tid];
-            cnt[k * RADIX + tid] = before;
-            before += c;
-        }
+        sum += all[k];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < TIPT; ++i)
+    for (int i = 0; i < SORT_IPT; ++i)
+        rank[i] = wave_rank((key[i] >> A.shift) & (RADIX - 1), on[i], (volatile LDSP int*)cnt + w * RADIX);
+    int before = block_scan<THR>(sum, wsum);
+#pragma unroll
+    for (int k = 0; k < DPT; ++k) {
+        const int d = tid * DPT + k;
+        if (d < RADIX) {
+            int to = before + mine[k];
+            for (int i = 0; i < WAVES; ++i) {
+                const int c = cnt[i * RADIX + d];
+                cnt[i * RADIX + d] = to;
+                to += c;
+            }
+        }
+        before += all[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < SORT_IPT; ++i)
         if (on[i]) {
             const int to = cnt[w * RADIX + ((key[i] >> A.shift) & (RADIX - 1))] + rank[i];
             gp(A.key_out)[to] = (int32_t)key[i];
@@ -392,9 +381,39 @@ __device__ __forceinline__ void put_row(const SumArgs& A, int64_t v, int64_t col
 }
 
 constexpr int NTHR_SUM = 256;
-template <typename TR, typename TG>
+// Eight columns of a row as they lie in memory.
+template <typename T> struct Raw8 {
+    bf16x8 q;
+    __device__ __forceinline__ void load(const MU_GLOBAL T* p) { q = *(const MU_GLOBAL bf16x8u*)p; }
+    __device__ __forceinline__ float operator[](int e) const { return (float)q[e]; }
+    __device__ __forceinline__ void set(int e, T v) { q[e] = v; }
+};
+template <> struct Raw8<float> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const MU_GLOBAL float* p) {
+        a = *(const MU_GLOBAL f32x4u*)p;
+        b = *(const MU_GLOBAL f32x4u*)(p + 4);
+    }
+    __device__ __forceinline__ float operator[](int e) const { return e < 4 ? a[e] : b[e - 4]; }
+    __device__ __forceinline__ void set(int e, float v) {
+        if (e < 4) a[e] = v;
+        else b[e - 4] = v;
+    }
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw8<T>& r, const MU_GLOBAL T* p, int cnt) {
+    if (cnt >= 8) r.load(p);
+    else
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.set(e, e < cnt ? p[e] : (T)0.f);
+}
+
+// SUM_U entries at a time: their keys and positions, then all their rows (ACC:
+// and the gradient's rows that the runs ending there are added to) before the
+// first addition. Bound by memory and, with few tokens, by its latency.
+constexpr int SUM_U = 8;
+template <typename TR, typename TG, bool ACC>
 __global__ __launch_bounds__(NTHR_SUM) void k_sum_rows(SumArgs A) {
-    constexpr int U = 8;   // rows in flight
     const int64_t g = ((int64_t)blockIdx.x * NTHR_SUM + threadIdx.x) / A.lanes;
     const int64_t c = g / A.slices;
     if (c >= A.chunks) return;
@@ -406,42 +425,70 @@ __global__ __launch_bounds__(NTHR_SUM) void k_sum_rows(SumArgs A) {
     const MU_GLOBAL int32_t* key = (const MU_GLOBAL int32_t*)A.key;
     const MU_GLOBAL int32_t* pos = (const MU_GLOBAL int32_t*)A.pos;
     const MU_GLOBAL TR* rows = (const MU_GLOBAL TR*)A.e.rows + col;
-    uint32_t cur = (uint32_t)key[i0];
-    if (cur >= vocab) return;
-    bool from_before = i0 > 0 && (uint32_t)key[i0 - 1] == cur;
+    MU_GLOBAL TG* grad = (MU_GLOBAL TG*)A.e.grad + col;
+    MU_GLOBAL float* part = (MU_GLOBAL float*)A.part + c * 2 * A.e.dim + col;
+    const float scale = A.e.scale;
+    // keys of a batch and the one behind it; places past the chunk's end repeat
+    // its last entry and are skipped
+    uint32_t k[SUM_U + 1], kn[SUM_U + 1];
+    int p[SUM_U];
     const uint32_t behind = i1 < A.n ? (uint32_t)key[i1] : 0xffffffffu;
+    auto entries = [&](int i, uint32_t (&kk)[SUM_U + 1]) {
+#pragma unroll
+        for (int u = 0; u < SUM_U; ++u) {
+            const int j = min(i + u, i1 - 1);
+            kk[u] = (uint32_t)key[j];
+            p[u] = pos[j];
+        }
+        kk[SUM_U] = i + SUM_U < i1 ? (uint32_t)key[i + SUM_U] : behind;
+    };
+    const uint32_t ahead = i0 > 0 ? (uint32_t)key[i0 - 1] : 0xffffffffu;
+    entries(i0, k);
+    if (k[0] >= vocab) return;
+    bool from_before = ahead == k[0];
     float s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = 0.f;
-    MU_GLOBAL float* part = (MU_GLOBAL float*)A.part + c * 2 * A.e.dim + col;
-    auto flush = [&](bool goes_on) {
-        if (from_before) store8<float>(part, cnt, s);
-        else if (goes_on) store8<float>(part + A.e.dim, cnt, s);
-        else put_row<TG>(A, cur, col, cnt, s);
-    };
-    for (int i = i0; i < i1; i += U) {
-        uint32_t k[U];
-        float v[U][8];
+    for (int i = i0; i < i1; i += SUM_U) {
+        Raw8<TR> v[SUM_U];
+        Raw8<TG> o[ACC ? SUM_U : 1];
+        // (rows of tokens that add nothing are read too, and skipped)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            k[u] = i + u < i1 ? (uint32_t)key[i + u] : 0xffffffffu;
-            if (k[u] < vocab) load8<TR>(rows + (int64_t)pos[i + u] * A.e.dim, cnt, v[u]);
+        for (int u = 0; u < SUM_U; ++u) load_raw<TR>(v[u], rows + (int64_t)p[u] * A.e.dim, cnt);
+        if constexpr (ACC) {
+#pragma unroll
+            for (int u = 0; u < SUM_U; ++u)
+                if (k[u] < vocab && (u + 1 < SUM_U && i + u + 1 >= i1 ? behind : k[u + 1]) != k[u])
+                    load_raw<TG>(o[u], grad + (int64_t)k[u] * A.e.dim, cnt);
         }
+        entries(i + SUM_U, kn);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (k[u] >= vocab) continue;
-            if (k[u] != cur) {
-                flush(false);
-                cur = k[u];
-                from_before = false;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[e] = 0.f;
-            }
+        for (int u = 0; u < SUM_U; ++u) {
+            if (i + u >= i1 || k[u] >= vocab) break;
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] += v[u][e];
+            const bool end = i + u + 1 >= i1;   // of the chunk
+            const uint32_t next = end ? behind : k[u + 1];
+            if (next == k[u] && !end) continue;
+            // the run ends here, or goes on in the next chunk
+            if (from_before) store8<float>(part, cnt, s);
+            else if (next == k[u]) store8<float>(part + A.e.dim, cnt, s);
+            else {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = scale * s[e];
+                    if constexpr (ACC) x[e] += o[u][e];
+                }
+                store8<TG>(grad + (int64_t)k[u] * A.e.dim, cnt, x);
+            }
+            from_before = false;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = 0.f;
         }
+#pragma unroll
+        for (int u = 0; u <= SUM_U; ++u) k[u] = kn[u];
     }
-    flush(cur == behind);
 }
 
 // Joins the partial sums of the runs that cross chunk borders: a workgroup for
@@ -522,7 +569,7 @@ int check_rowgrad(const mu_rowgrad* e) {
 
 // What a call of these sizes launches and keeps in its workspace.
 struct GradPlan {
-    int n, passes, tiles, chunk, chunks, lanes, slices;
+    int n, bits, passes, thr, tiles, chunk, chunks, lanes, slices;
     size_t off_key[2], off_pos[2], off_hist, off_part, bytes;
 };
 GradPlan grad_plan(const mu_rowgrad* e) {
@@ -530,8 +577,11 @@ GradPlan grad_plan(const mu_rowgrad* e) {
     p.n = (int)e->n_tokens;
     int bits = 1;
     while (bits < 32 && (e->vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
+    p.bits = bits;
     p.passes = (bits + DIGIT - 1) / DIGIT;
-    p.tiles = p.n <= SORT_ONE ? 1 : (p.n + SORT_TILE - 1) / SORT_TILE;
+    // small tiles while they are few: every tile reads all tiles' counts
+    p.thr = p.n <= (1 << 18) ? 256 : 1024;
+    p.tiles = p.n <= SORT_RANK ? 0 : (p.n + p.thr * SORT_IPT - 1) / (p.thr * SORT_IPT);
     // short chunks while tokens are few (more waves), longer ones as their
     // partial sums would pass 64 MB
     p.chunk = 16;
@@ -547,11 +597,11 @@ GradPlan grad_plan(const mu_rowgrad* e) {
         return at;
     };
     for (int k = 0; k < 2; ++k) {
-        const size_t n = k == 0 || p.tiles > 1 ? sizeof(int32_t) * (size_t)p.n : 0;
+        const size_t n = k == 0 || p.tiles > 0 ? sizeof(int32_t) * (size_t)p.n : 0;
         p.off_key[k] = take(n);
         p.off_pos[k] = take(n);
     }
-    p.off_hist = take(p.tiles > 1 ? sizeof(int32_t) * RADIX * (size_t)p.tiles : 0);
+    p.off_hist = take(p.tiles > 0 ? sizeof(int32_t) * RADIX * (size_t)p.tiles : 0);
     p.off_part = take(p.chunks > 1 ? sizeof(float) * 2 * (size_t)p.chunks * (size_t)e->dim : 0);
     p.bytes = o;
     return p;
@@ -560,7 +610,9 @@ GradPlan grad_plan(const mu_rowgrad* e) {
 template <typename TR, typename TG>
 hipError_t launch_sum(const SumArgs& a, hipStream_t s) {
     const int64_t groups = (int64_t)a.chunks * a.slices, per = NTHR_SUM / a.lanes;
-    hipLaunchKernelGGL((k_sum_rows<TR, TG>), dim3((unsigned)((groups + per - 1) / per)), dim3(NTHR_SUM), 0, s, a);
+    const dim3 grid((unsigned)((groups + per - 1) / per));
+    if (a.e.accumulate) hipLaunchKernelGGL((k_sum_rows<TR, TG, true>), grid, dim3(NTHR_SUM), 0, s, a);
+    else hipLaunchKernelGGL((k_sum_rows<TR, TG, false>), grid, dim3(NTHR_SUM), 0, s, a);
     return hipGetLastError();
 }
 
@@ -569,10 +621,10 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
     const size_t er = es_of(e->row_dtype), eg = es_of(e->grad_dtype);
     // zeros in equal shares of the sorting launches (a multiple of 16 bytes each)
     const int64_t zeros = e->accumulate ? 0 : e->vocab * e->dim * (int64_t)eg;
-    const int launches = p.n == 0 ? 1 : p.tiles == 1 ? 1 : 2 * p.passes;
+    const int launches = p.tiles == 0 ? 1 : 2 * p.passes;
     const int64_t share = (zeros / launches + 15) / 16 * 16;
     int done = 0;
-    auto sort_launch = [&](void (*kernel)(SortArgs), SortArgs a, int sorters, double bytes) {
+    auto sort_launch = [&](void (*kernel)(SortArgs), SortArgs a, int sorters, int thr, size_t lds, double bytes) {
         const int64_t from = std::min(zeros, share * done), to = done + 1 == launches ? zeros : std::min(zeros, share * (done + 1));
         ++done;
         a.fill = (char*)e->grad + from;
@@ -581,7 +633,7 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
         const int64_t grid = sorters + (a.fill_bytes + FILL_WG - 1) / FILL_WG;
         if (grid == 0) return (int)MU_OK;
         return timed_launch(MU_K_ROWGRAD, 0.0, bytes + (double)a.fill_bytes, s, [&] {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(STHR), 0, s, a);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(thr), lds, s, a);
             return hipGetLastError();
         }, "embedding gradient sort launch");
     };
@@ -589,13 +641,19 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
     a.e = *e;
     a.n = p.n;
     a.tiles = p.tiles;
-    a.passes = p.passes;
     a.hist = (int32_t*)(ws + p.off_hist);
     int out = 0;   // the buffer that holds the sorted keys at the end
-    if (p.tiles == 1) {
+    if (p.tiles == 0) {
         a.key_out = (int32_t*)(ws + p.off_key[0]);
         a.pos_out = (int32_t*)(ws + p.off_pos[0]);
-        const int rc = sort_launch(k_sort_one, a, p.n > 0 ? 1 : 0, (double)p.n * (e->token_bits / 8 + 8));
+        while ((1 << a.index_bits) < p.n) ++a.index_bits;
+        const int groups = (p.n + RANK_ITEMS - 1) / RANK_ITEMS;
+        const size_t words = ((size_t)p.n + RANK_PARTS - 1) / RANK_PARTS + 3;
+        // the largest word, the padding of the last eighth, must stay above all
+        const bool small = p.bits + a.index_bits < 32;
+        const size_t lds = p.n == 0 ? 0 : words / 4 * 4 * RANK_PARTS * (small ? 4 : 8);
+        const int rc = sort_launch(small ? k_sort_rank<uint32_t> : k_sort_rank<uint64_t>, a, groups, RANK_THR, lds,
+                                   (double)p.n * (e->token_bits / 8 + 8));
         if (rc) return rc;
     } else {
         for (int k = 0; k < p.passes; ++k) {
@@ -604,9 +662,10 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
             a.pos_in = k == 0 ? nullptr : (const int32_t*)(ws + p.off_pos[out ^ 1]);
             a.key_out = (int32_t*)(ws + p.off_key[out]);
             a.pos_out = (int32_t*)(ws + p.off_pos[out]);
-            int rc = sort_launch(k_sort_count, a, p.tiles, 8.0 * p.n);
+            const bool few = p.thr == 256;
+            int rc = sort_launch(few ? k_sort_count<256> : k_sort_count<1024>, a, p.tiles, p.thr, 0, 8.0 * p.n);
             if (rc) return rc;
-            rc = sort_launch(k_sort_place, a, p.tiles, 16.0 * p.n);
+            rc = sort_launch(few ? k_sort_place<256> : k_sort_place<1024>, a, p.tiles, p.thr, 0, 16.0 * p.n);
             if (rc) return rc;
             out ^= 1;
         }
