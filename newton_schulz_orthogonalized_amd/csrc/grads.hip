@@ -24,6 +24,7 @@ namespace {
 constexpr int NTHR = 256;
 constexpr int GRAD_CHUNK = 8192;    // elements a workgroup takes at a time
 constexpr int SQ_WGS = 1024;        // workgroups (and float64 partial sums) of one launch
+constexpr int CLIP_WGS = 512;
 
 // A tensor's elements; chunk c of the launch belongs to the last segment with c0 <= c.
 struct SqSeg {
@@ -105,89 +106,191 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
     return s;
 }
 
+// Sum of squares of a chunk (elements i0 .. of a tensor of n). Squares of
+// float32 values are exact in float64, whose additions hide behind the loads.
+// Bound by memory: every load of a chunk is in flight before the first square,
+// and non-temporal (Llama-1B-shaped set, 2.68 GB of bfloat16: 529 us with loads
+// as they come, 440 with all of a chunk's first, 393 non-temporal, 6.8 TB/s; one
+// run of chunks for each XCD 414-418, 2048 workgroups 432).
 template <typename T>
-__device__ double sumsq_chunk(const void* base, int64_t i0, int64_t n) {
-    const MU_GLOBAL T* p = (const MU_GLOBAL T*)base;
+__device__ __forceinline__ double sumsq_chunk(const void* base, int64_t i0, int64_t n, int tid) {
+    const MU_GLOBAL T* p = (const MU_GLOBAL T*)base + i0;
+    constexpr int EPV = 16 / (int)sizeof(T), STEPS = GRAD_CHUNK / (NTHR * EPV);
+    typedef T V __attribute__((ext_vector_type(EPV)));
+    typedef V VU __attribute__((aligned(sizeof(T))));
     double s = 0.0;
-    for (int64_t i = i0 + threadIdx.x * 8; i < min<int64_t>(n, i0 + GRAD_CHUNK); i += NTHR * 8) {
-        float v[8];
-        if (i + 8 <= n) load8<T>(p + i, v);
-        else
-            for (int e = 0; e < 8; ++e) v[e] = i + e < n ? to_f32<T>(p[i + e]) : 0.f;
+    const int64_t left = n - i0;
+    if (left >= GRAD_CHUNK) {
+        V v[STEPS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s = fma((double)v[e], (double)v[e], s);
+        for (int k = 0; k < STEPS; ++k)
+            v[k] = __builtin_nontemporal_load((const MU_GLOBAL VU*)(p + (k * NTHR + tid) * EPV));
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                const double x = (double)(float)v[k][e];
+                s = fma(x, x, s);
+            }
+        return s;
+    }
+    for (int i = tid * EPV; i < (int)left; i += NTHR * EPV) {
+        V v;
+        if (i + EPV <= left) v = *(const MU_GLOBAL VU*)(p + i);
+        else
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) v[e] = i + e < left ? p[i + e] : (T)0.f;
+#pragma unroll
+        for (int e = 0; e < EPV; ++e) {
+            const double x = (double)(float)v[e];
+            s = fma(x, x, s);
+        }
     }
     return s;
+}
+
+// The segment of chunk c: the last one that starts at or before it, found by
+// all lanes of a wave at once.
+template <typename Seg>
+__device__ __forceinline__ int seg_of(const Seg* seg, int n, int c) {
+    int before = 0;
+    for (int j = 0; j < n; j += 64) {
+        const int k = j + (int)(threadIdx.x & 63);
+        before += __popcll(__ballot(k < n && seg[min(k, n - 1)].c0 <= c));
+    }
+    return __builtin_amdgcn_readfirstlane(before - 1);
+}
+
+__device__ __forceinline__ double sumsq_of(const SqSeg& S, int c, int tid) {
+    const int64_t i0 = (int64_t)(c - S.c0) * GRAD_CHUNK;
+    return S.dtype == DT_BF16 ? sumsq_chunk<bf16>(S.p, i0, S.n, tid) : sumsq_chunk<float>(S.p, i0, S.n, tid);
 }
 
 __global__ __launch_bounds__(NTHR) void k_sumsq(SqArgs A) {
     __shared__ double red[4];
     double s = 0.0;
-    int i = 0;
+    int i = (int)blockIdx.x < A.chunks ? seg_of(A.seg, A.nseg, blockIdx.x) : 0;
     for (int c = blockIdx.x; c < A.chunks; c += gridDim.x) {
         while (i + 1 < A.nseg && A.seg[i + 1].c0 <= c) ++i;
-        const int64_t i0 = (int64_t)(c - A.seg[i].c0) * GRAD_CHUNK;
-        if (A.seg[i].dtype == DT_BF16) s += sumsq_chunk<bf16>(A.seg[i].p, i0, A.seg[i].n);
-        else s += sumsq_chunk<float>(A.seg[i].p, i0, A.seg[i].n);
+        s += sumsq_of(A.seg[i], c, threadIdx.x);
     }
     s = block_sum(s, red);
     if (threadIdx.x == 0) gp(A.partials)[blockIdx.x] = s;
 }
 
-// The sum of the partials in a fixed order, by every thread of a workgroup;
-// norm and c are written by the workgroup that `writes`. Returns c.
-__device__ float finish_norm(const NormOut& N, bool writes, double* red) {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < N.n; i += NTHR) s += gp(N.partials)[i];
-    s = block_sum(s, red);
+// norm and c from the sum of squares; written where `writes`. Returns c.
+__device__ __forceinline__ float norm_out(const NormOut& N, double s, bool writes) {
     const double norm = sqrt(s);
     const double r = (double)N.max_norm / (norm + (double)N.eps);
     // 0 / 0 (both bounds 0 and no gradient) clips nothing; a NaN norm stays NaN
     const float c = isnan(norm) ? (float)norm : (r < 1.0 ? (float)r : 1.f);
-    if (writes && threadIdx.x == 0) {
+    if (writes) {
         if (N.norm) *gp(N.norm) = (float)norm;
         if (N.scale) *gp(N.scale) = c;
     }
     return c;
 }
 
-__global__ __launch_bounds__(NTHR) void k_norm_final(NormOut N) {
-    __shared__ double red[4];
-    finish_norm(N, true, red);
+// The sum of the partials in a fixed order, by every thread of a workgroup.
+__device__ __forceinline__ double sum_partials(const NormOut& N, double* red) {
+    double s = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < N.n; i += NTHR) s += gp(N.partials)[i];
+    return block_sum(s, red);
 }
 
+__global__ __launch_bounds__(NTHR) void k_norm_final(NormOut N) {
+    __shared__ double red[4];
+    norm_out(N, sum_partials(N, red), threadIdx.x == 0);
+}
+
+// A chunk times c, all loads before the first store. Bound by memory: four layers
+// and the embedding of the Llama-1B-shaped set, float32 into bfloat16, norm and
+// scaling together (2.7 GB): 478 us, 461 with the loads first, 429 with
+// non-temporal loads and stores, 417 with CLIP_WGS = 512 rather than 1024
+// workgroups; going through the chunks backwards, last read first, gained nothing.
 template <typename TI, typename TO>
-__device__ void clip_chunk(const void* base, void* out, int64_t i0, int64_t n, float c) {
-    const MU_GLOBAL TI* p = (const MU_GLOBAL TI*)base;
-    MU_GLOBAL TO* o = (MU_GLOBAL TO*)out;
-    for (int64_t i = i0 + threadIdx.x * 8; i < min<int64_t>(n, i0 + GRAD_CHUNK); i += NTHR * 8) {
-        if (i + 8 <= n) {
-            float v[8];
-            load8<TI>(p + i, v);
+__device__ __forceinline__ void clip_chunk(const void* base, void* out, int64_t i0, int64_t n, float c, int tid) {
+    const MU_GLOBAL TI* p = (const MU_GLOBAL TI*)base + i0;
+    MU_GLOBAL TO* o = (MU_GLOBAL TO*)out + i0;
+    constexpr int EPV = sizeof(TI) == 2 && sizeof(TO) == 2 ? 8 : 4, STEPS = GRAD_CHUNK / (NTHR * EPV);
+    typedef TI VI __attribute__((ext_vector_type(EPV)));
+    typedef TO VO __attribute__((ext_vector_type(EPV)));
+    typedef VI VIU __attribute__((aligned(sizeof(TI))));
+    typedef VO VOU __attribute__((aligned(sizeof(TO))));
+    const int64_t left = n - i0;
+    if (left >= GRAD_CHUNK) {
+        VI v[STEPS];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= c;
-            store8<TO>(o + i, v);
-        } else {
-            for (int64_t j = i; j < n; ++j) o[j] = from_f32<TO>(c * to_f32<TI>(p[j]));
+        for (int k = 0; k < STEPS; ++k) v[k] = __builtin_nontemporal_load((const MU_GLOBAL VIU*)(p + (k * NTHR + tid) * EPV));
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+            VO r;
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) r[e] = (TO)(c * (float)v[k][e]);
+            __builtin_nontemporal_store(r, (MU_GLOBAL VOU*)(o + (k * NTHR + tid) * EPV));
         }
+        return;
+    }
+    for (int i = tid * EPV; i < (int)left; i += NTHR * EPV) {
+        if (i + EPV <= left) {
+            const VI v = *(const MU_GLOBAL VIU*)(p + i);
+            VO r;
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) r[e] = (TO)(c * (float)v[e]);
+            *(MU_GLOBAL VOU*)(o + i) = r;
+        } else {
+            for (int j = i; j < (int)left; ++j) o[j] = (TO)(c * (float)p[j]);
+        }
+    }
+}
+
+__device__ __forceinline__ void clip_of(const ClipSeg& S, int q, float c, int tid) {
+    if (c == 1.f && S.p == S.out) return;   // in place and nothing to clip
+    const int64_t i0 = (int64_t)(q - S.c0) * GRAD_CHUNK;
+    if (S.dtype == DT_BF16) {
+        if (S.out_dtype == DT_BF16) clip_chunk<bf16, bf16>(S.p, S.out, i0, S.n, c, tid);
+        else clip_chunk<bf16, float>(S.p, S.out, i0, S.n, c, tid);
+    } else {
+        if (S.out_dtype == DT_BF16) clip_chunk<float, bf16>(S.p, S.out, i0, S.n, c, tid);
+        else clip_chunk<float, float>(S.p, S.out, i0, S.n, c, tid);
     }
 }
 
 __global__ __launch_bounds__(NTHR) void k_clip(ClipArgs A) {
     __shared__ double red[4];
-    const float c = finish_norm(A.no, blockIdx.x == 0, red);
-    int i = 0;
+    int i = (int)blockIdx.x < A.chunks ? seg_of(A.seg, A.nseg, blockIdx.x) : 0;
+    const float c = norm_out(A.no, sum_partials(A.no, red), blockIdx.x == 0 && threadIdx.x == 0);
     for (int q = blockIdx.x; q < A.chunks; q += gridDim.x) {
         while (i + 1 < A.nseg && A.seg[i + 1].c0 <= q) ++i;
-        const ClipSeg& S = A.seg[i];
-        if (c == 1.f && S.p == S.out) continue;   // in place and nothing to clip
-        const int64_t i0 = (int64_t)(q - S.c0) * GRAD_CHUNK;
-        if (S.dtype == DT_BF16) {
-            if (S.out_dtype == DT_BF16) clip_chunk<bf16, bf16>(S.p, S.out, i0, S.n, c);
-            else clip_chunk<bf16, float>(S.p, S.out, i0, S.n, c);
-        } else {
-            if (S.out_dtype == DT_BF16) clip_chunk<float, bf16>(S.p, S.out, i0, S.n, c);
-            else clip_chunk<float, float>(S.p, S.out, i0, S.n, c);
+        const ClipSeg S = A.seg[i];
+        clip_of(S, q, c, threadIdx.x);
+    }
+}
+
+// A few chunks in one launch of one workgroup: its four quarters take a chunk
+// each at a time, and for clipping read theirs again from the caches.
+constexpr int FEW_CHUNKS = 16, FEW_THR = 4 * NTHR;
+template <bool CLIP>
+__global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
+    __shared__ double red[FEW_THR / 64];
+    const int tid = threadIdx.x % NTHR, quarter = __builtin_amdgcn_readfirstlane(threadIdx.x / NTHR);
+    double s = 0.0;
+    for (int q = quarter; q < A.chunks; q += 4) {
+        const ClipSeg& S = A.seg[seg_of(A.seg, A.nseg, q)];
+        s += sumsq_of(SqSeg{S.p, S.n, S.c0, S.dtype}, q, tid);
+    }
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < FEW_THR / 64; ++w) s += red[w];
+    const float c = norm_out(A.no, s, threadIdx.x == 0);
+    if constexpr (CLIP) {
+        for (int q = quarter; q < A.chunks; q += 4) {
+            const ClipSeg S = A.seg[seg_of(A.seg, A.nseg, q)];
+            clip_of(S, q, c, tid);
         }
     }
 }
@@ -240,9 +343,11 @@ int batches(const mu_grad* gs, int32_t n, int segs, std::vector<Batch>& out) {
     return MU_OK;
 }
 
+// Workgroups of a launch over so many chunks: a multiple of 8, so that every XCD has some.
+int wgs_of(int64_t chunks, int most) { return (int)std::min<int64_t>((chunks + 7) / 8 * 8, most); }
 size_t partials_of(const std::vector<Batch>& b) {
     size_t p = 0;
-    for (auto& x : b) p += (size_t)std::min<int64_t>(x.chunks, SQ_WGS);
+    for (auto& x : b) p += (size_t)wgs_of(x.chunks, SQ_WGS);
     return p;
 }
 
@@ -263,6 +368,29 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
         if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
     }
+    auto clip_args = [&](const Batch& b, ClipArgs& a) {
+        double bytes = 0;
+        int64_t c = 0;
+        a.nseg = (int)b.items.size();
+        for (int k = 0; k < a.nseg; ++k) {
+            const mu_grad& g = gs[b.items[k]];
+            a.seg[k] = ClipSeg{g.grad, g.out, g.numel, (int32_t)c, (int16_t)g.dtype, (int16_t)g.out_dtype};
+            c += chunks_of(g.numel);
+            bytes += (double)g.numel * (es_of(g.dtype) + (clip ? es_of(g.out_dtype) : 0));
+        }
+        a.chunks = (int)c;
+        return bytes;
+    };
+    if (bs.size() == 1 && bs[0].chunks <= FEW_CHUNKS && bs[0].items.size() <= (size_t)CLIP_SEGS) {
+        ClipArgs a;
+        const double bytes = clip_args(bs[0], a);
+        a.no = NormOut{nullptr, 0, max_norm, eps, norm_out, scale_out};
+        return timed_launch(clip ? MU_K_CLIP : MU_K_GRADNORM, 0.0, bytes, s, [&] {
+            if (clip) hipLaunchKernelGGL(k_few<true>, dim3(1), dim3(FEW_THR), 0, s, a);
+            else hipLaunchKernelGGL(k_few<false>, dim3(1), dim3(FEW_THR), 0, s, a);
+            return hipGetLastError();
+        }, "gradient norm launch");
+    }
     double* part = (double*)ws;
     for (auto& b : bs) {
         SqArgs a;
@@ -277,7 +405,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         }
         a.chunks = (int)c;
         a.partials = part;
-        const int grid = (int)std::min<int64_t>(c, SQ_WGS);
+        const int grid = wgs_of(c, SQ_WGS);
         part += grid;
         rc = timed_launch(MU_K_GRADNORM, 0.0, bytes, s, [&] {
             hipLaunchKernelGGL(k_sumsq, dim3(grid), dim3(NTHR), 0, s, a);
@@ -297,18 +425,9 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
     if (rc) return rc;
     for (auto& b : bs) {
         ClipArgs a;
-        double bytes = 0;
-        int64_t c = 0;
+        const double bytes = clip_args(b, a);
         a.no = no;
-        a.nseg = (int)b.items.size();
-        for (int k = 0; k < a.nseg; ++k) {
-            const mu_grad& g = gs[b.items[k]];
-            a.seg[k] = ClipSeg{g.grad, g.out, g.numel, (int32_t)c, (int16_t)g.dtype, (int16_t)g.out_dtype};
-            c += chunks_of(g.numel);
-            bytes += (double)g.numel * (es_of(g.dtype) + es_of(g.out_dtype));
-        }
-        a.chunks = (int)c;
-        const int grid = (int)std::min<int64_t>(c, SQ_WGS);
+        const int grid = wgs_of(a.chunks, CLIP_WGS);
         rc = timed_launch(MU_K_CLIP, 0.0, bytes, s, [&] {
             hipLaunchKernelGGL(k_clip, dim3(grid), dim3(NTHR), 0, s, a);
             return hipGetLastError();
