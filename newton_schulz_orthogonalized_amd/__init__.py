@@ -15,9 +15,10 @@ __all__ = [*_CALLS, "MuonAdamW", "split_params"]
 
 def __getattr__(name):
     if name in _CALLS:
-        from . import api
-        return getattr(api, name)
-    if name in ("MuonAdamW", "split_params"):
-        from . import optim
-        return getattr(optim, name)
-    raise AttributeError(name)
+        from . import api as mod
+    elif name in ("MuonAdamW", "split_params"):
+        from . import optim as mod
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(mod, name)   # found without this function from now on
+    return value

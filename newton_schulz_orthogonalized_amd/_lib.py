@@ -10,6 +10,7 @@ loudly when the shared library is missing.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 from typing import Optional, Sequence
@@ -362,50 +363,60 @@ def mu_adamw_step_scaled(ts, n, beta1: float, beta2: float, eps: float, step: in
     _check(LIB.mu_adamw_step_scaled(ts, n, ctypes.byref(hp), grad_scale_ptr(grad_scale), ws, nb, _stream(stream)))
 
 
-def device_of(tensors, what: str) -> torch.device:
-    """The one GPU that all of `tensors` (None entries aside) live on."""
+def device_of(tensors, what: str) -> int:
+    """The index of the one GPU that all of `tensors` (None entries aside) live
+    on; the current one where there is none."""
     dev = None
     for t in tensors:
         if t is None:
             continue
+        d = t.get_device()
         if dev is None:
-            dev = t.device
-            if dev.type != "cuda":
-                raise ValueError(f"{what} must be on a GPU (got a tensor on {dev})")
-        elif t.device != dev:
-            raise ValueError(f"{what} must share one device (got {dev} and {t.device})")
-    return dev
+            dev = d
+            if d < 0:
+                raise ValueError(f"{what} must be on a GPU (got a tensor on {t.device})")
+        elif d != dev:
+            raise ValueError(f"{what} must share one device (got GPU {dev} and {t.device})")
+    return torch.cuda.current_device() if dev is None else dev
+
+
+def scratch(nbytes: int, device: int) -> Optional[torch.Tensor]:
+    """workspace() without the slice where the allocator's address will do."""
+    if nbytes == 0:
+        return None
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    return buf if buf.data_ptr() % 256 == 0 else workspace(nbytes, buf.device)
 
 
 _CODES = {torch.float32: MU_F32, torch.bfloat16: MU_BF16}
+_Tensor = torch._C.TensorBase
+
+
+def _list_of(tensors, what: str):
+    """Addresses, sizes and type codes of a list, in a few passes of C speed (a
+    list may hold hundreds of tensors)."""
+    try:
+        codes = [_CODES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]}") from None
+    if not all(map(_Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{what} must be contiguous (the library takes dense row-major buffers)")
+    return list(map(_Tensor.data_ptr, tensors)), list(map(_Tensor.numel, tensors)), codes
 
 
 def gradients(grads, outs=None):
-    """(mu_grad list as packed bytes, n): a list of hundreds of tensors is
-    described in one pass, without a ctypes object each."""
+    """(mu_grad list as packed bytes, n)."""
     n = len(grads)
-    if outs is not None and len(outs) != n:
-        raise ValueError("outs must have one tensor for each gradient")
-    vals = []
-    for i, g in enumerate(grads):
-        code = _CODES.get(g.dtype)
-        if code is None:
-            raise TypeError(f"unsupported dtype {g.dtype}")
-        if not g.is_contiguous():
-            raise ValueError("gradient must be contiguous (the library takes dense row-major buffers)")
-        if outs is None:
-            vals += (g.data_ptr(), 0, g.numel(), code, code)
-            continue
-        o = outs[i]
-        oc = _CODES.get(o.dtype)
-        if oc is None:
-            raise TypeError(f"unsupported dtype {o.dtype}")
-        if not o.is_contiguous():
-            raise ValueError("output must be contiguous (the library takes dense row-major buffers)")
-        if o.shape != g.shape:
+    ptrs, sizes, codes = _list_of(grads, "gradient")
+    if outs is None:
+        optrs, ocodes = [0] * n, codes
+    else:
+        if len(outs) != n:
+            raise ValueError("outs must have one tensor for each gradient")
+        optrs, _, ocodes = _list_of(outs, "output")
+        if outs is not grads and [o.shape for o in outs] != [g.shape for g in grads]:
             raise ValueError("each output must have its gradient's shape")
-        vals += (g.data_ptr(), o.data_ptr(), g.numel(), code, oc)
-    return struct.pack("=" + "QQqii" * n, *vals), n
+    return struct.pack("=" + "QQqii" * n, *itertools.chain.from_iterable(zip(ptrs, optrs, sizes, codes, ocodes))), n
 
 
 def mu_grad_norm_workspace_size(gs, n) -> int:

@@ -12,7 +12,6 @@ kernels still read it. Nothing here computes.
 
 from __future__ import annotations
 
-import contextlib
 import math
 from typing import Optional, Sequence
 
@@ -118,15 +117,26 @@ def qk_clip(wqs, wks, max_logits, *, q_heads, k_heads, tau: float = 100.0, gamma
     _lib.mu_qk_clip(pairs, n, tau, workspace, stream)
 
 
-@contextlib.contextmanager
-def _on(device: torch.device, stream):
-    """Make the tensors' device current and give the stream to launch on: the
-    caller's, or the current one of that device."""
-    if device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream(device) if stream is None else stream
-    else:
+def _on(device: int, stream, call, *args):
+    """call(stream, *args) with GPU `device` current; the stream is the caller's
+    or the device's current one (as its handle: a torch.cuda.Stream object costs
+    more to make than a small kernel to run)."""
+    if device != torch.cuda.current_device():
         with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device) if stream is None else stream
+            return _on(device, stream, call, *args)
+    return call(torch._C._cuda_getCurrentRawStream(device) if stream is None else stream, *args)
+
+
+def _new(shape, dtype, device: int, stream) -> torch.Tensor:
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
+    _lib.tie_to_stream(t, stream)
+    return t
+
+
+def _scratch(nbytes: int, device: int, stream) -> Optional[torch.Tensor]:
+    buf = _lib.scratch(nbytes, device)
+    _lib.tie_to_stream(buf, stream)
+    return buf
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float = math.inf, eps: float = 1e-6,
@@ -149,25 +159,22 @@ def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, outs: Optional
 
 
 def _norm(grads, outs, max_norm, eps, norm_out, scale_out, workspace, stream):
-    grads = list(grads)
+    if not isinstance(grads, (list, tuple)):
+        raise TypeError("grads must be a list or tuple of tensors")
     gs, n = _lib.gradients(grads, outs)
     for t in (norm_out, scale_out):
         if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
             raise TypeError("norm_out and scale_out must be one float32 element")
-    known = grads + ([] if outs is None or outs is grads else list(outs)) + [norm_out, scale_out, workspace]
-    device = _lib.device_of(known, "gradients and outputs")
-    if device is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    with _on(device, stream) as st:
-        if norm_out is None:
-            norm_out = torch.empty((), dtype=torch.float32, device=device)
-            _lib.tie_to_stream(norm_out, st)
-        if workspace is None:
-            workspace = _lib.workspace(_lib.mu_grad_norm_workspace_size(gs, n), device)
-            _lib.tie_to_stream(workspace, st)
-        call = _lib.mu_grad_norm if outs is None else _lib.mu_clip_grads
-        call(gs, n, float(max_norm), float(eps), norm_out, scale_out, workspace, st)
-    return norm_out
+    others = () if outs is None or outs is grads else outs
+    device = _lib.device_of((*grads, *others, norm_out, scale_out, workspace), "gradients and outputs")
+
+    def call(st):
+        out = _new((), torch.float32, device, stream) if norm_out is None else norm_out
+        ws = _scratch(_lib.mu_grad_norm_workspace_size(gs, n), device, stream) if workspace is None else workspace
+        run = _lib.mu_grad_norm if outs is None else _lib.mu_clip_grads
+        run(gs, n, max_norm, eps, out, scale_out, ws, st)
+        return out
+    return _on(device, stream, call)
 
 
 def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0, padding_idx: Optional[int] = None,
@@ -187,12 +194,12 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0,
 
 def _lookup(tokens, weight, scale, out, stream):
     device = _lib.device_of((tokens, weight, out), "tokens, weight and out")
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty(tokens.shape + weight.shape[1:], dtype=weight.dtype, device=device)
-            _lib.tie_to_stream(out, st)
-        _lib.mu_embedding(_lib.lookup(tokens, weight, out, scale), st)
-    return out
+
+    def call(st):
+        o = _new(tokens.shape + weight.shape[1:], weight.dtype, device, stream) if out is None else out
+        _lib.mu_embedding(_lib.lookup(tokens, weight, o, scale), st)
+        return o
+    return _on(device, stream, call)
 
 
 class _Embedding(torch.autograd.Function):
@@ -228,16 +235,16 @@ def embedding_grad(tokens: torch.Tensor, rows: torch.Tensor, num_embeddings: int
     if out is not None and dtype is not None and out.dtype != dtype:
         raise TypeError("dtype differs from out's")
     device = _lib.device_of((tokens, rows, out, workspace), "tokens, rows and out")
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty(num_embeddings, rows.shape[-1], dtype=rows.dtype if dtype is None else dtype, device=device)
-            _lib.tie_to_stream(out, st)
-        e = _lib.rowgrad(tokens, rows, out, scale, padding_idx, accumulate)
-        if workspace is None:
-            workspace = _lib.workspace(_lib.mu_embedding_grad_workspace_size(e), device)
-            _lib.tie_to_stream(workspace, st)
-        _lib.mu_embedding_grad(e, workspace, st)
-    return out
+
+    def call(st):
+        g = out
+        if g is None:
+            g = _new((num_embeddings, rows.shape[-1]), rows.dtype if dtype is None else dtype, device, stream)
+        e = _lib.rowgrad(tokens, rows, g, scale, padding_idx, accumulate)
+        ws = _scratch(_lib.mu_embedding_grad_workspace_size(e), device, stream) if workspace is None else workspace
+        _lib.mu_embedding_grad(e, ws, st)
+        return g
+    return _on(device, stream, call)
 
 
 def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = None, causal: bool = True,
@@ -263,13 +270,11 @@ def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = 
     if k_lengths is None:
         k_lengths = lengths
     device = _lib.device_of((q, k, lengths, k_lengths, cu_seqlens, cu_seqlens_k, out, workspace), "q, k, lengths and out")
-    with _on(device, stream) as st:
-        if out is None:
-            out = torch.empty(q.shape[-2], dtype=torch.float32, device=device)
-            _lib.tie_to_stream(out, st)
-        a = _lib.qk_logits(q, k, out, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k, accumulate)
-        if workspace is None:
-            workspace = _lib.workspace(_lib.mu_qk_max_logits_workspace_size(a), device)
-            _lib.tie_to_stream(workspace, st)
-        _lib.mu_qk_max_logits(a, workspace, st)
-    return out
+
+    def call(st):
+        o = _new(q.shape[-2:-1], torch.float32, device, stream) if out is None else out
+        a = _lib.qk_logits(q, k, o, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k, accumulate)
+        ws = _scratch(_lib.mu_qk_max_logits_workspace_size(a), device, stream) if workspace is None else workspace
+        _lib.mu_qk_max_logits(a, ws, st)
+        return o
+    return _on(device, stream, call)

@@ -158,7 +158,7 @@ class MuonAdamW(torch.optim.Optimizer):
             return
         grads = list(self._grads.values())
         gs, n = _lib.gradients(grads)
-        dev = _lib.device_of(grads, "gradients")
+        dev = torch.device("cuda", _lib.device_of(grads, "gradients"))
         self._scale = torch.empty((), dtype=torch.float32, device=dev)
         self.grad_norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = self._ws(("norm",), _lib.mu_grad_norm_workspace_size(gs, n), dev)
