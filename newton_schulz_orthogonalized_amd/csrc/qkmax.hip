@@ -25,7 +25,8 @@ namespace {
 constexpr int NTHR = 256;
 
 #define LDSP __attribute__((address_space(3)))
-// s_waitcnt with vmcnt(n) and lgkmcnt(0) (gfx9 encoding)
+// s_waitcnt with vmcnt(n); with vmcnt(n) and lgkmcnt(0) (gfx9 encoding)
+#define MU_WAIT_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
 #define MU_WAIT_VMCNT_LGKM0(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (0 << 8) | (((n) >> 4) << 14))
 constexpr int BUF_RAW32 = 0x00020000;   // word 3 of a raw buffer resource
 
@@ -181,7 +182,7 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 
 // Logits of a query tile against a stream of key tiles. Four waves of MT * 32
 // queries each keep their queries in registers (the left operand of every
-// product); the keys pass through a ring of three LDS slots of BN rows, read as
+// product); the keys pass through a ring of four LDS slots of BN rows, read as
 // right operands by all four. Nothing but a running maximum leaves the matrix
 // instructions, one max3 for two logits.
 //
@@ -208,7 +209,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     constexpr int TB = BN * ROWB, NB = BN / 32;
     constexpr int PD = NK <= 8 ? NK : NK % 8 == 0 ? 8 : 6;
     static_assert(NK % PD == 0, "a column block is whole rounds of the operand ring");
-    __shared__ __align__(256) char s0[TB], s1[TB], s2[TB];
+    __shared__ __align__(256) char s0[TB], s1[TB], s2[TB], s3[TB];
     __shared__ int red[4];
     const mu_qk_logits& P = A.p;
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, half = lane >> 5;
@@ -239,6 +240,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
             ((LDSP f32x4*)(LDSP char*)s0)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             ((LDSP f32x4*)(LDSP char*)s1)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
             ((LDSP f32x4*)(LDSP char*)s2)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            ((LDSP f32x4*)(LDSP char*)s3)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
         __syncthreads();
     }
@@ -358,11 +360,13 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
 #pragma unroll
                 for (int e = 0; e < 16; e += 2) best = absmax3(c[m][e], c[m][e + 1], best);
         };
-        // Makes tile kt readable (slot kt % 3) and sends for tile kt + 2, whose
-        // slot tile kt - 1 has left: past the barrier every wave holds what it
-        // read there. The wait leaves the loads of tile kt + 1 in flight.
+        // Makes tile kt readable (slot kt % 4) and sends for tile kt + 2, whose
+        // slot tile kt - 2 has left: a wave that comes here has multiplied what
+        // it read of that tile. The wait leaves the loads of tile kt + 1, and a
+        // direct instance's reads of tile kt - 1, in flight.
         auto advance = [&](char* slot2, int kt) {
-            MU_WAIT_VMCNT_LGKM0(DIRECT ? NL : 0);
+            if constexpr (DIRECT) MU_WAIT_VMCNT(NL);
+            else MU_WAIT_VMCNT_LGKM0(0);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
@@ -408,7 +412,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
                 if (decltype(mask)::value) thr_prev = thr;
             }
         };
-        // Tiles that all of the workgroup's rows see whole go three at a time
+        // Tiles that all of the workgroup's rows see whole go four at a time
         // without a branch in between, then the others. The code keeps to
         // straight runs: where paths meet the compiler forgets which slot a
         // load in flight goes to and waits for all of them before the next read
@@ -419,22 +423,25 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         for (int k = 0; k < PD; ++k) f[k] = operand(s0, 0, k);
         const int nwhole = see >= nkeys ? ntiles : max(see, 0) / BN;
         int kt = 0;
-        for (; kt + 3 <= nwhole; kt += 3) {
-            tile(std::false_type{}, s0, s1, s0, kt);
-            tile(std::false_type{}, s1, s2, s1, kt + 1);
-            tile(std::false_type{}, s2, s0, s2, kt + 2);
+        for (; kt + 4 <= nwhole; kt += 4) {
+            tile(std::false_type{}, s0, s1, s3, kt);
+            tile(std::false_type{}, s1, s2, s0, kt + 1);
+            tile(std::false_type{}, s2, s3, s1, kt + 2);
+            tile(std::false_type{}, s3, s0, s2, kt + 3);
         }
         for (;;) {
             if (kt * BN >= see_last) break;
-            tile(std::true_type{}, s0, s1, s0, kt);
+            tile(std::true_type{}, s0, s1, s3, kt);
             if (++kt * BN >= see_last) break;
-            tile(std::true_type{}, s1, s2, s1, kt);
+            tile(std::true_type{}, s1, s2, s0, kt);
             if (++kt * BN >= see_last) break;
-            tile(std::true_type{}, s2, s0, s2, kt);
+            tile(std::true_type{}, s2, s3, s1, kt);
+            if (++kt * BN >= see_last) break;
+            tile(std::true_type{}, s3, s0, s2, kt);
             ++kt;
         }
         if constexpr (NB > 1) take(std::true_type{}, acc[1], thr_prev);
-        for (; kt < ntiles; ++kt) advance(kt % 3 == 0 ? s0 : kt % 3 == 1 ? s1 : s2, kt + 1);
+        for (; kt < ntiles; ++kt) advance(kt % 4 == 0 ? s3 : kt % 4 == 1 ? s0 : kt % 4 == 2 ? s1 : s2, kt + 1);
         int bits = __float_as_int(best) & 0x7fffffff;
         for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
         if (lane == 0) red[wave] = bits;
@@ -493,10 +500,10 @@ int run_any(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, d
         if (d <= 192) return run<bf16, 192, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
         return run<bf16, 256, 32, 2, 1>(a, prefix, direct, flops, bytes, s);
     }
-    if (d <= 32) return run<float, 32, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 64) return run<float, 64, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 96) return run<float, 96, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 128) return run<float, 128, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 32) return run<float, 32, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 64) return run<float, 64, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 96) return run<float, 96, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 128) return run<float, 128, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
     if (d <= 192) return run<float, 192, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
     return run<float, 256, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
 }
