@@ -139,7 +139,6 @@ __global__ __launch_bounds__(NTHR) void k_lookup(LookupArgs A) {
 // Sort. Keys are table rows, `vocab` for tokens that add nothing.
 // ---------------------------------------------------------------------------
 constexpr int DIGIT = 9, RADIX = 1 << DIGIT;      // two passes up to 2^18 - 1 rows
-constexpr int SORT_RANK = 16384;                  // tokens sorted by counting smaller ones
 constexpr int SORT_IPT = 8;                       // digit passes: tokens a thread
 
 struct SortArgs {
@@ -187,15 +186,18 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs& A, int t) {
 
 // Few tokens: a token's place is the number of tokens that sort before it. With
 // key and place in one word (the place below the key) these are the smaller
-// words. A workgroup holds all words in LDS and places RANK_ITEMS tokens, each
-// counted by eight lanes over an eighth of the words: n^2 comparisons spread
-// over the chip, one launch and no passes. 8192 tokens: the digit passes of one
-// workgroup took 22 us.
-constexpr int RANK_THR = 256, RANK_ITEMS = 32, RANK_PARTS = RANK_THR / RANK_ITEMS;
+// words. A workgroup holds all words in LDS and places RANK_ITEMS tokens; a lane
+// compares RANK_LANE of them with one of RANK_PARTS runs of words, so that a
+// word read from LDS serves four comparisons. n^2 comparisons spread over the
+// chip, one launch and no passes: 8192 tokens 11 us (256 threads a workgroup
+// 17.4, 512 13.1: one wave a SIMD does not hide its own latencies), bound by the
+// comparisons (2.5 operations each) and by every workgroup reading every token;
+// digit passes of one workgroup took 22 us, of small tiles about 25.
+constexpr int RANK_THR = 1024, RANK_ITEMS = 32, RANK_LANE = 4, RANK_PARTS = RANK_THR / (RANK_ITEMS / RANK_LANE);
 template <typename W>
 __global__ __launch_bounds__(RANK_THR) void k_sort_rank(SortArgs A) {
     extern __shared__ __align__(16) char raw[];
-    __shared__ int count[RANK_PARTS][RANK_ITEMS];
+    __shared__ int count[RANK_THR / 64][RANK_ITEMS];
     if ((int)blockIdx.x >= A.sorters) {
         fill_zeros(A);
         return;
@@ -204,36 +206,47 @@ __global__ __launch_bounds__(RANK_THR) void k_sort_rank(SortArgs A) {
     typedef W WV __attribute__((ext_vector_type(PER)));
     LDSP W* word = (LDSP W*)(LDSP char*)raw;
     const int tid = threadIdx.x;
-    const int part = ((A.n + RANK_PARTS - 1) / RANK_PARTS + PER - 1) / PER * PER;   // words of an eighth
+    // run q is reads q, q + RANK_PARTS, ..: the runs of a wave read side by side
+    const int reads = (A.n + PER * RANK_PARTS - 1) / (PER * RANK_PARTS) * RANK_PARTS, words = reads * PER;
     // (each workgroup begins elsewhere: all at one place would queue at one
     // memory channel)
-    const int words = part * RANK_PARTS;
-    int start = (int)((int64_t)words * (blockIdx.x >> 3) / ((A.sorters >> 3) + 1)) / RANK_THR * RANK_THR;
-#pragma unroll 8
+    const int start = (int)((int64_t)words * (blockIdx.x >> 3) / ((A.sorters >> 3) + 1)) / RANK_THR * RANK_THR;
+#pragma unroll 16
     for (int j = tid; j < words; j += RANK_THR) {
         int i = j + start;
         if (i >= words) i -= words;
         word[i] = i < A.n ? ((W)key_of(A, min(i, A.n - 1)) << A.index_bits) | (W)i : ~(W)0 >> 1;
     }
     __syncthreads();
-    const int item = blockIdx.x * RANK_ITEMS + tid % RANK_ITEMS, q = tid / RANK_ITEMS;
-    const W mine = word[min(item, A.n - 1)];
-    int n = 0;
-    const LDSP WV* from = (const LDSP WV*)(word + q * part);
-#pragma unroll 8
-    for (int i = 0; i < part / PER; ++i) {
-        const WV x = from[i];
+    const int g = tid % (RANK_ITEMS / RANK_LANE), q = tid / (RANK_ITEMS / RANK_LANE), first = blockIdx.x * RANK_ITEMS;
+    W mine[RANK_LANE];
+    int n[RANK_LANE];
 #pragma unroll
-        for (int k = 0; k < PER; ++k) n += (int)((x[k] - mine) >> (8 * sizeof(W) - 1));   // 1 where x < mine
+    for (int k = 0; k < RANK_LANE; ++k) {
+        mine[k] = word[min(first + g * RANK_LANE + k, A.n - 1)];
+        n[k] = 0;
     }
-    count[q][tid % RANK_ITEMS] = n;
-    __syncthreads();
-    if (tid >= RANK_ITEMS || item >= A.n) return;
-    n = 0;
+#pragma unroll 4
+    for (int i = q; i < reads; i += RANK_PARTS) {
+        const WV x = ((const LDSP WV*)word)[i];
 #pragma unroll
-    for (int k = 0; k < RANK_PARTS; ++k) n += count[k][tid];
-    gp(A.key_out)[n] = (int32_t)(mine >> A.index_bits);
-    gp(A.pos_out)[n] = item;
+        for (int k = 0; k < RANK_LANE; ++k)
+#pragma unroll
+            for (int e = 0; e < PER; ++e) n[k] += (int)((x[e] - mine[k]) >> (8 * sizeof(W) - 1));   // 1 where x < mine
+    }
+#pragma unroll
+    for (int k = 0; k < RANK_LANE; ++k) {
+        for (int off = RANK_ITEMS / RANK_LANE; off < 64; off *= 2) n[k] += __shfl_xor(n[k], off, 64);
+        if ((tid & 63) == g) count[tid >> 6][g * RANK_LANE + k] = n[k];
+    }
+    __syncthreads();
+    const int item = first + tid;
+    if (tid >= RANK_ITEMS || item >= A.n) return;
+    int to = 0;
+#pragma unroll
+    for (int k = 0; k < RANK_THR / 64; ++k) to += count[k][tid];
+    gp(A.key_out)[to] = (int32_t)(word[item] >> A.index_bits);
+    gp(A.pos_out)[to] = item;
 }
 
 // More tokens: two launches for each digit, over tiles of THR * SORT_IPT.
@@ -591,7 +604,7 @@ int check_rowgrad(const mu_rowgrad* e) {
 
 // What a call of these sizes launches and keeps in its workspace.
 struct GradPlan {
-    int n, bits, passes, thr, tiles, chunk, chunks, lanes, slices;
+    int n, index_bits, word_bits, passes, thr, tiles, chunk, chunks, lanes, slices;
     size_t off_key[2], off_pos[2], off_hist, off_part, bytes;
 };
 GradPlan grad_plan(const mu_rowgrad* e) {
@@ -599,11 +612,19 @@ GradPlan grad_plan(const mu_rowgrad* e) {
     p.n = (int)e->n_tokens;
     int bits = 1;
     while (bits < 32 && (e->vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
-    p.bits = bits;
     p.passes = (bits + DIGIT - 1) / DIGIT;
     // small tiles while they are few: every tile reads all tiles' counts
     p.thr = p.n <= (1 << 18) ? 256 : 1024;
-    p.tiles = p.n <= SORT_RANK ? 0 : (p.n + p.thr * SORT_IPT - 1) / (p.thr * SORT_IPT);
+    // Counting or digit passes: 9000 tokens 33 against 46 us (768 columns), 12000
+    // 39 against 48, 16384 51 against 48; with 64-bit words 32 against 34 at 9000
+    // and 40 against 35 at 12000.
+    p.index_bits = 0;
+    while ((1 << p.index_bits) < p.n) ++p.index_bits;
+    // words stay below half the type's range: the padding of the last reads is
+    // above all, and a difference of two has the sign of its comparison
+    p.word_bits = bits + p.index_bits < 31 ? 32 : 64;
+    const bool rank = p.n <= (p.word_bits == 32 ? 12288 : 8192);
+    p.tiles = rank ? 0 : (p.n + p.thr * SORT_IPT - 1) / (p.thr * SORT_IPT);
     // short chunks while tokens are few (more waves), longer ones as their
     // partial sums would pass 64 MB
     p.chunk = 16;
@@ -668,13 +689,11 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
     if (p.tiles == 0) {
         a.key_out = (int32_t*)(ws + p.off_key[0]);
         a.pos_out = (int32_t*)(ws + p.off_pos[0]);
-        while ((1 << a.index_bits) < p.n) ++a.index_bits;
+        a.index_bits = p.index_bits;
         const int groups = (p.n + RANK_ITEMS - 1) / RANK_ITEMS;
-        const size_t words = ((size_t)p.n + RANK_PARTS - 1) / RANK_PARTS + 3;
-        // words stay below half the type's range: the padding of the last eighth
-        // is above all, and a difference of two has the sign of its comparison
-        const bool small = p.bits + a.index_bits < 31;
-        const size_t lds = p.n == 0 ? 0 : words / 4 * 4 * RANK_PARTS * (small ? 4 : 8);
+        const bool small = p.word_bits == 32;
+        const int per = (small ? 4 : 2) * RANK_PARTS;   // words of one read of every run
+        const size_t lds = (size_t)(p.n + per - 1) / per * 16 * RANK_PARTS;
         const int rc = sort_launch(small ? k_sort_rank<uint32_t> : k_sort_rank<uint64_t>, a, groups, RANK_THR, lds,
                                    (double)p.n * (e->token_bits / 8 + 8));
         if (rc) return rc;

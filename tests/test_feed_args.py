@@ -108,6 +108,16 @@ def test_bad_rowgrad_rejected(lib, kw, code):
     assert _rowgrad(lib, **kw) == code
 
 
+def test_rowgrad_workspace_rejected(lib):
+    need = ctypes.c_size_t(0)
+    e = lib.MuRowgrad(tokens=A, rows=A + (1 << 30), grad=A + (2 << 30), n_tokens=8, vocab=16, dim=32, padding_idx=-1,
+                      token_bits=64, row_dtype=lib.MU_BF16, grad_dtype=lib.MU_F32, accumulate=0, scale=1.0, pad0=0)
+    assert lib.LIB.mu_embedding_grad_workspace_size(ctypes.byref(e), ctypes.byref(need)) == 0 and need.value > 0
+    for kw in (dict(ws=None), dict(ws=A + (4 << 30) + 8), dict(nb=need.value - 1)):
+        assert _rowgrad(lib, **kw) == lib.MU_ERR_WORKSPACE, kw
+    assert lib.LIB.mu_embedding_grad_workspace_size(ctypes.byref(e), None) == lib.MU_ERR_INVALID_ARG
+
+
 def test_empty_accumulation_is_nothing(lib):
     assert _rowgrad(lib, n_tokens=0, tokens=None, rows=None, accumulate=1) == lib.MU_OK
 
