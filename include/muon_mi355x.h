@@ -281,7 +281,8 @@ int mu_grad_norm_workspace_size(const mu_grad* gs, int32_t n, size_t* bytes);
 int mu_grad_norm(const mu_grad* gs, int32_t n, float max_norm, float eps, float* norm_out, float* scale_out,
                  void* workspace, size_t workspace_bytes, void* stream);
 
-/* The norm and the scaled gradients; norm_out and scale_out are optional. */
+/* The norm and the scaled gradients; norm_out and scale_out are optional. No
+ * buffer may overlap another, the two results included. */
 int mu_clip_grads(const mu_grad* gs, int32_t n, float max_norm, float eps, float* norm_out, float* scale_out,
                   void* workspace, size_t workspace_bytes, void* stream);
 
@@ -289,7 +290,8 @@ int mu_clip_grads(const mu_grad* gs, int32_t n, float max_norm, float eps, float
  * mu_muon_step and mu_adamw_step with every gradient multiplied by *grad_scale
  * (device float32, read when the kernels run; mu_grad_norm's scale_out) as it
  * is read, in float32 and unrounded: a clipped step without a pass that writes
- * the scaled gradients. NULL is the plain step.
+ * the scaled gradients. grad_scale lies outside the list's buffers; NULL is the
+ * plain step.
  */
 int mu_muon_step_scaled(const mu_matrix* mats, int32_t n, const mu_muon_hparams* hp, const float* grad_scale,
                         void* workspace, size_t workspace_bytes, void* stream);

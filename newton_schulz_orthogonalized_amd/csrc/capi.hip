@@ -1480,16 +1480,17 @@ int mu_muon_step(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, void*
 
 int mu_muon_step_scaled(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, const float* grad_scale, void* ws,
                         size_t ws_bytes, void* stream) {
-    g_err.clear();
-    if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
-    int rc = check_hparams(hp, true);
-    if (rc) return rc;
-    std::vector<Item> items;
-    int dt;
-    rc = validate_mats(m, n, items, dt);
-    if (rc) return rc;
-    if (n == 0) return MU_OK;
-    return run_call(items, hp, dt, true, ws, ws_bytes, grad_scale, (hipStream_t)stream);
+    return guarded([&]() -> int {
+        if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
+        int rc = check_hparams(hp, true);
+        if (rc) return rc;
+        std::vector<Item> items;
+        int dt;
+        rc = validate_mats(m, n, items, dt);
+        if (rc) return rc;
+        if (n == 0) return MU_OK;
+        return run_call(items, hp, dt, true, ws, ws_bytes, grad_scale, (hipStream_t)stream);
+    });
 }
 
 int mu_muon_step_noalloc(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp, void* stream) {
@@ -1646,72 +1647,73 @@ int mu_adamw_step(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, vo
 
 int mu_adamw_step_scaled(const mu_tensor* ts, int32_t n, const mu_adamw_hparams* hp, const float* grad_scale, void* ws,
                          size_t ws_bytes, void* stream) {
-    g_err.clear();
-    if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
-    if (!hp) return fail(MU_ERR_INVALID_ARG, "hparams is null");
-    if (n < 0) return fail(MU_ERR_INVALID_ARG, "n must be >= 0");
-    if (n > 0 && !ts) return fail(MU_ERR_INVALID_ARG, "tensor list is null");
-    if (hp->step < 1) return fail(MU_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)hp->step);
-    if (!std::isfinite(hp->beta1) || !std::isfinite(hp->beta2) || !std::isfinite(hp->eps))
-        return fail(MU_ERR_INVALID_ARG, "beta1, beta2 and eps must be finite");
-    if (hp->beta1 < 0.f || hp->beta1 >= 1.f || hp->beta2 < 0.f || hp->beta2 >= 1.f)
-        return fail(MU_ERR_INVALID_ARG, "betas must lie in [0, 1)");
-    std::vector<AdamWDesc> d((size_t)n);
-    std::vector<int64_t> prefix(1, 0);
-    std::vector<Range> ranges;
-    for (int i = 0; i < n; ++i) {
-        const mu_tensor& t = ts[i];
-        if (t.dtype != MU_F32 && t.dtype != MU_BF16) return fail(MU_ERR_DTYPE, "tensor %d: unknown dtype %d", i, t.dtype);
-        if (t.numel < 0) return fail(MU_ERR_INVALID_ARG, "tensor %d: numel must be >= 0", i);
-        if (t.numel > 0 && (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq))
-            return fail(MU_ERR_INVALID_ARG, "tensor %d: null buffer", i);
-        if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
-            return fail(MU_ERR_INVALID_ARG, "tensor %d: lr and weight_decay must be finite", i);
-        const size_t es = dtype_size(t.dtype);
-        if (!aligned(t.param, es) || !aligned(t.grad, es) || !aligned(t.exp_avg, 4) || !aligned(t.exp_avg_sq, 4))
-            return fail(MU_ERR_LAYOUT, "tensor %d: misaligned buffer", i);
-        if (t.numel > 0) {
-            ranges.push_back({(uintptr_t)t.param, (uintptr_t)t.param + t.numel * es, i});
-            ranges.push_back({(uintptr_t)t.grad, (uintptr_t)t.grad + t.numel * es, i});
-            ranges.push_back({(uintptr_t)t.exp_avg, (uintptr_t)t.exp_avg + t.numel * 4, i});
-            ranges.push_back({(uintptr_t)t.exp_avg_sq, (uintptr_t)t.exp_avg_sq + t.numel * 4, i});
+    return guarded([&]() -> int {
+        if (!aligned(grad_scale, 4)) return fail(MU_ERR_LAYOUT, "misaligned grad_scale");
+        if (!hp) return fail(MU_ERR_INVALID_ARG, "hparams is null");
+        if (n < 0) return fail(MU_ERR_INVALID_ARG, "n must be >= 0");
+        if (n > 0 && !ts) return fail(MU_ERR_INVALID_ARG, "tensor list is null");
+        if (hp->step < 1) return fail(MU_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)hp->step);
+        if (!std::isfinite(hp->beta1) || !std::isfinite(hp->beta2) || !std::isfinite(hp->eps))
+            return fail(MU_ERR_INVALID_ARG, "beta1, beta2 and eps must be finite");
+        if (hp->beta1 < 0.f || hp->beta1 >= 1.f || hp->beta2 < 0.f || hp->beta2 >= 1.f)
+            return fail(MU_ERR_INVALID_ARG, "betas must lie in [0, 1)");
+        std::vector<AdamWDesc> d((size_t)n);
+        std::vector<int64_t> prefix(1, 0);
+        std::vector<Range> ranges;
+        for (int i = 0; i < n; ++i) {
+            const mu_tensor& t = ts[i];
+            if (t.dtype != MU_F32 && t.dtype != MU_BF16) return fail(MU_ERR_DTYPE, "tensor %d: unknown dtype %d", i, t.dtype);
+            if (t.numel < 0) return fail(MU_ERR_INVALID_ARG, "tensor %d: numel must be >= 0", i);
+            if (t.numel > 0 && (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq))
+                return fail(MU_ERR_INVALID_ARG, "tensor %d: null buffer", i);
+            if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
+                return fail(MU_ERR_INVALID_ARG, "tensor %d: lr and weight_decay must be finite", i);
+            const size_t es = dtype_size(t.dtype);
+            if (!aligned(t.param, es) || !aligned(t.grad, es) || !aligned(t.exp_avg, 4) || !aligned(t.exp_avg_sq, 4))
+                return fail(MU_ERR_LAYOUT, "tensor %d: misaligned buffer", i);
+            if (t.numel > 0) {
+                ranges.push_back({(uintptr_t)t.param, (uintptr_t)t.param + t.numel * es, i});
+                ranges.push_back({(uintptr_t)t.grad, (uintptr_t)t.grad + t.numel * es, i});
+                ranges.push_back({(uintptr_t)t.exp_avg, (uintptr_t)t.exp_avg + t.numel * 4, i});
+                ranges.push_back({(uintptr_t)t.exp_avg_sq, (uintptr_t)t.exp_avg_sq + t.numel * 4, i});
+            }
+            d[i] = AdamWDesc{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.numel, t.dtype,
+                             (int32_t)(aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.exp_avg, 16) && aligned(t.exp_avg_sq, 16)),
+                             t.lr, t.weight_decay};
+            prefix.push_back(prefix.back() + (t.numel + ADAMW_CHUNK - 1) / ADAMW_CHUNK);
         }
-        d[i] = AdamWDesc{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.numel, t.dtype,
-                         (int32_t)(aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.exp_avg, 16) && aligned(t.exp_avg_sq, 16)),
-                         t.lr, t.weight_decay};
-        prefix.push_back(prefix.back() + (t.numel + ADAMW_CHUNK - 1) / ADAMW_CHUNK);
-    }
-    if (ranges_overlap(ranges)) return fail(MU_ERR_LAYOUT, "buffers of the tensor list overlap");
-    if (n == 0 || prefix.back() == 0) return MU_OK;
-    size_t need = 0;
-    mu_adamw_workspace_size(n, &need);
-    if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
-    if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-    if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
-    if (prefix.back() > 0x7ffffff8LL) return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
+        if (ranges_overlap(ranges)) return fail(MU_ERR_LAYOUT, "buffers of the tensor list overlap");
+        if (n == 0 || prefix.back() == 0) return MU_OK;
+        size_t need = 0;
+        mu_adamw_workspace_size(n, &need);
+        if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
+        if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+        if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+        if (prefix.back() > 0x7ffffff8LL) return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
 
-    std::vector<char> table(sizeof(AdamWDesc) * n + sizeof(int64_t) * (n + 1));
-    std::memcpy(table.data(), d.data(), sizeof(AdamWDesc) * n);
-    std::memcpy(table.data() + sizeof(AdamWDesc) * n, prefix.data(), sizeof(int64_t) * (n + 1));
-    hipStream_t s = (hipStream_t)stream;
-    int rc = check_not_capturing(s);
-    if (rc) return rc;
-    rc = upload(table.data(), table.size(), ws, s);
-    if (rc) return rc;
-    AdamWArgs a{};
-    a.descs = (const AdamWDesc*)ws;
-    a.prefix = (const int64_t*)((char*)ws + sizeof(AdamWDesc) * n);
-    a.n = n;
-    a.total_chunks = prefix.back();
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.eps = hp->eps;
-    a.bc1 = (float)(1.0 - std::pow((double)hp->beta1, (double)hp->step));
-    a.bc2 = (float)(1.0 - std::pow((double)hp->beta2, (double)hp->step));
-    a.gscale = grad_scale;
-    double bytes = 0;
-    for (int i = 0; i < n; ++i) bytes += (double)ts[i].numel * (3.0 * dtype_size(ts[i].dtype) + 16.0);
-    return timed_launch(MU_K_ADAMW, 0.0, bytes, s, [&] { return launch_adamw(a, s); }, "adamw launch");
+        std::vector<char> table(sizeof(AdamWDesc) * n + sizeof(int64_t) * (n + 1));
+        std::memcpy(table.data(), d.data(), sizeof(AdamWDesc) * n);
+        std::memcpy(table.data() + sizeof(AdamWDesc) * n, prefix.data(), sizeof(int64_t) * (n + 1));
+        hipStream_t s = (hipStream_t)stream;
+        int rc = check_not_capturing(s);
+        if (rc) return rc;
+        rc = upload(table.data(), table.size(), ws, s);
+        if (rc) return rc;
+        AdamWArgs a{};
+        a.descs = (const AdamWDesc*)ws;
+        a.prefix = (const int64_t*)((char*)ws + sizeof(AdamWDesc) * n);
+        a.n = n;
+        a.total_chunks = prefix.back();
+        a.beta1 = hp->beta1;
+        a.beta2 = hp->beta2;
+        a.eps = hp->eps;
+        a.bc1 = (float)(1.0 - std::pow((double)hp->beta1, (double)hp->step));
+        a.bc2 = (float)(1.0 - std::pow((double)hp->beta2, (double)hp->step));
+        a.gscale = grad_scale;
+        double bytes = 0;
+        for (int i = 0; i < n; ++i) bytes += (double)ts[i].numel * (3.0 * dtype_size(ts[i].dtype) + 16.0);
+        return timed_launch(MU_K_ADAMW, 0.0, bytes, s, [&] { return launch_adamw(a, s); }, "adamw launch");
+    });
 }
 
 int mu_profile_enable(int on) {

@@ -297,10 +297,12 @@ __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
 
 size_t es_of(int dt) { return dt == MU_BF16 ? 2 : 4; }
 
-int check_list(const mu_grad* gs, int32_t n, bool with_out) {
+int check_list(const mu_grad* gs, int32_t n, bool with_out, const float* norm_out, const float* scale_out) {
     if (n < 0) return fail(MU_ERR_INVALID_ARG, "n must be >= 0");
     if (n > 0 && !gs) return fail(MU_ERR_INVALID_ARG, "gradient list is null");
     std::vector<Range> ranges;
+    for (const float* p : {norm_out, scale_out})
+        if (p) ranges.push_back({(uintptr_t)p, (uintptr_t)p + 4, -1});
     for (int i = 0; i < n; ++i) {
         const mu_grad& g = gs[i];
         if (g.dtype != MU_F32 && g.dtype != MU_BF16) return fail(MU_ERR_DTYPE, "gradient %d: unknown dtype %d", i, g.dtype);
@@ -353,7 +355,7 @@ size_t partials_of(const std::vector<Batch>& b) {
 
 int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float* norm_out, float* scale_out, bool clip,
                   void* ws, size_t ws_bytes, hipStream_t s) {
-    int rc = check_list(gs, n, clip);
+    int rc = check_list(gs, n, clip, norm_out, scale_out);
     if (rc) return rc;
     if (!(max_norm >= 0.f)) return fail(MU_ERR_INVALID_ARG, "max_norm must be >= 0");
     if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MU_ERR_INVALID_ARG, "eps must be finite and >= 0");
@@ -444,7 +446,7 @@ extern "C" {
 int mu_grad_norm_workspace_size(const mu_grad* gs, int32_t n, size_t* bytes) {
     return guarded([&]() -> int {
         if (!bytes) return fail(MU_ERR_INVALID_ARG, "bytes is null");
-        int rc = check_list(gs, n, false);
+        int rc = check_list(gs, n, false, nullptr, nullptr);
         if (rc) return rc;
         std::vector<Batch> bs;
         rc = batches(gs, n, SQ_SEGS, bs);

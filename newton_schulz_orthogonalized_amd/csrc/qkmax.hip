@@ -504,7 +504,7 @@ int run_any(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, d
     if (d <= 64) return run<float, 64, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
     if (d <= 96) return run<float, 96, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
     if (d <= 128) return run<float, 128, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 192) return run<float, 192, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
+    if (d <= 192) return run<float, 192, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
     return run<float, 256, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
 }
 

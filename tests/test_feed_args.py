@@ -56,6 +56,8 @@ def test_bad_clip_outputs_rejected(lib):
     assert _norm(lib, _grads(lib, dict(out=A + (1 << 20) + 1)), 1, clip=True) == lib.MU_ERR_LAYOUT
     assert _norm(lib, _grads(lib, dict(out=A + 4)), 1, clip=True) == lib.MU_ERR_LAYOUT           # overlaps its input
     assert _norm(lib, _grads(lib, dict(out=A), dict(out=A)), 2, clip=True) == lib.MU_ERR_LAYOUT  # one buffer twice in place
+    for kw in (dict(norm=A + 8), dict(scale=A + (1 << 20)), dict(norm=A + (1 << 30), scale=A + (1 << 30))):
+        assert _norm(lib, _grads(lib, ok), 1, clip=True, **kw) == lib.MU_ERR_LAYOUT, kw          # results inside buffers
     # the same buffer as another type is not an in-place call
     assert _norm(lib, _grads(lib, dict(out=A, out_dtype=lib.MU_BF16)), 1, clip=True) == lib.MU_ERR_LAYOUT
 
