@@ -40,7 +40,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // starts and ends.
 struct QkMaxArgs {
     mu_qk_logits p;
-    const int64_t* prefix;   // [batch + 1] places of one head before each sequence
+    const int64_t* prefix;   // [batch + 1] places of one head before each sequence; null: see BY_HEAD
 };
 
 struct Seq {
@@ -95,6 +95,10 @@ struct Tiles {
     }
     __device__ int64_t total() const { return last < 0 ? 0 : before(last) + COST + all; }
 };
+
+// With no more key tiles than this in a head, a workgroup takes all of one: it
+// needs no plan and stores its maximum itself, one launch instead of two.
+constexpr int BY_HEAD = 4;
 
 // One workgroup: the places before each sequence, and zeros to take maxima from.
 constexpr int PLAN_THR = 1024;
@@ -245,35 +249,63 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         __syncthreads();
     }
 
-    const int64_t per_head = uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
-    // XCD x takes places [x * total / 8, (x + 1) * total / 8), so few key heads
-    const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3, w_in = blockIdx.x >> 3;
-    const int64_t x_lo = total * xcd / 8, x_n = total * (xcd + 1) / 8 - x_lo;
-    int64_t u = x_lo + x_n * w_in / wgs;
-    const int64_t u_end = x_lo + x_n * (w_in + 1) / wgs;
-    if (u >= u_end) return;
-    int h = (int)(u / per_head);
-    int64_t r = u - h * per_head;   // place in the head
-    // its sequence: the last one that starts at or before r, 64 candidates at a time
-    int64_t b = 0;
-    for (int64_t n = P.batch; n > 1;) {
-        const int64_t st = (n + 63) / 64, at = b + min<int64_t>(st * lane, n - 1);
-        const int k = __popcll(__ballot(lane * st < n && gp(A.prefix)[at] <= r));   // >= 1
-        b += (k - 1) * st;
-        n = min<int64_t>(st, n - (k - 1) * st);
+    const bool by_head = A.prefix == nullptr;
+    int64_t u = 0, u_end = (int64_t)1 << 60, r = 0, b = 0;
+    int h = blockIdx.x, t = 0;
+    if (!by_head) {
+        const int64_t per_head = uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
+        // XCD x takes places [x * total / 8, (x + 1) * total / 8), so few key heads
+        const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3, w_in = blockIdx.x >> 3;
+        const int64_t x_lo = total * xcd / 8, x_n = total * (xcd + 1) / 8 - x_lo;
+        u = x_lo + x_n * w_in / wgs;
+        u_end = x_lo + x_n * (w_in + 1) / wgs;
+        if (u >= u_end) return;
+        h = (int)(u / per_head);
+        r = u - h * per_head;   // place in the head
+        // its sequence: the last one that starts at or before r, 64 candidates at a time
+        for (int64_t n = P.batch; n > 1;) {
+            const int64_t st = (n + 63) / 64, at = b + min<int64_t>(st * lane, n - 1);
+            const int k = __popcll(__ballot(lane * st < n && gp(A.prefix)[at] <= r));   // >= 1
+            b += (k - 1) * st;
+            n = min<int64_t>(st, n - (k - 1) * st);
+        }
+        b = uni64(b);
+        r -= uni64(gp(A.prefix)[b]);
     }
-    b = uni64(b);
-    Seq S = seq_of(P, b);
+    const bool none = P.batch == 0 || P.q_len == 0 || P.k_len == 0;   // (lengths are not read then)
+    Seq S{0, 0, 0, 0};
+    if (!none) S = seq_of(P, b);
     Tiles<BM, BN> tl(S, P.causal != 0);
-    r -= uni64(gp(A.prefix)[b]);
-    int t = tl.t0;
-    for (int n = tl.last - tl.t0 + 1; n > 1;) {   // its query tile
+    if (by_head && !none)
+        while (tl.last < 0 && ++b < P.batch) {
+            S = seq_of(P, b);
+            tl = Tiles<BM, BN>(S, P.causal != 0);
+        }
+    t = tl.t0;
+    for (int n = tl.last - tl.t0 + 1; !by_head && n > 1;) {   // the query tile of place r
         const int half_n = n / 2;
         if (tl.before(t + half_n) <= r) t += half_n, n -= half_n;
         else n = half_n;
     }
-    r -= tl.before(t);
-    for (; u < u_end; r = 0) {
+    if (!by_head) r -= tl.before(t);
+    bool more = tl.last >= 0;   // (false: by head, and no sequence has a tile)
+    // the largest magnitude of head h, kept over its query tiles
+    float best = 0.f;
+    auto flush = [&] {
+        int bits = __float_as_int(best) & 0x7fffffff;
+        for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
+        if (lane == 0) red[wave] = bits;
+        __syncthreads();
+        if (tid == 0) {
+            bits = max(max(red[0], red[1]), max(red[2], red[3]));
+            bits = __float_as_int(__builtin_fabsf(P.scale) * __int_as_float(bits)) & 0x7fffffff;
+            int* out = (int*)P.max_logit + h;
+            if (!by_head) atomicMax(out, bits);
+            else *gp(out) = P.accumulate ? max(*gp(out), bits) : bits;
+        }
+        best = 0.f;
+    };
+    for (; more; r = 0) {
         // key tiles first .. first + ntiles - 1 of query tile t, from its place r on
         const int64_t places = min<int64_t>(COST + tl.of(t) - r, u_end - u);
         u += places;
@@ -329,7 +361,6 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
             for (int k = 0; k < NK; ++k) qf[m][k] = load_chunk<T, ROWS>(row, 2 * k + half, P.dim);
         }
 
-        float best = 0.f;
         // The stream of right operands: tile after tile, 32 keys (a column
         // block) after 32 keys, chunk pair after chunk pair. f holds the next
         // PD of them; each place is read again as soon as its matrix
@@ -442,23 +473,25 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         }
         if constexpr (NB > 1) take(std::true_type{}, acc[1], thr_prev);
         for (; kt < ntiles; ++kt) advance(kt % 4 == 0 ? s3 : kt % 4 == 1 ? s0 : kt % 4 == 2 ? s1 : s2, kt + 1);
-        int bits = __float_as_int(best) & 0x7fffffff;
-        for (int o = 32; o >= 1; o >>= 1) bits = max(bits, __shfl_xor(bits, o, 64));
-        if (lane == 0) red[wave] = bits;
-        __syncthreads();   // also: every wave is done with the slots
-        if (tid == 0) {
-            bits = max(max(red[0], red[1]), max(red[2], red[3]));
-            if (bits > 0) atomicMax((int*)P.max_logit + h, __float_as_int(__builtin_fabsf(P.scale) * __int_as_float(bits)) & 0x7fffffff);
-        }
+        __syncthreads();   // every wave is done with the slots
         // the next query tile, sequence or head
-        if (++t <= tl.last || u >= u_end) continue;
+        more = u < u_end;
+        if (!more || ++t <= tl.last) continue;
         do {
-            if (++b == P.batch) b = 0, ++h;
+            if (++b == P.batch) {
+                if (by_head) {
+                    more = false;
+                    break;
+                }
+                flush();
+                b = 0, ++h;
+            }
             S = seq_of(P, b);
             tl = Tiles<BM, BN>(S, P.causal != 0);
-        } while (tl.last < 0);   // a later sequence has tiles: u < u_end
+        } while (tl.last < 0);   // (not by head: a later sequence has tiles, as u < u_end)
         t = tl.t0;
     }
+    flush();
 }
 
 template <typename T, int DP, int BN, int MT, int WPE>
@@ -469,23 +502,31 @@ hipError_t launch(const QkMaxArgs& a, bool direct, int grid, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Key tiles of a head at most (lengths on the device may leave fewer).
+double most_tiles(const mu_qk_logits* a, int bm, int bn) {
+    const double q = a->cu_q ? (double)(a->q_len / bm) + a->batch : (double)a->batch * ((a->q_len + bm - 1) / bm);
+    return a->q_len == 0 || a->k_len == 0 ? 0.0 : q * (double)((a->k_len + bn - 1) / bn);
+}
+
 // An instance: padded head width, keys and queries of a tile.
 template <typename T, int DP, int BN, int MT, int WPE>
 int run(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, double bytes, hipStream_t s) {
-    const QkMaxArgs q{*a, prefix};
     constexpr int BM = 4 * MT * 32;
+    const double tiles = most_tiles(a, BM, BN);
+    const QkMaxArgs q{*a, tiles <= BY_HEAD ? nullptr : prefix};
+    if (tiles <= BY_HEAD)
+        return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch<T, DP, BN, MT, WPE>(q, direct, a->q_heads, s); },
+                            "max logits launch");
     int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, s, [&] {
         hipLaunchKernelGGL((k_qk_plan<BM, BN>), dim3(1), dim3(PLAN_THR), 0, s, q, prefix);
         return hipGetLastError();
     }, "max logits plan");
-    if (rc || flops == 0.0) return rc;
+    if (rc) return rc;
     int cus = 0;
     rc = cu_count(&cus);
     if (rc) return rc;
     // two workgroups a compute unit; fewer where there cannot be as many tiles
-    const int64_t seqs = a->cu_q ? 1 : a->batch, more = a->cu_q ? a->batch : 0;
-    const double tiles = ((double)seqs * ((a->q_len + BM - 1) / BM) + (double)more) * (double)((a->k_len + BN - 1) / BN) * a->q_heads;
-    const int grid = (int)std::min<double>((double)WPE * cus, 8.0 * std::ceil(tiles / 8.0));
+    const int grid = (int)std::min<double>((double)WPE * cus, 8.0 * std::ceil(tiles * a->q_heads / 8.0));
     return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch<T, DP, BN, MT, WPE>(q, direct, grid, s); },
                         "max logits launch");
 }
@@ -534,7 +575,12 @@ int check(const mu_qk_logits* a) {
     return MU_OK;
 }
 
-size_t qk_workspace(const mu_qk_logits* a) { return align_up(sizeof(int64_t) * ((size_t)a->batch + 1)); }
+// (the smallest tiles of the type's instances: a call that needs none by these
+// counts needs none by its own)
+size_t qk_workspace(const mu_qk_logits* a) {
+    const bool few = most_tiles(a, a->dtype == MU_BF16 ? 256 : 128, 32) <= BY_HEAD;
+    return few ? 0 : align_up(sizeof(int64_t) * ((size_t)a->batch + 1));
+}
 
 }  // namespace
 
@@ -557,9 +603,11 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* str
         const bool empty = a->batch == 0 || a->q_len == 0 || a->k_len == 0;
         if (empty && a->accumulate) return MU_OK;
         const size_t need = qk_workspace(a);
-        if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
-        if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-        if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+        if (need) {
+            if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
+            if (!aligned(ws, ALIGN)) return fail(MU_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+            if (ws_bytes < need) return fail(MU_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+        }
         const int es = a->dtype == MU_BF16 ? 2 : 4;
         // rows as whole 16-byte chunks, a tile of them within 32-bit offsets
         const int64_t mix = a->q_stride_b | a->q_stride_s | a->q_stride_h | a->k_stride_b | a->k_stride_s | a->k_stride_h | a->dim;
@@ -567,7 +615,7 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* str
                             a->k_stride_s < ((int64_t)1 << 30) / (64 * es);
         const double nb = a->cu_q ? 1 : a->batch;
         const double bytes = nb * a->dim * es * ((double)a->q_len * a->q_heads + (double)a->k_len * a->k_heads);
-        const double flops = empty ? 0.0 : 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
+        const double flops = 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
         return run_any(a, (int64_t*)ws, direct, flops, bytes, (hipStream_t)stream);
     });
 }
