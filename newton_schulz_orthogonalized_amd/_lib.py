@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import itertools
+import operator
 import os
 import struct
 from typing import Optional, Sequence
@@ -366,18 +367,14 @@ def mu_adamw_step_scaled(ts, n, beta1: float, beta2: float, eps: float, step: in
 def device_of(tensors, what: str) -> int:
     """The index of the one GPU that all of `tensors` (None entries aside) live
     on; the current one where there is none."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if dev is None:
-            dev = d
-            if d < 0:
-                raise ValueError(f"{what} must be on a GPU (got a tensor on {t.device})")
-        elif d != dev:
-            raise ValueError(f"{what} must share one device (got GPU {dev} and {t.device})")
-    return torch.cuda.current_device() if dev is None else dev
+    devs = {t.get_device() for t in tensors if t is not None}
+    if not devs:
+        return torch.cuda.current_device()
+    if min(devs) < 0:
+        raise ValueError(f"{what} must be on a GPU")
+    if len(devs) > 1:
+        raise ValueError(f"{what} must share one device (got GPUs {sorted(devs)})")
+    return devs.pop()
 
 
 def scratch(nbytes: int, device: int) -> Optional[torch.Tensor]:
@@ -390,13 +387,15 @@ def scratch(nbytes: int, device: int) -> Optional[torch.Tensor]:
 
 _CODES = {torch.float32: MU_F32, torch.bfloat16: MU_BF16}
 _Tensor = torch._C.TensorBase
+_SHAPE = operator.attrgetter("shape")
+_DTYPE = operator.attrgetter("dtype")
 
 
 def _list_of(tensors, what: str):
     """Addresses, sizes and type codes of a list, in a few passes of C speed (a
     list may hold hundreds of tensors)."""
     try:
-        codes = [_CODES[t.dtype] for t in tensors]
+        codes = list(map(_CODES.__getitem__, map(_DTYPE, tensors)))
     except KeyError as e:
         raise TypeError(f"unsupported dtype {e.args[0]}") from None
     if not all(map(_Tensor.is_contiguous, tensors)):
@@ -414,7 +413,7 @@ def gradients(grads, outs=None):
         if len(outs) != n:
             raise ValueError("outs must have one tensor for each gradient")
         optrs, _, ocodes = _list_of(outs, "output")
-        if outs is not grads and [o.shape for o in outs] != [g.shape for g in grads]:
+        if outs is not grads and list(map(_SHAPE, outs)) != list(map(_SHAPE, grads)):
             raise ValueError("each output must have its gradient's shape")
     return struct.pack("=" + "QQqii" * n, *itertools.chain.from_iterable(zip(ptrs, optrs, sizes, codes, ocodes))), n
 
@@ -491,26 +490,31 @@ def mu_embedding_grad(e: MuRowgrad, workspace: Optional[torch.Tensor], stream=No
 def qk_logits(q, k, out, scale: float, causal: bool, lengths, k_lengths, cu_seqlens, cu_seqlens_k,
               accumulate: bool) -> MuQkLogits:
     packed = cu_seqlens is not None
+    q_shape, k_shape, q_stride, k_stride = q.shape, k.shape, q.stride(), k.stride()
     nd = 3 if packed else 4
-    if q.dim() != nd or k.dim() != nd:
+    if len(q_shape) != nd or len(k_shape) != nd:
         raise ValueError("q and k must be [batch, length, heads, dim], or [rows, heads, dim] with cu_seqlens")
     if k.dtype != q.dtype:
         raise TypeError("k must share q's dtype")
-    if q.shape[-1] != k.shape[-1] or (not packed and q.shape[0] != k.shape[0]):
+    dim = q_shape[-1]
+    if dim != k_shape[-1] or (not packed and q_shape[0] != k_shape[0]):
         raise ValueError("q and k must agree in dim and batch")
-    for t, what in ((q, "q"), (k, "k")):
-        if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {what} must be contiguous")
-    if out.dtype != torch.float32 or out.shape != (q.shape[-2],):
+    if dim > 1 and (q_stride[-1] != 1 or k_stride[-1] != 1):
+        raise ValueError("the last dimension of q and k must be contiguous")
+    if out.dtype != torch.float32 or out.shape != q_shape[-2:-1]:
         raise ValueError("out must be float32 with one element for each query head")
     _require(out, "out")
-    if packed and (lengths is not None or k_lengths is not None):
-        raise ValueError("packed sequences (cu_seqlens) take no lengths")
-    if cu_seqlens_k is not None and not packed:
-        raise ValueError("cu_seqlens_k needs cu_seqlens")
-    batch = cu_seqlens.numel() - 1 if packed else q.shape[0]
-    if packed and batch < 0:
-        raise ValueError("cu_seqlens must have at least one element")
+    if packed:
+        if lengths is not None or k_lengths is not None:
+            raise ValueError("packed sequences (cu_seqlens) take no lengths")
+        batch = cu_seqlens.numel() - 1
+        if batch < 0:
+            raise ValueError("cu_seqlens must have at least one element")
+        q_stride, k_stride = (0, *q_stride), (0, *k_stride)
+    else:
+        if cu_seqlens_k is not None:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        batch = q_shape[0]
     for t, what, size in ((lengths, "lengths", batch), (k_lengths, "k_lengths", batch),
                           (cu_seqlens, "cu_seqlens", batch + 1), (cu_seqlens_k, "cu_seqlens_k", batch + 1)):
         if t is None:
@@ -520,15 +524,10 @@ def qk_logits(q, k, out, scale: float, causal: bool, lengths, k_lengths, cu_seql
         if t.dim() != 1 or t.numel() != size:
             raise ValueError(f"{what} must have {size} elements")
         _require(t, what)
-    if packed:
-        qs, ks = (0,) + q.stride()[:2], (0,) + k.stride()[:2]
-        q_len, k_len = q.shape[0], k.shape[0]
-    else:
-        qs, ks = q.stride()[:3], k.stride()[:3]
-        q_len, k_len = q.shape[1], k.shape[1]
-    return MuQkLogits(_ptr(q), _ptr(k), *qs, *ks, q_len, k_len, batch, q.shape[-2], k.shape[-2], q.shape[-1],
-                      _ptr(lengths), _ptr(k_lengths), _ptr(cu_seqlens), _ptr(cu_seqlens_k), _dtype_code(q),
-                      1 if causal else 0, 1 if accumulate else 0, float(scale), _ptr(out))
+    return MuQkLogits(q.data_ptr(), k.data_ptr(), *q_stride[:3], *k_stride[:3], q_shape[-3], k_shape[-3], batch,
+                      q_shape[-2], k_shape[-2], dim, _ptr(lengths), _ptr(k_lengths), _ptr(cu_seqlens),
+                      _ptr(cu_seqlens_k), _dtype_code(q), 1 if causal else 0, 1 if accumulate else 0, float(scale),
+                      out.data_ptr())
 
 
 def mu_qk_max_logits_workspace_size(a: MuQkLogits) -> int:
