@@ -303,6 +303,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
             if (!by_head) atomicMax(out, bits);
             else *gp(out) = P.accumulate ? max(*gp(out), bits) : bits;
         }
+        __syncthreads();   // (a run that ends before its next head's first tile flushes twice in a row)
         best = 0.f;
     };
     for (; more; r = 0) {
@@ -350,7 +351,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         const int w_row = wave * (MT * 32);
         const bool live = w_row < nrows;
         const int see_last = !live ? 0 : min(nkeys, see + min(w_row + MT * 32, nrows) - 1);
-                stage(s0, 0);
+        stage(s0, 0);
         stage(s1, 1);
         V qf[MT][NK];
 #pragma unroll
@@ -494,59 +495,74 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     flush();
 }
 
-template <typename T, int DP, int BN, int MT, int WPE>
-hipError_t launch(const QkMaxArgs& a, bool direct, int grid, hipStream_t s) {
-    if (!direct) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, RAGGED>), dim3(grid), dim3(NTHR), 0, s, a);
-    else if (a.p.dim < DP) hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, PADDED>), dim3(grid), dim3(NTHR), 0, s, a);
-    else hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, FULL>), dim3(grid), dim3(NTHR), 0, s, a);
-    return hipGetLastError();
-}
-
 // Key tiles of a head at most (lengths on the device may leave fewer).
 double most_tiles(const mu_qk_logits* a, int bm, int bn) {
     const double q = a->cu_q ? (double)(a->q_len / bm) + a->batch : (double)a->batch * ((a->q_len + bm - 1) / bm);
     return a->q_len == 0 || a->k_len == 0 ? 0.0 : q * (double)((a->k_len + bn - 1) / bn);
 }
 
-// An instance: padded head width, keys and queries of a tile.
-template <typename T, int DP, int BN, int MT, int WPE>
-int run(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, double bytes, hipStream_t s) {
+struct Call {
+    const mu_qk_logits* p;
+    int64_t* prefix;
+    bool direct;
+    double flops, bytes;
+    hipStream_t s;
+};
+
+// An instance: padded head width, keys of a tile, queries of a wave in 32s, waves a SIMD.
+template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
+int run(const Call& c) {
     constexpr int BM = 4 * MT * 32;
-    const double tiles = most_tiles(a, BM, BN);
-    const QkMaxArgs q{*a, tiles <= BY_HEAD ? nullptr : prefix};
-    if (tiles <= BY_HEAD)
-        return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch<T, DP, BN, MT, WPE>(q, direct, a->q_heads, s); },
-                            "max logits launch");
-    int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, s, [&] {
-        hipLaunchKernelGGL((k_qk_plan<BM, BN>), dim3(1), dim3(PLAN_THR), 0, s, q, prefix);
+    const double tiles = most_tiles(c.p, BM, BN);
+    QkMaxArgs q{*c.p, nullptr};
+    int grid = c.p->q_heads;
+    if (tiles > BY_HEAD) {
+        q.prefix = c.prefix;
+        int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, c.s, [&] {
+            hipLaunchKernelGGL((k_qk_plan<BM, BN>), dim3(1), dim3(PLAN_THR), 0, c.s, q, c.prefix);
+            return hipGetLastError();
+        }, "max logits plan");
+        if (rc) return rc;
+        int cus = 0;
+        rc = cu_count(&cus);
+        if (rc) return rc;
+        // as many workgroups as the chip holds at a time, fewer where there
+        // cannot be as many tiles; the same number on each of the 8 XCDs
+        grid = (int)std::min<double>(std::max(WPE * cus / 8, 1) * 8, 8.0 * std::ceil(tiles * c.p->q_heads / 8.0));
+    }
+    return timed_launch(MU_K_QKMAX, c.flops, c.bytes, c.s, [&] {
+        hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, ROWS>), dim3(grid), dim3(NTHR), 0, c.s, q);
         return hipGetLastError();
-    }, "max logits plan");
-    if (rc) return rc;
-    int cus = 0;
-    rc = cu_count(&cus);
-    if (rc) return rc;
-    // two workgroups a compute unit; fewer where there cannot be as many tiles
-    const int grid = (int)std::min<double>((double)WPE * cus, 8.0 * std::ceil(tiles * a->q_heads / 8.0));
-    return timed_launch(MU_K_QKMAX, flops, bytes, s, [&] { return launch<T, DP, BN, MT, WPE>(q, direct, grid, s); },
-                        "max logits launch");
+    }, "max logits launch");
 }
 
-int run_any(const mu_qk_logits* a, int64_t* prefix, bool direct, double flops, double bytes, hipStream_t s) {
-    const int d = a->dim;
-    if (a->dtype == MU_BF16) {
-        if (d <= 32) return run<bf16, 32, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
-        if (d <= 64) return run<bf16, 64, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
-        if (d <= 96) return run<bf16, 96, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
-        if (d <= 128) return run<bf16, 128, 64, 2, 2>(a, prefix, direct, flops, bytes, s);
-        if (d <= 192) return run<bf16, 192, 32, 2, 2>(a, prefix, direct, flops, bytes, s);
-        return run<bf16, 256, 32, 2, 1>(a, prefix, direct, flops, bytes, s);
+template <typename T, int DP, int BN, int MT, int WPE>
+int run_direct(const Call& c) {
+    return c.p->dim < DP ? run<T, DP, BN, MT, WPE, PADDED>(c) : run<T, DP, BN, MT, WPE, FULL>(c);
+}
+
+int run_any(const Call& c) {
+    const int d = c.p->dim;
+    if (c.p->dtype == MU_BF16) {
+        if (!c.direct)
+            return d <= 64 ? run<bf16, 64, 32, 1, 2, RAGGED>(c) : d <= 128 ? run<bf16, 128, 32, 1, 2, RAGGED>(c)
+                                                                          : run<bf16, 256, 32, 1, 1, RAGGED>(c);
+        if (d <= 32) return run_direct<bf16, 32, 64, 2, 2>(c);
+        if (d <= 64) return run_direct<bf16, 64, 64, 2, 2>(c);
+        if (d <= 96) return run_direct<bf16, 96, 64, 2, 2>(c);
+        if (d <= 128) return run_direct<bf16, 128, 64, 2, 2>(c);
+        if (d <= 192) return run_direct<bf16, 192, 32, 2, 2>(c);
+        return run_direct<bf16, 256, 32, 2, 1>(c);
     }
-    if (d <= 32) return run<float, 32, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 64) return run<float, 64, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 96) return run<float, 96, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 128) return run<float, 128, 32, 1, 2>(a, prefix, direct, flops, bytes, s);
-    if (d <= 192) return run<float, 192, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
-    return run<float, 256, 32, 1, 1>(a, prefix, direct, flops, bytes, s);
+    if (!c.direct)
+        return d <= 64 ? run<float, 64, 32, 1, 2, RAGGED>(c) : d <= 128 ? run<float, 128, 32, 1, 2, RAGGED>(c)
+                                                                       : run<float, 256, 32, 1, 1, RAGGED>(c);
+    if (d <= 32) return run_direct<float, 32, 32, 1, 2>(c);
+    if (d <= 64) return run_direct<float, 64, 32, 1, 2>(c);
+    if (d <= 96) return run_direct<float, 96, 32, 1, 2>(c);
+    if (d <= 128) return run_direct<float, 128, 32, 1, 2>(c);
+    if (d <= 192) return run_direct<float, 192, 32, 1, 1>(c);
+    return run_direct<float, 256, 32, 1, 1>(c);
 }
 
 int check(const mu_qk_logits* a) {
@@ -578,7 +594,7 @@ int check(const mu_qk_logits* a) {
 // (the smallest tiles of the type's instances: a call that needs none by these
 // counts needs none by its own)
 size_t qk_workspace(const mu_qk_logits* a) {
-    const bool few = most_tiles(a, a->dtype == MU_BF16 ? 256 : 128, 32) <= BY_HEAD;
+    const bool few = most_tiles(a, 128, 32) <= BY_HEAD;
     return few ? 0 : align_up(sizeof(int64_t) * ((size_t)a->batch + 1));
 }
 
@@ -616,7 +632,7 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* str
         const double nb = a->cu_q ? 1 : a->batch;
         const double bytes = nb * a->dim * es * ((double)a->q_len * a->q_heads + (double)a->k_len * a->k_heads);
         const double flops = 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
-        return run_any(a, (int64_t*)ws, direct, flops, bytes, (hipStream_t)stream);
+        return run_any(Call{a, (int64_t*)ws, direct, flops, bytes, (hipStream_t)stream});
     });
 }
 

@@ -250,6 +250,62 @@ def test_empty_calls():
     assert nso.qk_max_logits(q, q, cu_seqlens=cu).tolist() == [0.0] * 3
 
 
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 72), (BF, 50), (BF, 256), (FP, 64), (FP, 33)])
+def test_heads_of_few_keys(dtype, d):
+    """Calls so short that a workgroup takes a whole head: sequences of lengths 0
+    and 1 among them, first, last and all empty, into fresh and kept maxima, and
+    captured with lengths that change."""
+    import newton_schulz_orthogonalized_amd as nso
+    q, k = _qk(4, 30, 32, 6, 3, d, dtype, 89400 + d)
+    print(f"[qkmax] few keys {dtype} {d}", flush=True)
+    first = torch.full((6,), 0.25, device="cuda")
+    out = torch.zeros(6, device="cuda")
+    lens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    nso.qk_max_logits(q, k, lengths=lens, out=out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nso.qk_max_logits(q, k, lengths=lens, out=out)
+    for lq in ([0, 0, 0, 0], [0, 30, 0, 0], [1, 0, 0, 30], [0, 0, 0, 1], [30, 1, 17, 30]):
+        lens.copy_(torch.tensor(lq, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for causal in (True, False):
+            seqs = _dense(q, k, lq, lq)
+            got = nso.qk_max_logits(q, k, causal=causal, lengths=lens)
+            torch.cuda.synchronize()
+            _agree(got, seqs, 2, d ** -0.5, causal, d)
+            if causal:
+                assert torch.equal(got, out)
+            kept = nso.qk_max_logits(q, k, causal=causal, lengths=lens, out=first.clone(), accumulate=True)
+            assert torch.equal(kept, torch.maximum(first, got))
+    cu = torch.tensor([0, 0, 7, 7, 24], dtype=torch.int32, device="cuda")
+    got = nso.qk_max_logits(q[0], k[0, :30], cu_seqlens=cu)
+    torch.cuda.synchronize()
+    _agree(got, [(to_np(q[0, a:b]), to_np(k[0, a:b])) for a, b in ((0, 7), (7, 24))], 2, d ** -0.5, True, d)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("d", [50, 100, 190])
+def test_rows_at_odd_addresses(d, dtype):
+    """Rows that do not begin at 16-byte pieces, over many query and key tiles."""
+    import newton_schulz_orthogonalized_amd as nso
+    q, k = _qk(2, 700, 650, 4, 2, d, dtype, 89500 + d)
+    for causal in (True, False):
+        got = nso.qk_max_logits(q, k, causal=causal)
+        torch.cuda.synchronize()
+        _agree(got, _dense(q, k), 2, d ** -0.5, causal, d)
+
+
+def test_more_workgroups_than_tiles():
+    """Runs of the work that end before, in and behind a head's first tile."""
+    import newton_schulz_orthogonalized_amd as nso
+    for n, hq in ((33, 511), (65, 97), (200, 65), (257, 40), (300, 13)):
+        q, k = _qk(1, n, n, hq, 1, 64, BF, 89600 + n)
+        got = nso.qk_max_logits(q, k)
+        torch.cuda.synchronize()
+        _agree(got, _dense(q, k), hq, 0.125, True, 64)
+
+
 def test_long_sequence_against_blocks():
     """A long sequence with many key blocks for each query block."""
     import newton_schulz_orthogonalized_amd as nso
