@@ -37,10 +37,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // one line (head slowest, then sequence, query tile, key tile), each query tile
 // with COST more places in front for what it costs to begin and to end at the
 // border, and every workgroup takes an equal run of the line, wherever that
-// starts and ends.
+// starts and ends. COST in tiles of bfloat16 and of float32, which take about
+// three times as long: 6 and 2, the best of 1, 2, 3, 6 and 12 (8192 tokens,
+// 16 heads of 64: 66, 62, 62, 59, 61 us; 4 x 1024 tokens, 12 heads of 64 in
+// float32: 37.4, 37.2, 38.4, 42.4, 51.4 us).
+template <typename T> constexpr int COST_OF = sizeof(T) == 2 ? 6 : 2;
 struct QkMaxArgs {
     mu_qk_logits p;
-    const int64_t* prefix;   // [batch + 1] places of one head before each sequence; null: see BY_HEAD
+    const int64_t* prefix;   // [batch + 1] places of one head before each sequence; null: a workgroup takes a head
 };
 
 struct Seq {
@@ -72,8 +76,7 @@ __device__ inline Seq seq_of(const mu_qk_logits& A, int64_t b) {
 // Key tiles of a sequence and head. Query tile t < last sees (t + 1) BM + nk - nq
 // keys (causal), so (t + 1) BM / BN + o tiles with o = ceil((nk - nq) / BN) from
 // the first t that sees any; the last one sees all keys.
-constexpr int COST = 6;
-template <int BM, int BN>
+template <int BM, int BN, int COST>
 struct Tiles {
     int t0, last, all;   // first and last query tile with keys, tiles of all keys
     int o;
@@ -96,13 +99,9 @@ struct Tiles {
     __device__ int64_t total() const { return last < 0 ? 0 : before(last) + COST + all; }
 };
 
-// With no more key tiles than this in a head, a workgroup takes all of one: it
-// needs no plan and stores its maximum itself, one launch instead of two.
-constexpr int BY_HEAD = 4;
-
 // One workgroup: the places before each sequence, and zeros to take maxima from.
 constexpr int PLAN_THR = 1024;
-template <int BM, int BN>
+template <int BM, int BN, int COST>
 __global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* prefix) {
     __shared__ int64_t wsum[PLAN_THR / 64];
     const int tid = threadIdx.x;
@@ -111,7 +110,7 @@ __global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* pref
     int64_t carry = 0;
     for (int64_t b0 = 0; b0 < A.p.batch; b0 += PLAN_THR) {
         const int64_t b = b0 + tid;
-        int64_t n = b < A.p.batch ? Tiles<BM, BN>(seq_of(A.p, b), A.p.causal != 0).total() : 0;
+        int64_t n = b < A.p.batch ? Tiles<BM, BN, COST>(seq_of(A.p, b), A.p.causal != 0).total() : 0;
         for (int off = 1; off < 64; off <<= 1) {
             const int64_t up = __shfl_up(n, off, 64);
             if ((tid & 63) >= off) n += up;
@@ -204,7 +203,7 @@ template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
 __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     typedef typename Frag<T>::V V;
     constexpr bool DIRECT = ROWS != RAGGED;
-    constexpr int EPC = Frag<T>::EPC, NC = DP / EPC, NK = NC / 2, ROWB = NC * 16, BM = 4 * MT * 32;
+    constexpr int COST = COST_OF<T>, EPC = Frag<T>::EPC, NC = DP / EPC, NK = NC / 2, ROWB = NC * 16, BM = 4 * MT * 32;
     constexpr int GR = NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : NC % 4 == 0 ? 4 : 2;
     constexpr int SH = GR == 16 ? 0 : GR == 8 ? 1 : GR == 4 ? 2 : 3;
     constexpr int SLOTS = BN * NC;                     // chunks of a tile
@@ -275,11 +274,11 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     const bool none = P.batch == 0 || P.q_len == 0 || P.k_len == 0;   // (lengths are not read then)
     Seq S{0, 0, 0, 0};
     if (!none) S = seq_of(P, b);
-    Tiles<BM, BN> tl(S, P.causal != 0);
+    Tiles<BM, BN, COST> tl(S, P.causal != 0);
     if (by_head && !none)
         while (tl.last < 0 && ++b < P.batch) {
             S = seq_of(P, b);
-            tl = Tiles<BM, BN>(S, P.causal != 0);
+            tl = Tiles<BM, BN, COST>(S, P.causal != 0);
         }
     t = tl.t0;
     for (int n = tl.last - tl.t0 + 1; !by_head && n > 1;) {   // the query tile of place r
@@ -488,18 +487,26 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
                 b = 0, ++h;
             }
             S = seq_of(P, b);
-            tl = Tiles<BM, BN>(S, P.causal != 0);
+            tl = Tiles<BM, BN, COST>(S, P.causal != 0);
         } while (tl.last < 0);   // (not by head: a later sequence has tiles, as u < u_end)
         t = tl.t0;
     }
     flush();
 }
 
-// Key tiles of a head at most (lengths on the device may leave fewer).
-double most_tiles(const mu_qk_logits* a, int bm, int bn) {
+// Places of a head at most (lengths on the device may leave fewer).
+double most_places(const mu_qk_logits* a, int bm, int bn, int cost) {
     const double q = a->cu_q ? (double)(a->q_len / bm) + a->batch : (double)a->batch * ((a->q_len + bm - 1) / bm);
-    return a->q_len == 0 || a->k_len == 0 ? 0.0 : q * (double)((a->k_len + bn - 1) / bn);
+    return a->q_len == 0 || a->k_len == 0 ? 0.0 : q * (cost + (double)((a->k_len + bn - 1) / bn));
 }
+
+// Where a head has no more places than this, a workgroup takes all of one: it
+// needs no plan and stores its maximum itself, one launch instead of two. Whole
+// calls, with and without (16 us is two launches from the host): 12 heads of
+// 256 tokens (10 places) 13.5 and 16.1 us, 512 tokens in one workgroup (28
+// places) 13.5, but 16.8 and 16.2 with 64 heads of 128, 4 x 128 (32 places)
+// 18.6 and 16.2, in float32 4 x 64 (16 places) 17.0 and 16.2.
+constexpr int by_head_places(int cost) { return 4 * cost; }
 
 struct Call {
     const mu_qk_logits* p;
@@ -513,13 +520,13 @@ struct Call {
 template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
 int run(const Call& c) {
     constexpr int BM = 4 * MT * 32;
-    const double tiles = most_tiles(c.p, BM, BN);
+    const double places = most_places(c.p, BM, BN, COST_OF<T>);
     QkMaxArgs q{*c.p, nullptr};
     int grid = c.p->q_heads;
-    if (tiles > BY_HEAD) {
+    if (places > by_head_places(COST_OF<T>)) {
         q.prefix = c.prefix;
         int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, c.s, [&] {
-            hipLaunchKernelGGL((k_qk_plan<BM, BN>), dim3(1), dim3(PLAN_THR), 0, c.s, q, c.prefix);
+            hipLaunchKernelGGL((k_qk_plan<BM, BN, COST_OF<T>>), dim3(1), dim3(PLAN_THR), 0, c.s, q, c.prefix);
             return hipGetLastError();
         }, "max logits plan");
         if (rc) return rc;
@@ -528,7 +535,7 @@ int run(const Call& c) {
         if (rc) return rc;
         // as many workgroups as the chip holds at a time, fewer where there
         // cannot be as many tiles; the same number on each of the 8 XCDs
-        grid = (int)std::min<double>(std::max(WPE * cus / 8, 1) * 8, 8.0 * std::ceil(tiles * c.p->q_heads / 8.0));
+        grid = (int)std::min<double>(std::max(WPE * cus / 8, 1) * 8, 8.0 * std::ceil(most_places(c.p, BM, BN, 0) * c.p->q_heads / 8.0));
     }
     return timed_launch(MU_K_QKMAX, c.flops, c.bytes, c.s, [&] {
         hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, ROWS>), dim3(grid), dim3(NTHR), 0, c.s, q);
@@ -594,7 +601,8 @@ int check(const mu_qk_logits* a) {
 // (the smallest tiles of the type's instances: a call that needs none by these
 // counts needs none by its own)
 size_t qk_workspace(const mu_qk_logits* a) {
-    const bool few = most_tiles(a, 128, 32) <= BY_HEAD;
+    const int cost = a->dtype == MU_BF16 ? COST_OF<bf16> : COST_OF<float>;
+    const bool few = most_places(a, 128, 32, cost) <= by_head_places(cost);
     return few ? 0 : align_up(sizeof(int64_t) * ((size_t)a->batch + 1));
 }
 
