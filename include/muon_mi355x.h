@@ -327,7 +327,7 @@ int mu_embedding(const mu_lookup* e, void* stream);
  * gives the same bits. Rows no token names become zero (accumulate: stay).
  * Tokens outside [0, vocab) and tokens equal to padding_idx (-1: none) add
  * nothing. rows [n_tokens, dim] row_dtype, grad [vocab, dim] grad_dtype, any
- * mix of the two types. n_tokens < 2^31, vocab < 2^31.
+ * mix of the two types. n_tokens <= 2^30, vocab < 2^31.
  */
 typedef struct mu_rowgrad {
     const void* tokens;

@@ -5,9 +5,9 @@
 //   grad[v, :] = scale * sum over t with tokens[t] == v, in rising t, of rows[t, :]
 //
 // The gradient sorts the tokens (stable; tokens outside the table and the
-// padding token sort behind all others), then sums
-// the rows in sorted order: chunks of C consecutive entries, a wave for each
-// chunk and slice of columns, whatever the distribution of the tokens. A run
+// padding token sort behind all others), then sums the rows in sorted order:
+// chunks of consecutive entries, a wave for each chunk and slice of columns,
+// whatever the distribution of the tokens. A run
 // of equal tokens inside a chunk is a finished row; a run that crosses chunk
 // borders leaves a float32 partial sum in each chunk, and a last launch joins
 // them in order. Every sum's order is fixed by the tokens.
@@ -148,6 +148,7 @@ struct SortArgs {
     int32_t* key_out;
     int32_t* pos_out;
     int32_t* hist;           // [RADIX][tiles] digit counts of each tile
+    int32_t* totals;         // [RADIX] of each digit; null while every tile adds up all counts
     int n, tiles;
     int shift;               // digit of this pass
     int index_bits;          // counting: bits of a token's place
@@ -294,7 +295,7 @@ __device__ __forceinline__ int block_scan(int v, int* wsum) {
 // lane) is the items' order, and ranks taken in it are stable.
 template <int THR>
 __device__ __forceinline__ void tile_items(const SortArgs& A, uint32_t key[SORT_IPT], int pos[SORT_IPT], bool on[SORT_IPT]) {
-    const int first = blockIdx.x * (THR * SORT_IPT) + (threadIdx.x >> 6) * SORT_IPT * 64 + (threadIdx.x & 63);
+    const int first = (int)blockIdx.x * (THR * SORT_IPT) + (int)(threadIdx.x >> 6) * SORT_IPT * 64 + (int)(threadIdx.x & 63);
 #pragma unroll
     for (int i = 0; i < SORT_IPT; ++i) {
         const int j = min(first + i * 64, A.n - 1);
@@ -324,6 +325,26 @@ __global__ __launch_bounds__(THR) void k_sort_count(SortArgs A) {
     for (int i = threadIdx.x; i < RADIX; i += THR) gp(A.hist)[(int64_t)i * A.tiles + blockIdx.x] = cnt[i];
 }
 
+// Many tiles: a digit's counts become the items of the tiles before, one
+// workgroup a digit.
+constexpr int SCAN_THR = 256;
+__global__ __launch_bounds__(SCAN_THR) void k_sort_scan(SortArgs A) {
+    __shared__ int wsum[SCAN_THR / 64];
+    __shared__ int last;
+    MU_GLOBAL int32_t* h = gp(A.hist) + (int64_t)blockIdx.x * A.tiles;
+    int carry = 0;
+    for (int t0 = 0; t0 < A.tiles; t0 += SCAN_THR) {
+        const int t = t0 + (int)threadIdx.x;
+        const int c = t < A.tiles ? h[t] : 0;
+        const int before = carry + block_scan<SCAN_THR>(c, wsum);
+        if (t < A.tiles) h[t] = before;
+        if (threadIdx.x == SCAN_THR - 1) last = before + c;
+        __syncthreads();
+        carry = last;
+    }
+    if (threadIdx.x == 0) gp(A.totals)[blockIdx.x] = carry;
+}
+
 template <int THR>
 __global__ __launch_bounds__(THR) void k_sort_place(SortArgs A) {
     constexpr int WAVES = THR / 64, DPT = RADIX > THR ? RADIX / THR : 1;   // digits a thread adds up
@@ -348,11 +369,16 @@ __global__ __launch_bounds__(THR) void k_sort_place(SortArgs A) {
         const int d = tid * DPT + k;
         if (d < RADIX) {
             const MU_GLOBAL int32_t* h = gp(A.hist) + (int64_t)d * A.tiles;
+            if (A.totals) {
+                all[k] = gp(A.totals)[d];
+                mine[k] = h[blockIdx.x];
+            } else {
 #pragma unroll 8
-            for (int t = 0; t < A.tiles; ++t) {
-                const int c = h[t];
-                all[k] += c;
-                mine[k] += t < (int)blockIdx.x ? c : 0;
+                for (int t = 0; t < A.tiles; ++t) {
+                    const int c = h[t];
+                    all[k] += c;
+                    mine[k] += t < (int)blockIdx.x ? c : 0;
+                }
             }
         }
         sum += all[k];
@@ -528,7 +554,8 @@ __global__ __launch_bounds__(NTHR_SUM) void k_sum_rows(SumArgs A) {
 
 // Joins the partial sums of the runs that cross chunk borders: a workgroup for
 // the chunk in which the run starts and a slice of 64 lanes' columns; its four
-// waves take a quarter of a long run's partials each and add up in order.
+// waves take a quarter of a long run's partials each and add up in order. (Most
+// workgroups find nothing: with 16 waves each they cost 8192 chunks 33 us more.)
 template <typename TG>
 __global__ __launch_bounds__(NTHR_SUM) void k_join(SumArgs A) {
     __shared__ float q[3][64][8];
@@ -596,6 +623,7 @@ int check_rowgrad(const mu_rowgrad* e) {
     int rc = check_sizes(e->n_tokens, e->vocab, e->dim, e->token_bits, e->scale);
     if (rc) return rc;
     if (!known(e->row_dtype) || !known(e->grad_dtype)) return fail(MU_ERR_DTYPE, "unknown row or gradient dtype");
+    if (e->n_tokens > (1 << 30)) return fail(MU_ERR_INVALID_ARG, "n_tokens must be at most 2^30");
     if (e->accumulate != 0 && e->accumulate != 1) return fail(MU_ERR_INVALID_ARG, "accumulate must be 0 or 1");
     if (e->padding_idx < -1 || e->padding_idx >= e->vocab)
         return fail(MU_ERR_INVALID_ARG, "padding_idx must be -1 or in [0, vocab)");
@@ -605,8 +633,18 @@ int check_rowgrad(const mu_rowgrad* e) {
 // What a call of these sizes launches and keeps in its workspace.
 struct GradPlan {
     int n, index_bits, word_bits, passes, thr, tiles, chunk, chunks, lanes, slices;
-    size_t off_key[2], off_pos[2], off_hist, off_part, bytes;
+    bool scan;
+    size_t off_key[2], off_pos[2], off_hist, off_totals, off_part, bytes;
 };
+// Tiles from which a launch of its own adds up their counts (each tile adding
+// up all of them grows with the square): 64 tiles 67.2 us without and with,
+// 128 tiles (262144 tokens) 137 and 129, 512 tiles 583 and 470.
+constexpr int SCAN_TILES = 64;
+// Waves of the sums from which chunks grow instead: fewer partial sums, shorter
+// joins. 65536 x 4096 of which half are one token 440 us without a limit, 400,
+// 373, 371 with 8192, 4096, 2048; 2^20 x 256 uniform 237, 203, 186, 190 and with
+// half one token 711, 439, 308, 256; 2^21 x 64 343, 266, 209, 183.
+constexpr int64_t WAVES_MAX = 2048;
 GradPlan grad_plan(const mu_rowgrad* e) {
     GradPlan p;
     p.n = (int)e->n_tokens;
@@ -625,14 +663,14 @@ GradPlan grad_plan(const mu_rowgrad* e) {
     p.word_bits = bits + p.index_bits < 31 ? 32 : 64;
     const bool rank = p.n <= (p.word_bits == 32 ? 12288 : 8192);
     p.tiles = rank ? 0 : (p.n + p.thr * SORT_IPT - 1) / (p.thr * SORT_IPT);
-    // short chunks while tokens are few (more waves), longer ones as their
-    // partial sums would pass 64 MB
-    p.chunk = 16;
-    while (p.chunk < 1024 && 8.0 * (double)e->dim * (p.n / p.chunk) > (double)(64 << 20)) p.chunk *= 2;
-    p.chunks = (p.n + p.chunk - 1) / p.chunk;
+    p.scan = p.tiles > SCAN_TILES;
     p.lanes = 64;
     while (p.lanes > 1 && (int64_t)p.lanes / 2 * 8 >= e->dim) p.lanes /= 2;
     p.slices = (int)((e->dim + (int64_t)p.lanes * 8 - 1) / (p.lanes * 8));
+    // short chunks while tokens are few (more waves)
+    p.chunk = 16;
+    while (p.chunk < 1024 && (int64_t)(p.n / p.chunk) * p.slices * p.lanes / 64 > WAVES_MAX) p.chunk *= 2;
+    p.chunks = (p.n + p.chunk - 1) / p.chunk;
     size_t o = 0;
     auto take = [&](size_t n) {
         const size_t at = o;
@@ -645,6 +683,7 @@ GradPlan grad_plan(const mu_rowgrad* e) {
         p.off_pos[k] = take(n);
     }
     p.off_hist = take(p.tiles > 0 ? sizeof(int32_t) * RADIX * (size_t)p.tiles : 0);
+    p.off_totals = take(p.scan ? sizeof(int32_t) * RADIX : 0);
     p.off_part = take(p.chunks > 1 ? sizeof(float) * 2 * (size_t)p.chunks * (size_t)e->dim : 0);
     p.bytes = o;
     return p;
@@ -685,6 +724,7 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
     a.n = p.n;
     a.tiles = p.tiles;
     a.hist = (int32_t*)(ws + p.off_hist);
+    a.totals = p.scan ? (int32_t*)(ws + p.off_totals) : nullptr;
     int out = 0;   // the buffer that holds the sorted keys at the end
     if (p.tiles == 0) {
         a.key_out = (int32_t*)(ws + p.off_key[0]);
@@ -706,6 +746,12 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
             a.pos_out = (int32_t*)(ws + p.off_pos[out]);
             const bool few = p.thr == 256;
             int rc = sort_launch(few ? k_sort_count<256> : k_sort_count<1024>, a, p.tiles, p.thr, 0, 8.0 * p.n);
+            if (rc) return rc;
+            if (p.scan)
+                rc = timed_launch(MU_K_ROWGRAD, 0.0, 8.0 * RADIX * p.tiles, s, [&] {
+                    hipLaunchKernelGGL(k_sort_scan, dim3(RADIX), dim3(SCAN_THR), 0, s, a);
+                    return hipGetLastError();
+                }, "embedding gradient sort launch");
             if (rc) return rc;
             rc = sort_launch(few ? k_sort_place<256> : k_sort_place<1024>, a, p.tiles, p.thr, 0, 16.0 * p.n);
             if (rc) return rc;

@@ -102,6 +102,7 @@ def _rowgrad(lib, ws=A + (4 << 30), nb=1 << 30, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(tokens=None), 1), (dict(rows=None), 1), (dict(grad=None), 1), (dict(n_tokens=-1), 1), (dict(vocab=0), 1),
+    (dict(n_tokens=(1 << 30) + 1), 1),
     (dict(dim=0), 1), (dict(padding_idx=16), 1), (dict(padding_idx=-2), 1), (dict(accumulate=2), 1),
     (dict(scale=float("nan")), 1), (dict(row_dtype=3), 2), (dict(grad_dtype=3), 2), (dict(token_bits=8), 2),
     (dict(rows=A + (1 << 30) + 1), 3), (dict(grad=A + (2 << 30) + 2), 3), (dict(grad=A + (1 << 30)), 3),
