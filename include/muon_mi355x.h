@@ -43,7 +43,8 @@
  * block with a Gram and an apply per step (read whenever a call or a query plans).
  *
  * Layout rules common to every entry point:
- *   - every tensor is dense, row-major, with no padding between rows;
+ *   - every tensor is dense, row-major, with no padding between rows (q and k
+ *     of mu_qk_max_logits have strides);
  *   - parameter, gradient and state buffers of one entry must not overlap each
  *     other or any other entry's buffers;
  *   - bfloat16 buffers are 2-byte aligned, float32 buffers 4-byte aligned (16-

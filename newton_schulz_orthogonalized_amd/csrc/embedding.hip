@@ -805,13 +805,14 @@ int mu_embedding(const mu_lookup* e, void* stream) {
         if (ranges_overlap(in) || ranges_overlap(tk)) return fail(MU_ERR_LAYOUT, "out overlaps an input");
         hipStream_t s = (hipStream_t)stream;
         const double bytes = (double)e->n_tokens * (2.0 * (double)e->dim * es + e->token_bits / 8);
+        LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es > (double)(32 << 20)};
+        const int epv = (int)(16 / es);
+        while (a.lanes > 1 && (int64_t)a.lanes / 2 * epv >= e->dim) a.lanes /= 2;
+        a.slices = (int)((e->dim + (int64_t)a.lanes * epv - 1) / (a.lanes * epv));
+        const int64_t groups = (e->n_tokens + TOK - 1) / TOK * a.slices, per = NTHR / a.lanes, wgs = (groups + per - 1) / per;
+        if (wgs > 0xffffffffLL / NTHR) return fail(MU_ERR_INVALID_ARG, "too many tokens for one launch at this dim");
         return timed_launch(MU_K_LOOKUP, 0.0, bytes, s, [&] {
-            LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es > (double)(32 << 20)};
-            const int epv = (int)(16 / es);
-            while (a.lanes > 1 && (int64_t)a.lanes / 2 * epv >= e->dim) a.lanes /= 2;
-            a.slices = (int)((e->dim + (int64_t)a.lanes * epv - 1) / (a.lanes * epv));
-            const int64_t groups = (e->n_tokens + TOK - 1) / TOK * a.slices, per = NTHR / a.lanes;
-            const dim3 grid((unsigned)((groups + per - 1) / per)), block(NTHR);
+            const dim3 grid((unsigned)wgs), block(NTHR);
             if (e->dtype == MU_BF16) {
                 if (e->scale == 1.f) hipLaunchKernelGGL((k_lookup<bf16, false>), grid, block, 0, s, a);
                 else hipLaunchKernelGGL((k_lookup<bf16, true>), grid, block, 0, s, a);

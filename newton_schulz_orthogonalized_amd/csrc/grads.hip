@@ -204,7 +204,8 @@ __global__ __launch_bounds__(NTHR) void k_norm_final(NormOut N) {
     norm_out(N, sum_partials(N, red), threadIdx.x == 0);
 }
 
-// A chunk times c, all loads before the first store. Bound by memory: four layers
+// A chunk times c (float32, as the product before it is rounded to the output's
+// type), all loads before the first store. Bound by memory: four layers
 // and the embedding of the Llama-1B-shaped set, float32 into bfloat16, norm and
 // scaling together (2.7 GB): 478 us, 461 with the loads first, 429 with
 // non-temporal loads and stores, 417 with CLIP_WGS = 512 rather than 1024
@@ -269,8 +270,11 @@ __global__ __launch_bounds__(NTHR) void k_clip(ClipArgs A) {
 }
 
 // A few chunks in one launch of one workgroup: its four quarters take a chunk
-// each at a time, and for clipping read theirs again from the caches.
-constexpr int FEW_CHUNKS = 16, FEW_THR = 4 * NTHR;
+// each at a time, and for clipping read theirs again from the caches. Whole
+// calls on one float32 tensor, in one launch and in two: norm of 16 chunks 11.8
+// and 14.2 us, of 32 11.8 and 14.3, of 64 26.2 and 14.3; clipping of 12 chunks
+// 12.9 and 15.8, of 16 17.3 and 15.7, of 32 32.1 and 15.8.
+constexpr int FEW_NORM = 32, FEW_CLIP = 12, FEW_THR = 4 * NTHR;
 template <bool CLIP>
 __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     __shared__ double red[FEW_THR / 64];
@@ -383,7 +387,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         a.chunks = (int)c;
         return bytes;
     };
-    if (bs.size() == 1 && bs[0].chunks <= FEW_CHUNKS && bs[0].items.size() <= (size_t)CLIP_SEGS) {
+    if (bs.size() == 1 && bs[0].chunks <= (clip ? FEW_CLIP : FEW_NORM) && bs[0].items.size() <= (size_t)CLIP_SEGS) {
         ClipArgs a;
         const double bytes = clip_args(bs[0], a);
         a.no = NormOut{nullptr, 0, max_norm, eps, norm_out, scale_out};

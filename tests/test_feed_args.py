@@ -81,6 +81,7 @@ def _lookup(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(tokens=None), 1), (dict(weight=None), 1), (dict(out=None), 1), (dict(n_tokens=-1), 1), (dict(n_tokens=1 << 31), 1),
+    (dict(n_tokens=1 << 29, dim=1 << 20, weight=1 << 52, out=1 << 53), 1),
     (dict(vocab=0), 1), (dict(dim=0), 1), (dict(dim=(1 << 21) + 1), 1), (dict(scale=float("inf")), 1), (dict(token_bits=16), 2),
     (dict(dtype=5), 2), (dict(tokens=A + 4), 3), (dict(weight=A + (1 << 30) + 1), 3), (dict(out=A + (1 << 30) + 64), 3),
     (dict(out=A), 3),

@@ -89,6 +89,17 @@ def test_below_the_bound_keeps_the_gradients(size):
     _check(g, 1e3, o)
 
 
+@pytest.mark.parametrize("chunks", [11, 12, 13, 31, 32, 33, 34])
+def test_around_the_sizes_of_one_workgroup(chunks):
+    import newton_schulz_orthogonalized_amd as nso
+    for sizes in ([8192 * chunks], [8192 * chunks - 5], [5] + [8192] * (chunks - 1), [8192 * (chunks - 1) - 1, 3, 1]):
+        g = _list(sizes, [(FP, BF)[i % 2] for i in range(len(sizes))], 52100, shift=1)
+        want = F.grad_norm_ref([to_np(x) for x in g])
+        assert abs(float(nso.grad_norm(g)) - want) <= want * ULP * 1.001
+        _check(g, want / 2, _list(sizes, [FP] * len(sizes), 52200))
+        _check(g, want / 2, None)
+
+
 def test_norm_of_many_tensors_and_beyond_one_launch():
     """More tensors than one launch takes, single elements among them, and the
     same tensor twice (it counts twice)."""
