@@ -49,7 +49,8 @@ def _check(grads, max_norm, outs, eps=1e-6):
     norm = nso.clip_grads(grads, max_norm, outs=outs, eps=eps, scale_out=scale)
     torch.cuda.synchronize()
     want = F.grad_norm_ref(host)
-    c = F.clip_scale_ref(want, max_norm, eps)
+    # the bounds are float32 arguments: 0.2524.. itself is up to 2^-24 away from the one the call takes
+    c = F.clip_scale_ref(want, float(np.float32(max_norm)), float(np.float32(eps)))
     assert abs(float(norm) - want) <= want * ULP * 1.001
     assert abs(float(scale) - c) <= c * ULP * 1.001
     for h, o in zip(host, grads if outs is None else outs):
