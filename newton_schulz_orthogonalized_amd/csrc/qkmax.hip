@@ -107,6 +107,7 @@ __global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* pref
     const int tid = threadIdx.x;
     if (!A.p.accumulate)
         for (int i = tid; i < A.p.q_heads; i += PLAN_THR) gp(A.p.max_logit)[i] = 0.f;
+    if (!A.p.cu_q && !A.p.q_lengths && !A.p.k_lengths) return;   // not read then
     int64_t carry = 0;
     for (int64_t b0 = 0; b0 < A.p.batch; b0 += PLAN_THR) {
         const int64_t b = b0 + tid;
@@ -199,6 +200,13 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 //
 // Rows past the end of a sequence read its last row again, which cannot change
 // a maximum; only tiles that the causal border crosses test each pair.
+//
+// Bound by the matrix instructions: 8192 tokens, 32 heads of 128 on 8 key heads,
+// causal, take 203-219 us, 1.25-1.35 PFLOP/s of the visible pairs (a library
+// product of 8192^3 reaches 1.19 on the same card; the clock falls under this
+// load). float32 reaches 127 TFLOP/s at 4096 tokens, 12 heads of 64 (library
+// product 153). Short sequences are bound by what a query tile costs to begin:
+// 23 packed sequences of 16384 tokens, 16 heads of 128, 64 us, 0.72 PFLOP/s.
 template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
 __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     typedef typename Frag<T>::V V;
@@ -252,7 +260,14 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     int64_t u = 0, u_end = (int64_t)1 << 60, r = 0, b = 0;
     int h = blockIdx.x, t = 0;
     if (!by_head) {
-        const int64_t per_head = uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
+        // sequences of one length need no prefix; otherwise the first 64
+        // candidates of the search below are asked for with the total
+        const bool alike = !P.cu_q && !P.q_lengths && !P.k_lengths;
+        const int64_t each = alike ? Tiles<BM, BN, COST>(seq_of(P, 0), P.causal != 0).total() : 0;
+        int64_t st = (P.batch + 63) / 64, cand = 0;
+        const int64_t at = min<int64_t>(st * lane, P.batch - 1);
+        if (!alike) cand = gp(A.prefix)[at];
+        const int64_t per_head = alike ? each * P.batch : uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
         // XCD x takes places [x * total / 8, (x + 1) * total / 8), so few key heads
         const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3, w_in = blockIdx.x >> 3;
         const int64_t x_lo = total * xcd / 8, x_n = total * (xcd + 1) / 8 - x_lo;
@@ -262,14 +277,23 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         h = (int)(u / per_head);
         r = u - h * per_head;   // place in the head
         // its sequence: the last one that starts at or before r, 64 candidates at a time
-        for (int64_t n = P.batch; n > 1;) {
-            const int64_t st = (n + 63) / 64, at = b + min<int64_t>(st * lane, n - 1);
-            const int k = __popcll(__ballot(lane * st < n && gp(A.prefix)[at] <= r));   // >= 1
-            b += (k - 1) * st;
-            n = min<int64_t>(st, n - (k - 1) * st);
+        int64_t before = 0;
+        if (alike) {
+            b = r / each;
+            before = b * each;
+        } else {
+            for (int64_t n = P.batch; n > 1;) {
+                const int k = __popcll(__ballot(lane * st < n && cand <= r));   // >= 1
+                before = uni64(__shfl(cand, k - 1, 64));
+                b += (k - 1) * st;
+                n = min<int64_t>(st, n - (k - 1) * st);
+                st = (n + 63) / 64;
+                const int64_t next = b + min<int64_t>(st * lane, n - 1);
+                if (n > 1) cand = gp(A.prefix)[next];
+            }
+            b = uni64(b);
         }
-        b = uni64(b);
-        r -= uni64(gp(A.prefix)[b]);
+        r -= before;
     }
     const bool none = P.batch == 0 || P.q_len == 0 || P.k_len == 0;   // (lengths are not read then)
     Seq S{0, 0, 0, 0};
@@ -508,6 +532,15 @@ double most_places(const mu_qk_logits* a, int bm, int bn, int cost) {
 // 18.6 and 16.2, in float32 4 x 64 (16 places) 17.0 and 16.2.
 constexpr int by_head_places(int cost) { return 4 * cost; }
 
+// Up to so many tiles for each of the workgroups that the chip holds (all keys
+// counted for every query) one workgroup a compute unit is as fast or faster:
+// there the chain of loads before the first tile is what a run waits for. Whole
+// calls, with as many as the chip holds and with one: float32, 12 heads of 64,
+// 1024 tokens (6 tiles) 17.6 and 16.3 us, 16 heads of 128 (8 tiles) 29.8 and
+// 27.7; bfloat16, 16 heads of 128, 2048 tokens (8 tiles) 17.1 and 16.0; but 4 x
+// 1024 tokens, 32 heads of 64 (16 tiles) 17.3 and 19.7, float32 12 heads (24
+// tiles) 35.5 and 36.6.
+constexpr int FEW_TILES = 12;
 struct Call {
     const mu_qk_logits* p;
     int64_t* prefix;
@@ -533,9 +566,12 @@ int run(const Call& c) {
         int cus = 0;
         rc = cu_count(&cus);
         if (rc) return rc;
-        // as many workgroups as the chip holds at a time, fewer where there
-        // cannot be as many tiles; the same number on each of the 8 XCDs
-        grid = (int)std::min<double>(std::max(WPE * cus / 8, 1) * 8, 8.0 * std::ceil(most_places(c.p, BM, BN, 0) * c.p->q_heads / 8.0));
+        // as many workgroups as the chip holds at a time, one a compute unit
+        // where that leaves them few tiles, fewer where there cannot be as many
+        // tiles; the same number on each of the 8 XCDs
+        const double tiles = most_places(c.p, BM, BN, 0) * c.p->q_heads;
+        const int wgs = std::max(cus * (tiles <= (double)FEW_TILES * WPE * cus ? 1 : WPE) / 8, 1) * 8;
+        grid = (int)std::min<double>(wgs, 8.0 * std::ceil(tiles / 8.0));
     }
     return timed_launch(MU_K_QKMAX, c.flops, c.bytes, c.s, [&] {
         hipLaunchKernelGGL((k_qkmax<T, DP, BN, MT, WPE, ROWS>), dim3(grid), dim3(NTHR), 0, c.s, q);
@@ -548,6 +584,15 @@ int run_direct(const Call& c) {
     return c.p->dim < DP ? run<T, DP, BN, MT, WPE, PADDED>(c) : run<T, DP, BN, MT, WPE, FULL>(c);
 }
 
+// The instances. bfloat16: 64 rows a wave, as a key read from LDS then feeds two
+// matrix instructions (32 rows a wave 247 against 220 us at 8192 tokens, 32 heads
+// of 128; 128 rows and one wave a SIMD 263), 64 keys a tile while four slots of
+// them leave two workgroups a compute unit. float32 matrix instructions are so
+// long that one operand read for each suffices: 32 rows a wave and 32 keys, whose
+// finer tiles follow the causal border closer (12 heads of 64, 1024 tokens 18.6
+// against 22.5 us). RAGGED rows are read by elements, so registers are what the
+// loads in flight cost: 32 rows and 32 keys, without spills (dim 100 at 2 x 1024
+// tokens 58 us, 110 in tiles of 64 rows a wave and 64 keys).
 int run_any(const Call& c) {
     const int d = c.p->dim;
     if (c.p->dtype == MU_BF16) {
