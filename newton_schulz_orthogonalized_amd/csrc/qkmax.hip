@@ -42,9 +42,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // 16 heads of 64: 66, 62, 62, 59, 61 us; 4 x 1024 tokens, 12 heads of 64 in
 // float32: 37.4, 37.2, 38.4, 42.4, 51.4 us).
 template <typename T> constexpr int COST_OF = sizeof(T) == 2 ? 6 : 2;
+// How a workgroup finds its run: it takes all of a head; by arithmetic, as
+// sequences are of one length; from up to 64 sequences, one a lane; from the
+// places before each sequence that a launch before wrote.
+enum : int { BY_HEAD = 0, ALIKE = 1, IN_LANES = 2, PREFIX = 3 };
 struct QkMaxArgs {
     mu_qk_logits p;
-    const int64_t* prefix;   // [batch + 1] places of one head before each sequence; null: a workgroup takes a head
+    const int64_t* prefix;   // PREFIX: [batch + 1] places of one head before each sequence
+    int plan;
 };
 
 struct Seq {
@@ -99,7 +104,8 @@ struct Tiles {
     __device__ int64_t total() const { return last < 0 ? 0 : before(last) + COST + all; }
 };
 
-// One workgroup: the places before each sequence, and zeros to take maxima from.
+// One workgroup: zeros to take maxima from, and (PREFIX) the places before each
+// sequence.
 constexpr int PLAN_THR = 1024;
 template <int BM, int BN, int COST>
 __global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* prefix) {
@@ -107,7 +113,7 @@ __global__ __launch_bounds__(PLAN_THR) void k_qk_plan(QkMaxArgs A, int64_t* pref
     const int tid = threadIdx.x;
     if (!A.p.accumulate)
         for (int i = tid; i < A.p.q_heads; i += PLAN_THR) gp(A.p.max_logit)[i] = 0.f;
-    if (!A.p.cu_q && !A.p.q_lengths && !A.p.k_lengths) return;   // not read then
+    if (A.plan != PREFIX) return;
     int64_t carry = 0;
     for (int64_t b0 = 0; b0 < A.p.batch; b0 += PLAN_THR) {
         const int64_t b = b0 + tid;
@@ -256,18 +262,32 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         __syncthreads();
     }
 
-    const bool by_head = A.prefix == nullptr;
+    const int PLAN = A.plan;
+    const bool by_head = PLAN == BY_HEAD;
     int64_t u = 0, u_end = (int64_t)1 << 60, r = 0, b = 0;
     int h = blockIdx.x, t = 0;
     if (!by_head) {
-        // sequences of one length need no prefix; otherwise the first 64
-        // candidates of the search below are asked for with the total
-        const bool alike = !P.cu_q && !P.q_lengths && !P.k_lengths;
-        const int64_t each = alike ? Tiles<BM, BN, COST>(seq_of(P, 0), P.causal != 0).total() : 0;
-        int64_t st = (P.batch + 63) / 64, cand = 0;
-        const int64_t at = min<int64_t>(st * lane, P.batch - 1);
-        if (!alike) cand = gp(A.prefix)[at];
-        const int64_t per_head = alike ? each * P.batch : uni64(gp(A.prefix)[P.batch]), total = per_head * P.q_heads;
+        // places before each sequence (the first 64 candidates of the search
+        // below): of one length, of up to 64 in a wave's lanes, or from memory
+        int64_t st = (P.batch + 63) / 64, cand = 0, each = 0, per_head;
+        if (PLAN == ALIKE) {
+            each = Tiles<BM, BN, COST>(seq_of(P, 0), P.causal != 0).total();
+            per_head = each * P.batch;
+        } else if (PLAN == IN_LANES) {
+            const int64_t own = lane < P.batch ? Tiles<BM, BN, COST>(seq_of(P, lane), P.causal != 0).total() : 0;
+            cand = own;
+            for (int o = 1; o < 64; o <<= 1) {
+                const int64_t up = __shfl_up(cand, o, 64);
+                if (lane >= o) cand += up;
+            }
+            per_head = uni64(__shfl(cand, 63, 64));
+            cand -= own;
+        } else {
+            const int64_t at = min<int64_t>(st * lane, P.batch - 1);
+            cand = gp(A.prefix)[at];
+            per_head = uni64(gp(A.prefix)[P.batch]);
+        }
+        const int64_t total = per_head * P.q_heads;
         // XCD x takes places [x * total / 8, (x + 1) * total / 8), so few key heads
         const int xcd = blockIdx.x & 7, wgs = gridDim.x >> 3, w_in = blockIdx.x >> 3;
         const int64_t x_lo = total * xcd / 8, x_n = total * (xcd + 1) / 8 - x_lo;
@@ -278,7 +298,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
         r = u - h * per_head;   // place in the head
         // its sequence: the last one that starts at or before r, 64 candidates at a time
         int64_t before = 0;
-        if (alike) {
+        if (PLAN == ALIKE) {
             b = r / each;
             before = b * each;
         } else {
@@ -524,6 +544,13 @@ double most_places(const mu_qk_logits* a, int bm, int bn, int cost) {
     return a->q_len == 0 || a->k_len == 0 ? 0.0 : q * (cost + (double)((a->k_len + bn - 1) / bn));
 }
 
+// Reading the lengths in every workgroup costs less than waiting for another
+// launch to write them and then for two loads: 23 packed sequences 65.3 against
+// 66.2 us; one sequence of 1024 tokens (float32, 12 heads of 64) 17.6 against 18.8.
+int plan_of(const mu_qk_logits* a) {
+    return !a->cu_q && !a->q_lengths && !a->k_lengths ? ALIKE : a->batch <= 64 ? IN_LANES : PREFIX;
+}
+
 // Where a head has no more places than this, a workgroup takes all of one: it
 // needs no plan and stores its maximum itself, one launch instead of two. Whole
 // calls, with and without (16 us is two launches from the host): 12 heads of
@@ -554,14 +581,16 @@ template <typename T, int DP, int BN, int MT, int WPE, int ROWS>
 int run(const Call& c) {
     constexpr int BM = 4 * MT * 32;
     const double places = most_places(c.p, BM, BN, COST_OF<T>);
-    QkMaxArgs q{*c.p, nullptr};
+    QkMaxArgs q{*c.p, c.prefix, BY_HEAD};
     int grid = c.p->q_heads;
     if (places > by_head_places(COST_OF<T>)) {
-        q.prefix = c.prefix;
-        int rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, c.s, [&] {
-            hipLaunchKernelGGL((k_qk_plan<BM, BN, COST_OF<T>>), dim3(1), dim3(PLAN_THR), 0, c.s, q, c.prefix);
-            return hipGetLastError();
-        }, "max logits plan");
+        q.plan = plan_of(c.p);
+        int rc = MU_OK;
+        if (q.plan == PREFIX || !c.p->accumulate)
+            rc = timed_launch(MU_K_QKMAX, 0.0, 0.0, c.s, [&] {
+                hipLaunchKernelGGL((k_qk_plan<BM, BN, COST_OF<T>>), dim3(1), dim3(PLAN_THR), 0, c.s, q, c.prefix);
+                return hipGetLastError();
+            }, "max logits plan");
         if (rc) return rc;
         int cus = 0;
         rc = cu_count(&cus);
@@ -648,7 +677,7 @@ int check(const mu_qk_logits* a) {
 size_t qk_workspace(const mu_qk_logits* a) {
     const int cost = a->dtype == MU_BF16 ? COST_OF<bf16> : COST_OF<float>;
     const bool few = most_places(a, 128, 32, cost) <= by_head_places(cost);
-    return few ? 0 : align_up(sizeof(int64_t) * ((size_t)a->batch + 1));
+    return few || plan_of(a) != PREFIX ? 0 : align_up(sizeof(int64_t) * ((size_t)a->batch + 1));
 }
 
 }  // namespace

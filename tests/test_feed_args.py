@@ -146,7 +146,7 @@ def test_bad_qk_rejected(lib, kw, code):
 
 def test_qk_workspace_rejected(lib):
     for kw in (dict(ws=None), dict(ws=A + 8), dict(nb=16)):
-        assert _qk(lib, q_len=4096, k_len=4096, **kw) == lib.MU_ERR_WORKSPACE, kw
+        assert _qk(lib, batch=65, q_len=4096, k_len=4096, q_lengths=A, **kw) == lib.MU_ERR_WORKSPACE, kw
 
 
 def test_empty_accumulating_qk_is_nothing(lib):

@@ -296,6 +296,38 @@ def test_rows_at_odd_addresses(d, dtype):
         _agree(got, _dense(q, k), 2, d ** -0.5, causal, d)
 
 
+@pytest.mark.parametrize("batch", [1, 2, 63, 64, 65, 130, 4097])
+def test_numbers_of_sequences(batch):
+    """Padded and packed sequences of unlike lengths, empty ones among them, in
+    fresh and kept maxima."""
+    import newton_schulz_orthogonalized_amd as nso
+    d, most = 32, 300 if batch < 200 else 5
+    lens = np.clip(np.abs(host_normal((batch,), 89700 + batch)) * most / 2, 0, most).astype(int).tolist()
+    lens[-1] = most - 1
+    kept = torch.full((4,), 3.0, device="cuda")
+    edges = np.concatenate([[0], np.cumsum(lens)])
+    cu = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    q, k = _qk(1, int(edges[-1]), int(edges[-1]), 4, 2, d, BF, 89800)
+    q, k = q[0], k[0]
+    got = nso.qk_max_logits(q, k, cu_seqlens=cu)
+    both = nso.qk_max_logits(q, k, cu_seqlens=cu, out=kept.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    _agree(got, [(to_np(q[a:b]), to_np(k[a:b])) for a, b in zip(edges[:-1], edges[1:])], 2, d ** -0.5, True, d)
+    assert torch.equal(both, torch.maximum(kept, got))
+    q, k = _qk(batch, most, most, 4, 2, d, BF, 89900)
+    t = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = nso.qk_max_logits(q, k, lengths=t)
+    both = nso.qk_max_logits(q, k, lengths=t, out=kept.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    _agree(got, _dense(q, k, lens, lens), 2, d ** -0.5, True, d)
+    assert torch.equal(both, torch.maximum(kept, got))
+    got = nso.qk_max_logits(q, k, causal=False)
+    both = nso.qk_max_logits(q, k, causal=False, out=kept.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    _agree(got, _dense(q, k), 2, d ** -0.5, False, d)
+    assert torch.equal(both, torch.maximum(kept, got))
+
+
 def test_more_workgroups_than_tiles():
     """Runs of the work that end before, in and behind a head's first tile."""
     import newton_schulz_orthogonalized_amd as nso
