@@ -562,16 +562,31 @@ __global__ __launch_bounds__(NTHR_SUM) void k_join(SumArgs A) {
     const int c = blockIdx.x, i0 = c * A.chunk, i1 = i0 + A.chunk;
     if (i1 >= A.n) return;
     const MU_GLOBAL int32_t* key = (const MU_GLOBAL int32_t*)A.key;
-    const uint32_t cur = (uint32_t)key[i1 - 1];
-    if (cur >= (uint32_t)A.e.vocab || (uint32_t)key[i1] != cur) return;   // nothing goes on
-    if ((uint32_t)key[i0] == cur && i0 > 0 && (uint32_t)key[i0 - 1] == cur) return;   // started before
-    // chunks c + 1 .. end hold more of it: doubling steps, then halving
-    int lo = c + 1, step = 1;   // the run reaches chunk lo
-    while (lo + step < A.chunks && (uint32_t)key[(int64_t)(lo + step) * A.chunk] == cur) lo += step, step *= 2;
-    for (; step >= 1; step /= 2)
-        if (lo + step < A.chunks && (uint32_t)key[(int64_t)(lo + step) * A.chunk] == cur) lo += step;
-    const int n = lo - c;   // partials behind the first
     const int w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    // asked for together: the border's keys, those of the chunk's begin, and
+    // whether the run reaches each of the next 64 chunks
+    int step = 1, lo = c;   // the run reaches chunk lo
+    auto reached = [&] {   // of the chunks lo + step, lo + 2 step, ..
+        const int64_t j = min<int64_t>(lo + (int64_t)(lane + 1) * step, A.chunks - 1) * A.chunk;
+        return (uint32_t)key[j];
+    };
+    const uint32_t cur = (uint32_t)key[i1 - 1], next = (uint32_t)key[i1], begin = (uint32_t)key[i0];
+    const uint32_t ahead = (uint32_t)key[max(i0 - 1, 0)];
+    uint32_t at = reached();
+    if (cur >= (uint32_t)A.e.vocab || next != cur) return;   // nothing goes on
+    if (i0 > 0 && begin == cur && ahead == cur) return;      // started before
+    // steps of 1, 64, .. chunks while all 64 are reached, then back to 1
+    auto count = [&](uint32_t v) { return __popcll(__ballot(lo + (int64_t)(lane + 1) * step < A.chunks && v == cur)); };
+    for (int m = count(at);; m = count(reached())) {
+        lo += m * step;
+        if (m < 64) break;
+        step *= 64;
+    }
+    while (step > 1) {
+        step /= 64;
+        lo += count(reached()) * step;
+    }
+    const int n = lo - c;   // partials behind the first
     const int64_t col = ((int64_t)blockIdx.y * 64 + lane) * 8;
     const int cnt = (int)min<int64_t>(8, max<int64_t>(0, A.e.dim - col));
     const MU_GLOBAL float* part = (const MU_GLOBAL float*)A.part + col;

@@ -40,7 +40,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // starts and ends. COST in tiles of bfloat16 and of float32, which take about
 // three times as long: 6 and 2, the best of 1, 2, 3, 6 and 12 (8192 tokens,
 // 16 heads of 64: 66, 62, 62, 59, 61 us; 4 x 1024 tokens, 12 heads of 64 in
-// float32: 37.4, 37.2, 38.4, 42.4, 51.4 us).
+// float32: 37.4, 37.2, 38.4, 42.4, 51.4 us) and of 4, 6, 8, 10 and 14 (23 packed
+// sequences: 68.8, 65.9, 69.1, 70.0, 75.7 us).
 template <typename T> constexpr int COST_OF = sizeof(T) == 2 ? 6 : 2;
 // How a workgroup finds its run: it takes all of a head; by arithmetic, as
 // sequences are of one length; from up to 64 sequences, one a lane; from the
@@ -208,7 +209,7 @@ __device__ __forceinline__ float absmax3(float a, float b, float m) {
 // a maximum; only tiles that the causal border crosses test each pair.
 //
 // Bound by the matrix instructions: 8192 tokens, 32 heads of 128 on 8 key heads,
-// causal, take 203-219 us, 1.25-1.35 PFLOP/s of the visible pairs (a library
+// causal, take 203-219 us, 1.26-1.35 PFLOP/s of the visible pairs (a library
 // product of 8192^3 reaches 1.19 on the same card; the clock falls under this
 // load). float32 reaches 127 TFLOP/s at 4096 tokens, 12 heads of 64 (library
 // product 153). Short sequences are bound by what a query tile costs to begin:
