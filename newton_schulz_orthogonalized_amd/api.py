@@ -48,11 +48,17 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
         _lib.mu_muon_step_noalloc(mats, n, hp, stream)
         del keep
         return
+    _same_gpu(grad_scale, params)
     if workspace is None:
         workspace = _lib.workspace(_lib.mu_muon_workspace_size(mats, n, hp), params[0].device)
         _lib.tie_to_stream(workspace, stream)
     _lib.mu_muon_step_scaled(mats, n, hp, grad_scale, workspace, stream)
     del keep
+
+
+def _same_gpu(grad_scale: Optional[torch.Tensor], params):
+    if grad_scale is not None and grad_scale.is_cuda and params[0].is_cuda and grad_scale.device != params[0].device:
+        raise ValueError("grad_scale must be on the parameters' GPU")
 
 
 def muon_workspace_bytes(params, grads, moms, *, heads=None, ns_steps: int = 5, coeffs=None,
@@ -94,6 +100,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, weight_decay, beta1:
     ts, n = _lib.tensors(params, grads, exp_avgs, exp_avg_sqs, lrs, wds)
     if n == 0:
         return
+    _same_gpu(grad_scale, params)
     if workspace is None:
         workspace = _lib.workspace(_lib.mu_adamw_workspace_size(n), params[0].device)
         _lib.tie_to_stream(workspace, stream)

@@ -1255,10 +1255,11 @@ int check_not_capturing(hipStream_t s) {
     return MU_OK;
 }
 
-int validate_mats(const mu_matrix* m, int32_t n, std::vector<Item>& items, int& dt) {
+int validate_mats(const mu_matrix* m, int32_t n, std::vector<Item>& items, int& dt, const float* gscale = nullptr) {
     if (n < 0) return fail(MU_ERR_INVALID_ARG, "n must be >= 0");
     if (n > 0 && !m) return fail(MU_ERR_INVALID_ARG, "matrix list is null");
     std::vector<Range> ranges;
+    if (gscale) ranges.push_back({(uintptr_t)gscale, (uintptr_t)(gscale + 1), -1});
     dt = n > 0 ? m[0].dtype : MU_BF16;
     for (int i = 0; i < n; ++i) {
         const mu_matrix& x = m[i];
@@ -1486,7 +1487,7 @@ int mu_muon_step_scaled(const mu_matrix* m, int32_t n, const mu_muon_hparams* hp
         if (rc) return rc;
         std::vector<Item> items;
         int dt;
-        rc = validate_mats(m, n, items, dt);
+        rc = validate_mats(m, n, items, dt, grad_scale);
         if (rc) return rc;
         if (n == 0) return MU_OK;
         return run_call(items, hp, dt, true, ws, ws_bytes, grad_scale, (hipStream_t)stream);
@@ -1660,6 +1661,7 @@ int mu_adamw_step_scaled(const mu_tensor* ts, int32_t n, const mu_adamw_hparams*
         std::vector<AdamWDesc> d((size_t)n);
         std::vector<int64_t> prefix(1, 0);
         std::vector<Range> ranges;
+        if (grad_scale) ranges.push_back({(uintptr_t)grad_scale, (uintptr_t)(grad_scale + 1), -1});
         for (int i = 0; i < n; ++i) {
             const mu_tensor& t = ts[i];
             if (t.dtype != MU_F32 && t.dtype != MU_BF16) return fail(MU_ERR_DTYPE, "tensor %d: unknown dtype %d", i, t.dtype);

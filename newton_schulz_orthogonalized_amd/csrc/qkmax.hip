@@ -647,6 +647,18 @@ int run_any(const Call& c) {
     return run_direct<float, 256, 32, 1, 1>(c);
 }
 
+// The bytes that rows of (batch, len, heads, dim) elements at these strides span;
+// false if they pass any memory.
+bool span_of(const void* p, int64_t batch, int64_t sb, int64_t len, int64_t ss, int64_t heads, int64_t sh, int64_t dim,
+             size_t es, std::vector<Range>& out) {
+    if (batch <= 0 || len <= 0) return true;
+    const double n = (double)(batch - 1) * (double)sb + (double)(len - 1) * (double)ss + (double)(heads - 1) * (double)sh + (double)dim;
+    if (n > (double)((int64_t)1 << 50)) return false;
+    const int64_t last = (batch - 1) * sb + (len - 1) * ss + (heads - 1) * sh + dim;
+    out.push_back({(uintptr_t)p, (uintptr_t)p + (size_t)last * es, 0});
+    return true;
+}
+
 int check(const mu_qk_logits* a) {
     if (!a) return fail(MU_ERR_INVALID_ARG, "argument is null");
     if (a->dtype != MU_F32 && a->dtype != MU_BF16) return fail(MU_ERR_DTYPE, "unknown dtype %d", a->dtype);
@@ -670,6 +682,17 @@ int check(const mu_qk_logits* a) {
         !aligned(a->k_lengths, 4) || !aligned(a->cu_q, 4) || !aligned(a->cu_k, 4))
         return fail(MU_ERR_LAYOUT, "misaligned buffer");
     if (a->batch > 0 && a->q_len > 0 && a->k_len > 0 && (!a->q || !a->k)) return fail(MU_ERR_INVALID_ARG, "q or k is null");
+    // max_logit is written first, so it may lie in no input
+    std::vector<Range> in;
+    const int64_t nb = a->cu_q ? 1 : a->batch;
+    if (!span_of(a->q, nb, a->q_stride_b, a->q_len, a->q_stride_s, a->q_heads, a->q_stride_h, a->dim, es, in) ||
+        !span_of(a->k, nb, a->k_stride_b, a->k_len, a->k_stride_s, a->k_heads, a->k_stride_h, a->dim, es, in))
+        return fail(MU_ERR_INVALID_ARG, "strides are too large");
+    for (const int32_t* p : {a->q_lengths, a->k_lengths, a->cu_q, a->cu_k})
+        if (p) in.push_back({(uintptr_t)p, (uintptr_t)(p + a->batch + (a->cu_q ? 1 : 0)), 0});
+    for (const Range& r : in)
+        if (r.lo < (uintptr_t)(a->max_logit + a->q_heads) && (uintptr_t)a->max_logit < r.hi)
+            return fail(MU_ERR_LAYOUT, "max_logit overlaps an input");
     return MU_OK;
 }
 

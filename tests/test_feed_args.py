@@ -139,6 +139,9 @@ def _qk(lib, ws=A + (3 << 30), nb=1 << 20, **kw):
     (dict(causal=2), 1), (dict(accumulate=-1), 1), (dict(scale=float("nan")), 1), (dict(q_stride_s=-1), 1),
     (dict(cu_k=A), 1), (dict(cu_q=A, q_lengths=A), 1), (dict(cu_q=A, k_len=17), 1), (dict(dtype=2), 2),
     (dict(q=A + 1), 3), (dict(max_logit=A + 2), 3), (dict(q_lengths=A + 2), 3),
+    # max_logit inside q, at the end of k, among the lengths
+    (dict(max_logit=A + 64), 3), (dict(max_logit=A + (1 << 30) + 2 * (4096 + 15 * 256 + 64 + 63) - 2), 3),
+    (dict(q_lengths=A + (2 << 30) + 12), 3), (dict(q_stride_b=1 << 62), 1), (dict(k_stride_s=1 << 47), 1),
 ])
 def test_bad_qk_rejected(lib, kw, code):
     assert _qk(lib, **kw) == code
@@ -230,6 +233,21 @@ def test_marshalling_refuses_bad_shapes_and_types(lib):
         lib.grad_scale_ptr(torch.zeros(2))
     with pytest.raises(ValueError):
         lib.grad_scale_ptr(torch.zeros(()))
+
+
+def test_scaled_steps_refuse_a_factor_in_their_buffers(lib):
+    step = 1 << 30
+    mat = (lib.MuMatrix * 1)(lib.MuMatrix(A, A + step, A + 2 * step, 16, 32, lib.MU_F32, 1, 1.0, None, None))
+    ten = (lib.MuTensor * 1)(lib.MuTensor(A, A + step, A + 2 * step, A + 3 * step, 512, lib.MU_F32, 0.1, 0.0))
+    mh, keep = lib.muon_hparams(0.1, 0.0)
+    ah = lib.MuAdamwHparams(0.9, 0.95, 1e-8, 1)
+    ws, nb = A + 8 * step, 1 << 28
+    for at in (A, A + step + 64, A + 2 * step + 2044):
+        assert lib.LIB.mu_muon_step_scaled(mat, 1, ctypes.byref(mh), at, ws, nb, None) == lib.MU_ERR_LAYOUT
+        assert lib.LIB.mu_adamw_step_scaled(ten, 1, ctypes.byref(ah), at, ws, nb, None) == lib.MU_ERR_LAYOUT
+    assert lib.LIB.mu_muon_step_scaled(mat, 1, ctypes.byref(mh), A - 2, ws, nb, None) == lib.MU_ERR_LAYOUT   # misaligned
+    assert lib.LIB.mu_adamw_step_scaled(ten, 1, ctypes.byref(ah), A - 2, ws, nb, None) == lib.MU_ERR_LAYOUT
+    del keep
 
 
 def test_references_by_hand():
