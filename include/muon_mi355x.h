@@ -367,8 +367,9 @@ int mu_embedding_grad(const mu_rowgrad* e, void* workspace, size_t workspace_byt
  *           cu_q[b] .. cu_q[b+1] - 1 of q and cu_k[b] .. of k (cu_k NULL: cu_q);
  *           q_len and k_len are the packed buffers' row counts, to which the
  *           entries are clamped; stride_b and the lengths are not used
- * max_logit device float32 [q_heads] outside the inputs; accumulate = 1 keeps what is larger there
- *           (values >= 0, as this call writes), over micro-batches of a step
+ * max_logit device float32 [q_heads], outside the inputs; accumulate = 1 keeps
+ *           what is larger there (values >= 0, as this call writes), over
+ *           micro-batches of a step
  */
 #define MU_QK_MAX_DIM 256
 typedef struct mu_qk_logits {
