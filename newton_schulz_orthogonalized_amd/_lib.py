@@ -10,7 +10,6 @@ loudly when the shared library is missing.
 from __future__ import annotations
 
 import ctypes
-import itertools
 import operator
 import os
 import struct
@@ -367,7 +366,7 @@ def mu_adamw_step_scaled(ts, n, beta1: float, beta2: float, eps: float, step: in
 def device_of(tensors, what: str) -> int:
     """The index of the one GPU that all of `tensors` (None entries aside) live
     on; the current one where there is none."""
-    devs = {t.get_device() for t in tensors if t is not None}
+    devs = set(map(_Tensor.get_device, [t for t in tensors if t is not None]))
     if not devs:
         return torch.cuda.current_device()
     if min(devs) < 0:
@@ -415,7 +414,9 @@ def gradients(grads, outs=None):
         optrs, _, ocodes = _list_of(outs, "output")
         if outs is not grads and list(map(_SHAPE, outs)) != list(map(_SHAPE, grads)):
             raise ValueError("each output must have its gradient's shape")
-    return struct.pack("=" + "QQqii" * n, *itertools.chain.from_iterable(zip(ptrs, optrs, sizes, codes, ocodes))), n
+    flat = [0] * (5 * n)
+    flat[0::5], flat[1::5], flat[2::5], flat[3::5], flat[4::5] = ptrs, optrs, sizes, codes, ocodes
+    return struct.pack("=" + "QQqii" * n, *flat), n
 
 
 def mu_grad_norm_workspace_size(gs, n) -> int:
