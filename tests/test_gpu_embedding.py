@@ -133,6 +133,30 @@ def test_gradient_of_long_batches_and_large_tables(n, vocab, dim):
         _check_grad(_tokens(kind, n, vocab, n), vocab, dim, BF, FP, 72000)
 
 
+@pytest.mark.parametrize("n,vocab,dim,grad_t", [
+    (1, 300001, 256, BF), (100, 100003, 513, FP), (9000, 128256, 1024, BF), (20000, 50257, 2048, FP), (70000, 300000, 200, BF),
+    (300000, 2000003, 64, BF), (64, 70, 1 << 20, BF), (5000, 5000000, 17, FP)])
+def test_gradients_of_large_tables(n, vocab, dim, grad_t):
+    """Tables whose zeros take part of the call's time: every row that no token
+    names is zero, the others are those of a call that adds to zeros."""
+    import newton_schulz_orthogonalized_amd as nso
+    print(f"[rowgrad] table {n} {vocab} {dim}", flush=True)
+    rows = as_dtype(host_normal((n, 1), 74300), BF).cuda() * torch.arange(1, dim + 1, device="cuda").to(BF)
+    for kind in ("skewed", "outside", "sorted", "one"):
+        t = torch.from_numpy(_tokens(kind, n, vocab, n)).cuda()
+        got = torch.full((vocab, dim), float("nan"), dtype=grad_t, device="cuda")
+        guard = torch.full((vocab * dim + 64,), -3.0, dtype=grad_t, device="cuda")
+        for out in (got, guard[32:-32].view(vocab, dim)):
+            nso.embedding_grad(t, rows, vocab, out=out, scale=0.5, padding_idx=1)
+        want = nso.embedding_grad(t, rows, vocab, out=torch.zeros_like(got), scale=0.5, padding_idx=1, accumulate=True)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(got, guard[32:-32].view(vocab, dim)), kind
+        assert bool((guard[:32] == -3).all()) and bool((guard[-32:] == -3).all())
+        named = torch.zeros(vocab, dtype=torch.bool, device="cuda")
+        named[t[(t >= 0) & (t < vocab) & (t != 1)]] = True
+        assert not bool(got[~named].any()) and bool(got[named].any()) == bool(named.any())
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("padding", [None, 0, 40])
 @pytest.mark.parametrize("grad_t", [BF, FP])
