@@ -75,15 +75,19 @@ __device__ __forceinline__ void store8(MU_GLOBAL T* p, int cnt, const float v[8]
 // ---------------------------------------------------------------------------
 // Lookup. A group of `lanes` lanes copies one 16-byte piece a lane of TOK rows,
 // all loads before the first store. Bound by memory: the rows read once and the
-// output written, past the caches where it is larger than they are to any use
-// (16384 rows of 8 KB: 39.5 us, 33.2 us with non-temporal stores, 191 MB at
-// 5.7 TB/s; 8 rows a group 42.7, non-temporal loads 43.2).
+// output written (16384 rows of 8 KB: 39.5 us, 33.2 us with non-temporal stores,
+// 191 MB at 5.7 TB/s; 8 rows a group 42.7, non-temporal loads 43.2).
+//
+// Outputs of 128 MB (half the last-level cache) and more are written past the
+// caches: alone 43 and 40 us at 128 MB, 196 and 157 at 512, with a norm that reads
+// them next 110 and 113, 446 and 437. Smaller ones gain nothing alone (64 MB 21.1
+// and 20.9) and the norm finds them in the caches (48 and 54).
 // ---------------------------------------------------------------------------
 constexpr int TOK = 4;
 struct LookupArgs {
     mu_lookup e;
     int lanes, slices;
-    bool large;   // output beyond the caches
+    bool large;   // output written past the caches
 };
 template <typename T, bool SCALED>
 __global__ __launch_bounds__(NTHR) void k_lookup(LookupArgs A) {
@@ -666,8 +670,10 @@ GradPlan grad_plan(const mu_rowgrad* e) {
     int bits = 1;
     while (bits < 32 && (e->vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
     p.passes = (bits + DIGIT - 1) / DIGIT;
-    // small tiles while they are few: every tile reads all tiles' counts
-    p.thr = p.n <= (1 << 18) ? 256 : 1024;
+    // small tiles while they are few, as more workgroups hide a tile's latencies:
+    // 65536 tokens 49 us with 256 threads and 62 with 1024, 400000 101 and 114, but
+    // 2^20 126 and 118, 2^22 332 and 298
+    p.thr = p.n <= (1 << 19) ? 256 : 1024;
     // Counting or digit passes: 9000 tokens 33 against 46 us (768 columns), 12000
     // 39 against 48, 16384 51 against 48; with 64-bit words 32 against 34 at 9000
     // and 40 against 35 at 12000.
@@ -820,7 +826,7 @@ int mu_embedding(const mu_lookup* e, void* stream) {
         if (ranges_overlap(in) || ranges_overlap(tk)) return fail(MU_ERR_LAYOUT, "out overlaps an input");
         hipStream_t s = (hipStream_t)stream;
         const double bytes = (double)e->n_tokens * (2.0 * (double)e->dim * es + e->token_bits / 8);
-        LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es > (double)(32 << 20)};
+        LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es >= (double)(128 << 20)};
         const int epv = (int)(16 / es);
         while (a.lanes > 1 && (int64_t)a.lanes / 2 * epv >= e->dim) a.lanes /= 2;
         a.slices = (int)((e->dim + (int64_t)a.lanes * epv - 1) / (a.lanes * epv));

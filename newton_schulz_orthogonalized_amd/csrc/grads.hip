@@ -110,9 +110,9 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 // float32 values are exact in float64, whose additions hide behind the loads.
 // Bound by memory: every load of a chunk is in flight before the first square,
 // and non-temporal (Llama-1B-shaped set, 2.68 GB of bfloat16: 529 us with loads
-// as they come, 440 with all of a chunk's first, 393 non-temporal, 6.8 TB/s; one
-// run of chunks for each XCD 414-418, 2048 workgroups 432).
-template <typename T>
+// as they come, 440 with all of a chunk's first, 393 non-temporal (NT), 6.8 TB/s;
+// one run of chunks for each XCD 414-418, 2048 workgroups 432).
+template <bool NT, typename T>
 __device__ __forceinline__ double sumsq_chunk(const void* base, int64_t i0, int64_t n, int tid) {
     const MU_GLOBAL T* p = (const MU_GLOBAL T*)base + i0;
     constexpr int EPV = 16 / (int)sizeof(T), STEPS = GRAD_CHUNK / (NTHR * EPV);
@@ -123,8 +123,11 @@ __device__ __forceinline__ double sumsq_chunk(const void* base, int64_t i0, int6
     if (left >= GRAD_CHUNK) {
         V v[STEPS];
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k)
-            v[k] = __builtin_nontemporal_load((const MU_GLOBAL VU*)(p + (k * NTHR + tid) * EPV));
+        for (int k = 0; k < STEPS; ++k) {
+            const MU_GLOBAL VU* q = (const MU_GLOBAL VU*)(p + (k * NTHR + tid) * EPV);
+            if constexpr (NT) v[k] = __builtin_nontemporal_load(q);
+            else v[k] = *q;
+        }
 #pragma unroll
         for (int k = 0; k < STEPS; ++k)
 #pragma unroll
@@ -161,18 +164,20 @@ __device__ __forceinline__ int seg_of(const Seg* seg, int n, int c) {
     return __builtin_amdgcn_readfirstlane(before - 1);
 }
 
+template <bool NT>
 __device__ __forceinline__ double sumsq_of(const SqSeg& S, int c, int tid) {
     const int64_t i0 = (int64_t)(c - S.c0) * GRAD_CHUNK;
-    return S.dtype == DT_BF16 ? sumsq_chunk<bf16>(S.p, i0, S.n, tid) : sumsq_chunk<float>(S.p, i0, S.n, tid);
+    return S.dtype == DT_BF16 ? sumsq_chunk<NT, bf16>(S.p, i0, S.n, tid) : sumsq_chunk<NT, float>(S.p, i0, S.n, tid);
 }
 
+template <bool NT>
 __global__ __launch_bounds__(NTHR) void k_sumsq(SqArgs A) {
     __shared__ double red[4];
     double s = 0.0;
     int i = (int)blockIdx.x < A.chunks ? seg_of(A.seg, A.nseg, blockIdx.x) : 0;
     for (int c = blockIdx.x; c < A.chunks; c += gridDim.x) {
         while (i + 1 < A.nseg && A.seg[i + 1].c0 <= c) ++i;
-        s += sumsq_of(A.seg[i], c, threadIdx.x);
+        s += sumsq_of<NT>(A.seg[i], c, threadIdx.x);
     }
     s = block_sum(s, red);
     if (threadIdx.x == 0) gp(A.partials)[blockIdx.x] = s;
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(NTHR) void k_norm_final(NormOut N) {
 // scaling together (2.7 GB): 478 us, 461 with the loads first, 429 with
 // non-temporal loads and stores, 417 with CLIP_WGS = 512 rather than 1024
 // workgroups; going through the chunks backwards, last read first, gained nothing.
-template <typename TI, typename TO>
+template <bool NT, typename TI, typename TO>
 __device__ __forceinline__ void clip_chunk(const void* base, void* out, int64_t i0, int64_t n, float c, int tid) {
     const MU_GLOBAL TI* p = (const MU_GLOBAL TI*)base + i0;
     MU_GLOBAL TO* o = (MU_GLOBAL TO*)out + i0;
@@ -223,13 +228,19 @@ __device__ __forceinline__ void clip_chunk(const void* base, void* out, int64_t 
     if (left >= GRAD_CHUNK) {
         VI v[STEPS];
 #pragma unroll
-        for (int k = 0; k < STEPS; ++k) v[k] = __builtin_nontemporal_load((const MU_GLOBAL VIU*)(p + (k * NTHR + tid) * EPV));
+        for (int k = 0; k < STEPS; ++k) {
+            const MU_GLOBAL VIU* q = (const MU_GLOBAL VIU*)(p + (k * NTHR + tid) * EPV);
+            if constexpr (NT) v[k] = __builtin_nontemporal_load(q);
+            else v[k] = *q;
+        }
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
             VO r;
 #pragma unroll
             for (int e = 0; e < EPV; ++e) r[e] = (TO)(c * (float)v[k][e]);
-            __builtin_nontemporal_store(r, (MU_GLOBAL VOU*)(o + (k * NTHR + tid) * EPV));
+            MU_GLOBAL VOU* q = (MU_GLOBAL VOU*)(o + (k * NTHR + tid) * EPV);
+            if constexpr (NT) __builtin_nontemporal_store(r, q);
+            else *q = r;
         }
         return;
     }
@@ -246,18 +257,20 @@ __device__ __forceinline__ void clip_chunk(const void* base, void* out, int64_t 
     }
 }
 
+template <bool NT>
 __device__ __forceinline__ void clip_of(const ClipSeg& S, int q, float c, int tid) {
     if (c == 1.f && S.p == S.out) return;   // in place and nothing to clip
     const int64_t i0 = (int64_t)(q - S.c0) * GRAD_CHUNK;
     if (S.dtype == DT_BF16) {
-        if (S.out_dtype == DT_BF16) clip_chunk<bf16, bf16>(S.p, S.out, i0, S.n, c, tid);
-        else clip_chunk<bf16, float>(S.p, S.out, i0, S.n, c, tid);
+        if (S.out_dtype == DT_BF16) clip_chunk<NT, bf16, bf16>(S.p, S.out, i0, S.n, c, tid);
+        else clip_chunk<NT, bf16, float>(S.p, S.out, i0, S.n, c, tid);
     } else {
-        if (S.out_dtype == DT_BF16) clip_chunk<float, bf16>(S.p, S.out, i0, S.n, c, tid);
-        else clip_chunk<float, float>(S.p, S.out, i0, S.n, c, tid);
+        if (S.out_dtype == DT_BF16) clip_chunk<NT, float, bf16>(S.p, S.out, i0, S.n, c, tid);
+        else clip_chunk<NT, float, float>(S.p, S.out, i0, S.n, c, tid);
     }
 }
 
+template <bool NT>
 __global__ __launch_bounds__(NTHR) void k_clip(ClipArgs A) {
     __shared__ double red[4];
     int i = (int)blockIdx.x < A.chunks ? seg_of(A.seg, A.nseg, blockIdx.x) : 0;
@@ -265,7 +278,7 @@ __global__ __launch_bounds__(NTHR) void k_clip(ClipArgs A) {
     for (int q = blockIdx.x; q < A.chunks; q += gridDim.x) {
         while (i + 1 < A.nseg && A.seg[i + 1].c0 <= q) ++i;
         const ClipSeg S = A.seg[i];
-        clip_of(S, q, c, threadIdx.x);
+        clip_of<NT>(S, q, c, threadIdx.x);
     }
 }
 
@@ -282,7 +295,7 @@ __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     double s = 0.0;
     for (int q = quarter; q < A.chunks; q += 4) {
         const ClipSeg& S = A.seg[seg_of(A.seg, A.nseg, q)];
-        s += sumsq_of(SqSeg{S.p, S.n, S.c0, S.dtype}, q, tid);
+        s += sumsq_of<!CLIP>(SqSeg{S.p, S.n, S.c0, S.dtype}, q, tid);
     }
     s = wave_sum(s);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -294,10 +307,18 @@ __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     if constexpr (CLIP) {
         for (int q = quarter; q < A.chunks; q += 4) {
             const ClipSeg S = A.seg[seg_of(A.seg, A.nseg, q)];
-            clip_of(S, q, c, tid);
+            clip_of<false>(S, q, c, tid);
         }
     }
 }
+
+// Memory of a clipping call up to which it leaves what it touches in the caches.
+// Gradients just written, clipped, then read once more, non-temporal and not:
+// 48 MB of float32 into bfloat16 64 and 55 us, in place 70 and 60; 160 MB (240
+// with the outputs) 189 and 175, in place 211 and 191; 224 MB in place 310 and
+// 274, into bfloat16 (336) 274 and 281; 320 MB in place 452 and 489. A norm alone
+// reads past the caches: 160 MB 85 and 91 us, 96 MB 58 and 56.
+constexpr double CACHED = 256 << 20;
 
 size_t es_of(int dt) { return dt == MU_BF16 ? 2 : 4; }
 
@@ -397,6 +418,10 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
             return hipGetLastError();
         }, "gradient norm launch");
     }
+    double memory = 0;
+    for (int i = 0; i < n; ++i)
+        memory += (double)gs[i].numel * (es_of(gs[i].dtype) + (clip && gs[i].out != gs[i].grad ? es_of(gs[i].out_dtype) : 0));
+    const bool nt = !clip || memory > CACHED;
     double* part = (double*)ws;
     for (auto& b : bs) {
         SqArgs a;
@@ -414,7 +439,8 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         const int grid = wgs_of(c, SQ_WGS);
         part += grid;
         rc = timed_launch(MU_K_GRADNORM, 0.0, bytes, s, [&] {
-            hipLaunchKernelGGL(k_sumsq, dim3(grid), dim3(NTHR), 0, s, a);
+            if (nt) hipLaunchKernelGGL(k_sumsq<true>, dim3(grid), dim3(NTHR), 0, s, a);
+            else hipLaunchKernelGGL(k_sumsq<false>, dim3(grid), dim3(NTHR), 0, s, a);
             return hipGetLastError();
         }, "gradient norm launch");
         if (rc) return rc;
@@ -435,7 +461,8 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         a.no = no;
         const int grid = wgs_of(a.chunks, CLIP_WGS);
         rc = timed_launch(MU_K_CLIP, 0.0, bytes, s, [&] {
-            hipLaunchKernelGGL(k_clip, dim3(grid), dim3(NTHR), 0, s, a);
+            if (nt) hipLaunchKernelGGL(k_clip<true>, dim3(grid), dim3(NTHR), 0, s, a);
+            else hipLaunchKernelGGL(k_clip<false>, dim3(grid), dim3(NTHR), 0, s, a);
             return hipGetLastError();
         }, "clip launch");
         if (rc) return rc;

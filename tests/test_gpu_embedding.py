@@ -126,7 +126,7 @@ def test_gradient(n, vocab, dim, kind, row_t, grad_t, bits):
 @pytest.mark.parametrize("n,vocab,dim", [
     (8192, 5000, 8), (8192, 1 << 19, 2), (8193, 1 << 19, 2), (12288, 3000, 8), (12289, 3000, 8), (16383, 5000, 16),
     (16384, 300000, 8), (16385, 5000, 24), (40000, 70000, 8), (70000, 9, 16), (100003, 131072, 3), (20000, 1 << 19, 2),
-    (33000, 1 << 20, 1), (131073, 5000, 2), (262144, 300, 600), (262145, 5000, 2), (600001, 40000, 3), (2200001, 70, 1)])
+    (33000, 1 << 20, 1), (131073, 5000, 2), (262144, 300, 600), (262145, 5000, 2), (524288, 40000, 3), (524289, 40000, 3), (2200001, 70, 1)])
 def test_gradient_of_long_batches_and_large_tables(n, vocab, dim):
     print(f"[rowgrad] long {n} {vocab} {dim}", flush=True)
     for kind in ("skewed", "outside", "one") if n < 1 << 20 else ("outside",):

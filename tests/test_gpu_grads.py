@@ -101,6 +101,29 @@ def test_around_the_sizes_of_one_workgroup(chunks):
         _check(g, want / 2, None)
 
 
+@pytest.mark.parametrize("types,where", [((FP, FP), "in_place"), ((FP, BF), "other"), ((BF, BF), "other")])
+def test_lists_beyond_the_caches(types, where):
+    """More than 256 MB, at odd elements and sizes; the reference on the GPU, in
+    float64 for the norm, and the one float32 product and rounding exactly."""
+    import newton_schulz_orthogonalized_amd as nso
+    g = []
+    for n in (8192, 50_000_001, 41_234_567, 7):
+        x = torch.zeros(n + 3, dtype=types[0], device="cuda")[3:]
+        i = torch.arange(n, device="cuda", dtype=torch.int64)
+        x.copy_(((i * 7919) % 2003 - 1001).float() / 4096)
+        g.append(x)
+    want = math.sqrt(sum(float(x.double().square().sum()) for x in g))
+    outs = None if where == "in_place" else [torch.zeros(x.numel() + 1, dtype=types[1], device="cuda")[1:] for x in g]
+    keep = [x.clone() for x in g]
+    scale = torch.zeros((), device="cuda")
+    norm = nso.clip_grads(g, 3.0, outs=outs, scale_out=scale)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - want) <= want * ULP * 1.001 and float(scale) < 1.0
+    for k, x, o in zip(keep, g, g if outs is None else outs):
+        assert torch.equal(o, (k.float() * scale).to(o.dtype))
+        assert outs is None or torch.equal(x, k)
+
+
 def test_norm_of_many_tensors_and_beyond_one_launch():
     """More tensors than one launch takes, single elements among them, and the
     same tensor twice (it counts twice)."""
