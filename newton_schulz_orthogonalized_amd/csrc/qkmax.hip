@@ -164,7 +164,7 @@ template <> struct Frag<float> {
     }
 };
 
-// How rows lie: RAGGED element by element at any alignment and dim; PADDED and
+// How rows lie: RAGGED at any alignment and dim; PADDED and
 // FULL in whole 16-byte chunks, fewer than (exactly) the instance's width.
 enum : int { RAGGED = 0, PADDED = 1, FULL = 2 };
 
@@ -179,9 +179,14 @@ __device__ __forceinline__ typename Frag<T>::V load_chunk(const MU_GLOBAL T* row
     if constexpr (ROWS == PADDED) {
         if (c * EPC < dim) v = *(const MU_GLOBAL typename Frag<T>::V*)(row + c * EPC);
     } else {
+        // gfx950 takes global vector accesses at any address
+        typedef typename Frag<T>::V VU __attribute__((aligned(sizeof(T))));
+        if ((c + 1) * EPC <= dim) v = *(const MU_GLOBAL VU*)(row + c * EPC);
+        else if (c * EPC < dim) {
 #pragma unroll
-        for (int e = 0; e < EPC; ++e)
-            if (c * EPC + e < dim) v[e] = row[c * EPC + e];
+            for (int e = 0; e < EPC; ++e)
+                if (c * EPC + e < dim) v[e] = row[c * EPC + e];
+        }
     }
     return v;
 }
@@ -620,15 +625,16 @@ int run_direct(const Call& c) {
 // them leave two workgroups a compute unit. float32 matrix instructions are so
 // long that one operand read for each suffices: 32 rows a wave and 32 keys, whose
 // finer tiles follow the causal border closer (12 heads of 64, 1024 tokens 18.6
-// against 22.5 us). RAGGED rows are read by elements, so registers are what the
-// loads in flight cost: 32 rows and 32 keys, without spills (dim 100 at 2 x 1024
-// tokens 58 us, 110 in tiles of 64 rows a wave and 64 keys).
+// against 22.5 us). RAGGED rows pass through registers, so 32 keys a tile: dim
+// 100, 4 x 2048 tokens, 16 heads 104 us, 136 with 32 rows a wave, 463 (spilled)
+// with 64 rows and 64 keys; their whole chunks are loaded as vectors at any
+// address (dim 100, 2 x 1024 tokens, 32 rows a wave 27 us, 56 by elements).
 int run_any(const Call& c) {
     const int d = c.p->dim;
     if (c.p->dtype == MU_BF16) {
         if (!c.direct)
-            return d <= 64 ? run<bf16, 64, 32, 1, 2, RAGGED>(c) : d <= 128 ? run<bf16, 128, 32, 1, 2, RAGGED>(c)
-                                                                          : run<bf16, 256, 32, 1, 1, RAGGED>(c);
+            return d <= 64 ? run<bf16, 64, 32, 2, 2, RAGGED>(c) : d <= 128 ? run<bf16, 128, 32, 2, 2, RAGGED>(c)
+                                                                          : run<bf16, 256, 32, 2, 1, RAGGED>(c);
         if (d <= 32) return run_direct<bf16, 32, 64, 2, 2>(c);
         if (d <= 64) return run_direct<bf16, 64, 64, 2, 2>(c);
         if (d <= 96) return run_direct<bf16, 96, 64, 2, 2>(c);
