@@ -295,7 +295,7 @@ __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     double s = 0.0;
     for (int q = quarter; q < A.chunks; q += 4) {
         const ClipSeg& S = A.seg[seg_of(A.seg, A.nseg, q)];
-        s += sumsq_of<!CLIP>(SqSeg{S.p, S.n, S.c0, S.dtype}, q, tid);
+        s += sumsq_of<false>(SqSeg{S.p, S.n, S.c0, S.dtype}, q, tid);
     }
     s = wave_sum(s);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
@@ -312,12 +312,14 @@ __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     }
 }
 
-// Memory of a clipping call up to which it leaves what it touches in the caches.
-// Gradients just written, clipped, then read once more, non-temporal and not:
-// 48 MB of float32 into bfloat16 64 and 55 us, in place 70 and 60; 160 MB (240
-// with the outputs) 189 and 175, in place 211 and 191; 224 MB in place 310 and
-// 274, into bfloat16 (336) 274 and 281; 320 MB in place 452 and 489. A norm alone
-// reads past the caches: 160 MB 85 and 91 us, 96 MB 58 and 56.
+// Memory of a call up to which it leaves what it touches in the caches (256 MB
+// the last level), as the step reads it next. Gradients just written, clipped,
+// then read once more, non-temporal and not: 48 MB of float32 into bfloat16 64
+// and 55 us, in place 70 and 60; 160 MB (240 with the outputs) 189 and 175, in
+// place 211 and 191; 224 MB in place 310 and 274, into bfloat16 (336) 274 and 281;
+// 320 MB in place 452 and 489. Their norm and a reader: 32 MB 48 and 37 us, 96 MB
+// 107 and 94, 224 MB 238 and 207 (the norm alone, read again and again, 15.8 and
+// 15.7, 17.1 and 18.7, 36.7 and 37.7; 320 MB 51 and 56).
 constexpr double CACHED = 256 << 20;
 
 size_t es_of(int dt) { return dt == MU_BF16 ? 2 : 4; }
@@ -421,7 +423,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
     double memory = 0;
     for (int i = 0; i < n; ++i)
         memory += (double)gs[i].numel * (es_of(gs[i].dtype) + (clip && gs[i].out != gs[i].grad ? es_of(gs[i].out_dtype) : 0));
-    const bool nt = !clip || memory > CACHED;
+    const bool nt = memory > CACHED;
     double* part = (double*)ws;
     for (auto& b : bs) {
         SqArgs a;
