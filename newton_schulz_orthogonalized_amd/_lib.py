@@ -376,12 +376,12 @@ def device_of(tensors, what: str) -> int:
     return devs.pop()
 
 
-def scratch(nbytes: int, device: int) -> Optional[torch.Tensor]:
+def scratch(nbytes: int, device: int, stream=None) -> Optional[torch.Tensor]:
     """workspace() without the slice where the allocator's address will do."""
     if nbytes == 0:
         return None
-    buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-    return buf if buf.data_ptr() % 256 == 0 else workspace(nbytes, buf.device)
+    buf = allocate(lambda: torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device)), device, stream)
+    return buf if buf.data_ptr() % 256 == 0 else workspace(nbytes, buf.device, stream)
 
 
 _CODES = {torch.float32: MU_F32, torch.bfloat16: MU_BF16}
@@ -604,25 +604,51 @@ def mu_kernel_name(kernel: int) -> str:
     return LIB.mu_kernel_name(kernel).decode()
 
 
-def workspace(nbytes: int, device) -> Optional[torch.Tensor]:
-    """A 256-byte aligned uint8 device buffer of at least nbytes (None for 0)."""
+def workspace(nbytes: int, device, stream=None) -> Optional[torch.Tensor]:
+    """A 256-byte aligned uint8 device buffer of at least nbytes (None for 0)
+    for work on `stream` (default: the current one)."""
     if nbytes == 0:
         return None
-    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    buf = allocate(lambda: torch.empty(nbytes + 256, dtype=torch.uint8, device=device), device, stream)
     off = (-buf.data_ptr()) % 256
     return buf[off:off + nbytes]
+
+
+def torch_stream(stream, device) -> torch.cuda.Stream:
+    """A torch stream object as it is, or one for a raw hipStream_t value."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if int(stream) == 0:   # ExternalStream takes 0 for "any stream"
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+def allocate(make, device, stream, returned: bool = False):
+    """make() with `stream` current. The caching allocator hands out memory as
+    soon as its last owner has dropped it, when kernels queued on the stream of
+    that allocation may still use it: only work on the same stream comes behind
+    them. So a buffer of work on `stream` is allocated there, wherever the caller
+    works. One that is `returned` to the caller is also recorded on the caller's
+    stream, where it is read next."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(torch_stream(stream, device)):
+        buf = make()
+        if returned:
+            tie_to_stream(buf, caller)
+    return buf
 
 
 def tie_to_stream(buf: Optional[torch.Tensor], stream, current=None) -> None:
     """Keep a buffer allocated on the current stream alive for work queued on
     `stream` (a torch stream or a raw hipStream_t value): the caching
     allocator may otherwise hand its memory to the next allocation on the
-    current stream as soon as the caller drops it, while the library's kernels
-    on `stream` still read it. No-op for None or for the current stream."""
+    current stream as soon as the caller drops it, while kernels on `stream`
+    still use it. No-op for None or for the current stream."""
     if buf is None or stream is None:
         return
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=buf.device)
+    stream = torch_stream(stream, buf.device)
     cur = torch.cuda.current_stream(buf.device) if current is None else current
     if stream.cuda_stream != cur.cuda_stream:
         buf.record_stream(stream)

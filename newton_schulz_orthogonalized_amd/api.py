@@ -4,10 +4,12 @@ gradient, attention max logits).
 
 Each function marshals torch tensors into the library's descriptor lists,
 allocates the workspace the library asks for (unless one is passed in) and
-enqueues the work on `stream` (default: the current stream). A workspace
-allocated here on the current stream is recorded on `stream` when that is
-another stream, so the caching allocator does not reuse it while the library's
-kernels still read it. Nothing here computes.
+enqueues the work on `stream` (default: the current stream). Workspaces and
+results allocated here come from `stream`'s share of the caching allocator, so
+that neither the work that used their memory before nor the work that gets it
+next overlaps the library's kernels; a result is recorded on the current stream
+too. The caller orders `stream` behind what made the inputs, and its own use of
+the results behind `stream`. Nothing here computes.
 """
 
 from __future__ import annotations
@@ -50,8 +52,7 @@ def muon_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], mom
         return
     _same_gpu(grad_scale, params)
     if workspace is None:
-        workspace = _lib.workspace(_lib.mu_muon_workspace_size(mats, n, hp), params[0].device)
-        _lib.tie_to_stream(workspace, stream)
+        workspace = _lib.workspace(_lib.mu_muon_workspace_size(mats, n, hp), params[0].device, stream)
     _lib.mu_muon_step_scaled(mats, n, hp, grad_scale, workspace, stream)
     del keep
 
@@ -75,14 +76,13 @@ def orthogonalize(inputs: Sequence[torch.Tensor], *, heads: Optional[Sequence[in
                   workspace: Optional[torch.Tensor] = None, stream=None):
     """Frobenius-normalise and Newton-Schulz-orthogonalise each input (per head)."""
     if outputs is None:
-        outputs = [torch.empty_like(x) for x in inputs]
+        outputs = [_lib.allocate(lambda: torch.empty_like(x), x.device, stream, returned=True) for x in inputs]
     xs, n = _lib.orthos(inputs, outputs, heads, norm_outs)
     hp, keep = _lib.muon_hparams(0.0, 0.0, 0.95, True, norm_eps, ns_steps, coeffs, precision)
     if n == 0:
         return list(outputs)
     if workspace is None:
-        workspace = _lib.workspace(_lib.mu_ortho_workspace_size(xs, n, hp), inputs[0].device)
-        _lib.tie_to_stream(workspace, stream)
+        workspace = _lib.workspace(_lib.mu_ortho_workspace_size(xs, n, hp), inputs[0].device, stream)
     _lib.mu_muon_orthogonalize(xs, n, hp, workspace, stream)
     del keep
     return list(outputs)
@@ -102,8 +102,7 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, *, lr, weight_decay, beta1:
         return
     _same_gpu(grad_scale, params)
     if workspace is None:
-        workspace = _lib.workspace(_lib.mu_adamw_workspace_size(n), params[0].device)
-        _lib.tie_to_stream(workspace, stream)
+        workspace = _lib.workspace(_lib.mu_adamw_workspace_size(n), params[0].device, stream)
     _lib.mu_adamw_step_scaled(ts, n, beta1, beta2, eps, step, grad_scale, workspace, stream)
 
 
@@ -119,8 +118,7 @@ def qk_clip(wqs, wks, max_logits, *, q_heads, k_heads, tau: float = 100.0, gamma
     if n == 0:
         return
     if workspace is None:
-        workspace = _lib.workspace(_lib.mu_qk_clip_workspace_size(pairs, n), wqs[0].device)
-        _lib.tie_to_stream(workspace, stream)
+        workspace = _lib.workspace(_lib.mu_qk_clip_workspace_size(pairs, n), wqs[0].device, stream)
     _lib.mu_qk_clip(pairs, n, tau, workspace, stream)
 
 
@@ -135,15 +133,8 @@ def _on(device: int, stream, call, *args):
 
 
 def _new(shape, dtype, device: int, stream) -> torch.Tensor:
-    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", device))
-    _lib.tie_to_stream(t, stream)
-    return t
-
-
-def _scratch(nbytes: int, device: int, stream) -> Optional[torch.Tensor]:
-    buf = _lib.scratch(nbytes, device)
-    _lib.tie_to_stream(buf, stream)
-    return buf
+    return _lib.allocate(lambda: torch.empty(shape, dtype=dtype, device=torch.device("cuda", device)), device, stream,
+                         returned=True)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float = math.inf, eps: float = 1e-6,
@@ -177,7 +168,7 @@ def _norm(grads, outs, max_norm, eps, norm_out, scale_out, workspace, stream):
 
     def call(st):
         out = _new((), torch.float32, device, stream) if norm_out is None else norm_out
-        ws = _scratch(_lib.mu_grad_norm_workspace_size(gs, n), device, stream) if workspace is None else workspace
+        ws = _lib.scratch(_lib.mu_grad_norm_workspace_size(gs, n), device, stream) if workspace is None else workspace
         run = _lib.mu_grad_norm if outs is None else _lib.mu_clip_grads
         run(gs, n, max_norm, eps, out, scale_out, ws, st)
         return out
@@ -248,7 +239,7 @@ def embedding_grad(tokens: torch.Tensor, rows: torch.Tensor, num_embeddings: int
         if g is None:
             g = _new((num_embeddings, rows.shape[-1]), rows.dtype if dtype is None else dtype, device, stream)
         e = _lib.rowgrad(tokens, rows, g, scale, padding_idx, accumulate)
-        ws = _scratch(_lib.mu_embedding_grad_workspace_size(e), device, stream) if workspace is None else workspace
+        ws = _lib.scratch(_lib.mu_embedding_grad_workspace_size(e), device, stream) if workspace is None else workspace
         _lib.mu_embedding_grad(e, ws, st)
         return g
     return _on(device, stream, call)
@@ -281,7 +272,7 @@ def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = 
     def call(st):
         o = _new(q.shape[-2:-1], torch.float32, device, stream) if out is None else out
         a = _lib.qk_logits(q, k, o, scale, causal, lengths, k_lengths, cu_seqlens, cu_seqlens_k, accumulate)
-        ws = _scratch(_lib.mu_qk_max_logits_workspace_size(a), device, stream) if workspace is None else workspace
+        ws = _lib.scratch(_lib.mu_qk_max_logits_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_qk_max_logits(a, ws, st)
         return o
     return _on(device, stream, call)
