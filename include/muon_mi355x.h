@@ -258,6 +258,8 @@ int mu_qk_clip(const mu_qk_pair* pairs, int32_t n, float tau, void* workspace, s
  * The squares and their sum are float64 in a fixed order: no overflow or
  * underflow for any finite gradient, and the same list gives the same bits.
  * NaN anywhere makes norm and c NaN; an infinity makes norm infinite and c 0.
+ * Without a bound (max_norm = +inf) c is 1 for any norm but NaN, an infinite one
+ * too, and where max_norm, eps and norm are all 0.
  *
  * grad      [numel] dtype, read only unless out is the same buffer
  * out       mu_clip_grads: [numel] out_dtype receiving c * g (the float32

@@ -143,7 +143,7 @@ def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float = math.inf, eps:
     """The global 2-norm of a list of float32 and bfloat16 tensors, as a float32
     scalar on the GPU (no synchronisation). scale_out receives the factor
     min(1, max_norm / (norm + eps)), which muon_step and adamw_step take as
-    grad_scale."""
+    grad_scale; without a bound (the default) 1 unless the norm is NaN."""
     return _norm(grads, None, max_norm, eps, norm_out, scale_out, workspace, stream)
 
 

@@ -187,7 +187,8 @@ __global__ __launch_bounds__(NTHR) void k_sumsq(SqArgs A) {
 __device__ __forceinline__ float norm_out(const NormOut& N, double s, bool writes) {
     const double norm = sqrt(s);
     const double r = (double)N.max_norm / (norm + (double)N.eps);
-    // 0 / 0 (both bounds 0 and no gradient) clips nothing; a NaN norm stays NaN
+    // 0 / 0 (both bounds 0 and no gradient) and inf / inf (no bound and an infinite
+    // norm) clip nothing; a NaN norm stays NaN
     const float c = isnan(norm) ? (float)norm : (r < 1.0 ? (float)r : 1.f);
     if (writes) {
         if (N.norm) *gp(N.norm) = (float)norm;

@@ -170,6 +170,24 @@ def test_zero_empty_and_not_finite():
             assert bool(o[where].isnan()) and float(o.nan_to_num(0.0).abs().max()) == 0.0   # 0 * inf, 0 * 1
 
 
+@pytest.mark.parametrize("n", [100, 8192 * 40])   # one launch, several
+def test_no_bound_keeps_the_gradients(n):
+    """max_norm = inf, grad_norm's default: the factor is 1 for any norm but NaN,
+    an infinite one too (infinity over infinity clips nothing)."""
+    import newton_schulz_orthogonalized_amd as nso
+    for bad in (0.0, 3.0, 1e30, float("inf"), -float("inf"), float("nan")):
+        g = torch.ones(n, device="cuda")
+        g[n // 2] = bad
+        keep, scale, o = g.clone(), torch.full((), -1.0, device="cuda"), torch.zeros_like(g)
+        norm = float(nso.grad_norm([g], scale_out=scale))
+        assert math.isnan(float(scale)) if math.isnan(bad) else float(scale) == 1.0, bad
+        assert math.isinf(norm) == math.isinf(bad) and math.isnan(norm) == math.isnan(bad)
+        nso.clip_grads([g], math.inf, outs=[o])
+        nso.clip_grads([g], math.inf)
+        for x in (o, g):
+            assert bool(x.isnan().all()) if math.isnan(bad) else torch.equal(x, keep), bad
+
+
 def test_same_bits_again_and_on_another_stream():
     import newton_schulz_orthogonalized_amd as nso
     g = _list([200000, 77777, 5], [BF, FP, BF], 56000)
