@@ -9,7 +9,8 @@ results allocated here come from `stream`'s share of the caching allocator, so
 that neither the work that used their memory before nor the work that gets it
 next overlaps the library's kernels; a result is recorded on the current stream
 too. The caller orders `stream` behind what made the inputs, and its own use of
-the results behind `stream`. Nothing here computes.
+the results behind `stream`. Nothing here computes. Of the results only
+embedding's carries a gradient.
 """
 
 from __future__ import annotations
@@ -18,6 +19,7 @@ import math
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib
 
@@ -180,9 +182,12 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0,
     """scale * weight[tokens] for int32 or int64 tokens of any shape. A token
     outside the table reads nothing and gives a row of NaN. Differentiable in
     weight (embedding_grad; the row padding_idx gets no gradient) unless `out`
-    is given."""
+    is given; forward mode is refused. A captured backward pass needs what torch
+    asks of any: no eager graph of the same leaf alive meanwhile."""
     if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
         raise ValueError("padding_idx must name a row of the weight")
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(weight).tangent is not None:
+        raise NotImplementedError("embedding has no forward-mode derivative")
     if torch.is_grad_enabled() and weight.requires_grad:
         if out is not None:
             raise ValueError("out takes no gradient: call under torch.no_grad()")

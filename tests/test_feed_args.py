@@ -198,6 +198,25 @@ def test_python_calls_refuse_what_the_library_cannot_take():
         nso.muon_step([x], [x], [x], lr=0.1, weight_decay=0.0, noalloc=True, grad_scale=torch.ones(()))
 
 
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_embedding_refuses_forward_mode(requires_grad):
+    """A tangent would be lost without a word: the lookup works on addresses."""
+    import torch.autograd.forward_ad as fw
+
+    import newton_schulz_orthogonalized_amd as nso
+    w, tok = torch.ones(4, 8, requires_grad=requires_grad), torch.zeros(3, dtype=torch.int64)
+    with fw.dual_level():
+        dual = fw.make_dual(w, torch.ones(4, 8))
+        with pytest.raises(NotImplementedError, match="forward"):
+            nso.embedding(tok, dual)
+        with pytest.raises(NotImplementedError, match="forward"), torch.no_grad():
+            nso.embedding(tok, dual, out=torch.zeros(3, 8))
+        with pytest.raises(ValueError, match="on a GPU"):
+            nso.embedding(tok, w)           # no tangent: refused for another reason
+    with pytest.raises(ValueError, match="on a GPU"):
+        nso.embedding(tok, w)
+
+
 def test_marshalling_refuses_bad_shapes_and_types(lib):
     """What the binding checks for itself, on CPU tensors (nothing is called)."""
     q = torch.zeros(2, 6, 4, 8)
