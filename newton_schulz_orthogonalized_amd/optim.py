@@ -65,6 +65,10 @@ class MuonAdamW(torch.optim.Optimizer):
     An AdamW parameter may have a sparse gradient over its rows (that of
     nn.Embedding(sparse=True)): its rows are summed into a dense gradient
     (api.embedding_grad) and the step is that of the dense gradient.
+
+    Gradients that are not dense and contiguous are copied for the step. The
+    copies live until their group's step has been launched; with max_grad_norm,
+    which reads all gradients before the first group, until the end of step().
     """
 
     def __init__(self, param_groups: List[Dict], *, lr: float = 0.02, weight_decay: float = 0.0,
@@ -95,8 +99,8 @@ class MuonAdamW(torch.optim.Optimizer):
         self._workspaces: Dict[tuple, torch.Tensor] = {}
         self.max_grad_norm = max_grad_norm
         self.grad_norm: Optional[torch.Tensor] = None
-        self._grads: Dict[torch.Tensor, torch.Tensor] = {}   # during a step: each parameter's dense gradient
-        self._scale: Optional[torch.Tensor] = None           # during a step: the clip factor
+        self._grads: Dict[torch.Tensor, torch.Tensor] = {}   # during a clipped step: each parameter's dense gradient
+        self._scale: Optional[torch.Tensor] = None           # during a clipped step: the clip factor
 
     # float32 state of both rules (the library reads and writes it as float32)
     _F32_STATE = ("momentum_buffer", "exp_avg", "exp_avg_sq")
@@ -130,8 +134,10 @@ class MuonAdamW(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        self._check_grads()
         try:
-            self._gather_grads()
+            if self.max_grad_norm is not None:
+                self._clip_factor()
             for g in self.param_groups:
                 if g["kind"] == "muon":
                     self._step_muon(g)
@@ -141,20 +147,30 @@ class MuonAdamW(torch.optim.Optimizer):
             self._grads, self._scale = {}, None
         return loss
 
-    def _gather_grads(self):
-        """Dense contiguous gradients of all parameters, and with max_grad_norm
-        their norm and clip factor."""
+    def _check_grads(self):
+        """Refuses gradients that the step cannot take before it changes anything."""
         for g in self.param_groups:
             for p in g["params"]:
-                if p.grad is None:
+                if p.grad is None or p.grad.layout == torch.strided:
                     continue
-                if p.grad.layout == torch.strided:
-                    self._grads[p] = p.grad if p.grad.is_contiguous() else p.grad.contiguous()
-                elif g["kind"] == "adamw" and p.grad.layout == torch.sparse_coo and p.grad.sparse_dim() == 1 and p.dim() == 2:
-                    self._grads[p] = self._dense_rows(p)
-                else:
+                if not (g["kind"] == "adamw" and p.grad.layout == torch.sparse_coo and p.grad.sparse_dim() == 1
+                        and p.dim() == 2):
                     raise ValueError("a gradient is dense, or sparse over the rows of a 2-D AdamW parameter")
-        if self.max_grad_norm is None or not self._grads:
+
+    def _dense_grad(self, p):
+        """A parameter's gradient as a dense contiguous tensor."""
+        grad = self._grads.get(p)
+        if grad is not None:
+            return grad
+        if p.grad.layout == torch.strided:
+            return p.grad if p.grad.is_contiguous() else p.grad.contiguous()
+        return api.embedding_grad(p.grad._indices()[0].contiguous(), p.grad._values().contiguous(), p.shape[0], dtype=p.dtype)
+
+    def _clip_factor(self):
+        """The norm of all gradients and the clip factor. Dense copies made for it
+        are kept until the end of the step, which reads them again."""
+        self._grads = {p: self._dense_grad(p) for g in self.param_groups for p in g["params"] if p.grad is not None}
+        if not self._grads:
             return
         grads = list(self._grads.values())
         gs, n = _lib.gradients(grads)
@@ -163,14 +179,6 @@ class MuonAdamW(torch.optim.Optimizer):
         self.grad_norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = self._ws(("norm",), _lib.mu_grad_norm_workspace_size(gs, n), dev)
         _lib.mu_grad_norm(gs, n, float(self.max_grad_norm), 1e-6, self.grad_norm, self._scale, ws)
-
-    def _dense_rows(self, p):
-        rows = p.grad._values().contiguous()
-        key = ("rows", id(p))
-        buf = self._workspaces.get(key)
-        if buf is None or buf.shape != p.shape or buf.dtype != p.dtype or buf.device != p.device:
-            buf = self._workspaces[key] = torch.empty(p.shape, dtype=p.dtype, device=p.device)
-        return api.embedding_grad(p.grad._indices()[0].contiguous(), rows, p.shape[0], out=buf)
 
     def _step_muon(self, g):
         ps, gs, ms, heads, scales = [], [], [], [], []
@@ -184,7 +192,7 @@ class MuonAdamW(torch.optim.Optimizer):
                 st["momentum_buffer"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
             w2 = p.view(p.shape[0], -1)
             ps.append(w2)
-            gs.append(self._grads[p].view(p.shape[0], -1))
+            gs.append(self._dense_grad(p).view(p.shape[0], -1))
             ms.append(st["momentum_buffer"].view(p.shape[0], -1))
             h = g["num_heads"]
             heads.append(int(h(p) if callable(h) else h))
@@ -205,13 +213,14 @@ class MuonAdamW(torch.optim.Optimizer):
         for p in g["params"]:
             if p.grad is None:
                 continue
+            grad = self._dense_grad(p)
             st = self.state[p]
             if "step" not in st:
                 st["step"] = 0
                 st["exp_avg"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
                 st["exp_avg_sq"] = torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format)
             st["step"] += 1
-            batches.setdefault(int(st["step"]), []).append((p, self._grads[p], st["exp_avg"], st["exp_avg_sq"]))
+            batches.setdefault(int(st["step"]), []).append((p, grad, st["exp_avg"], st["exp_avg_sq"]))
         b1, b2 = g["betas"]
         for t, items in batches.items():
             ts, n = _lib.tensors([x[0] for x in items], [x[1] for x in items], [x[2] for x in items],

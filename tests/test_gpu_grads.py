@@ -404,3 +404,43 @@ def test_optimizer_refuses_a_sparse_matrix_gradient():
         opt.step()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(m.parameters(), before))
+
+
+def test_optimizer_copies_of_gradients_end_with_their_group():
+    """Gradients that are not contiguous are copied for the step: without a bound
+    on the norm one group's copies at a time, and none after the step."""
+    import newton_schulz_orthogonalized_amd as nso
+    shape, groups = (1024, 2048), 4
+    copy = shape[0] * shape[1] * 4
+    ps = [torch.nn.Parameter(torch.zeros(shape, device="cuda")) for _ in range(groups)]
+    for p in ps:
+        p.grad = torch.ones(shape[::-1], device="cuda").t()
+    for clip, most in ((None, 1.5), (1.0, groups + 0.5)):
+        opt = nso.MuonAdamW([{"params": [p], "kind": "muon" if i % 2 else "adamw"} for i, p in enumerate(ps)],
+                            max_grad_norm=clip)
+        opt.step()           # states and workspaces are made
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        opt.step()
+        torch.cuda.synchronize()
+        assert torch.cuda.max_memory_allocated() - before < most * copy, clip
+        assert torch.cuda.memory_allocated() - before < copy // 2
+
+
+@pytest.mark.parametrize("clip", [None, 1.0])
+def test_optimizer_keeps_no_dense_gradient_of_a_sparse_one(clip):
+    import newton_schulz_orthogonalized_amd as nso
+    emb = torch.nn.Embedding(20000, 128, sparse=True, device="cuda")
+    table = 20000 * 128 * 4
+    opt = nso.MuonAdamW([{"params": [emb.weight], "kind": "adamw"}], max_grad_norm=clip)
+    tok = torch.arange(64, device="cuda")
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    for _ in range(2):
+        emb(tok).sum().backward()
+        opt.step()
+        opt.zero_grad(set_to_none=True)
+    torch.cuda.synchronize()
+    # the two moments, nothing else of the table's size
+    assert abs(torch.cuda.memory_allocated() - before - 2 * table) < table // 2
