@@ -469,8 +469,10 @@ int mu_version(void);
 #define MU_K_GRADNORM 11 /* global gradient norm: squares, and the final sum */
 #define MU_K_CLIP 12     /* scaled gradients */
 #define MU_K_LOOKUP 13   /* embedding lookup */
-#define MU_K_ROWGRAD 14  /* embedding gradient: token sort, row sums, joins */
-#define MU_K_QKMAX 15    /* attention max logits */
+#define MU_K_ROWGRAD 14  /* embedding gradient: token sort, row sums, joins (bytes assume that */
+                         /* all tokens are valid and name as many rows as they can) */
+#define MU_K_QKMAX 15    /* attention max logits (lengths or cu_q given, which lie on the device: */
+                         /* operations 0, bytes of all rows) */
 #define MU_K_COUNT 16
 int mu_profile_enable(int on);
 int mu_profile_read(int kernel, double* total_ms, int64_t* launches, double* flops, double* bytes);

@@ -791,8 +791,10 @@ int run_rowgrad(const mu_rowgrad* e, char* ws, hipStream_t s) {
     b.chunks = p.chunks;
     b.lanes = p.lanes;
     b.slices = p.slices;
-    const double row = (double)p.n * e->dim;
-    int rc = timed_launch(MU_K_ROWGRAD, row, row * (er + eg), s, [&] {
+    // (tokens on the device: as if all were valid and as many rows named as can be;
+    // the partial sums of runs that cross chunks are not counted)
+    const double row = (double)p.n * e->dim, named = (double)std::min(e->n_tokens, e->vocab) * e->dim;
+    int rc = timed_launch(MU_K_ROWGRAD, row, row * er + named * eg * (e->accumulate ? 2 : 1) + 8.0 * p.n, s, [&] {
         if (e->row_dtype == MU_BF16)
             return e->grad_dtype == MU_BF16 ? launch_sum<bf16, bf16>(b, s) : launch_sum<bf16, float>(b, s);
         return e->grad_dtype == MU_BF16 ? launch_sum<float, bf16>(b, s) : launch_sum<float, float>(b, s);

@@ -544,6 +544,13 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     flush();
 }
 
+// Pairs of nq queries and nk keys that count: query i sees min(nk, i + 1 + nk - nq) keys.
+double visible_pairs(double nq, double nk, bool causal) {
+    if (!causal) return nq * nk;
+    const double n = std::min(nq, nk);   // the last n queries see nk - n + 1 .. nk keys
+    return n * (nk - n) + n * (n + 1) / 2;
+}
+
 // Places of a head at most (lengths on the device may leave fewer).
 double most_places(const mu_qk_logits* a, int bm, int bn, int cost) {
     const double q = a->cu_q ? (double)(a->q_len / bm) + a->batch : (double)a->batch * ((a->q_len + bm - 1) / bm);
@@ -741,9 +748,10 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* ws, size_t ws_bytes, void* str
         const int64_t mix = a->q_stride_b | a->q_stride_s | a->q_stride_h | a->k_stride_b | a->k_stride_s | a->k_stride_h | a->dim;
         const bool direct = (mix * es) % 16 == 0 && aligned(a->q, 16) && aligned(a->k, 16) &&
                             a->k_stride_s < ((int64_t)1 << 30) / (64 * es);
-        const double nb = a->cu_q ? 1 : a->batch;
-        const double bytes = nb * a->dim * es * ((double)a->q_len * a->q_heads + (double)a->k_len * a->k_heads);
-        const double flops = 2.0 * nb * (double)a->q_len * (double)a->k_len * a->q_heads * a->dim * (a->causal ? 0.5 : 1.0);
+        // the profiler's figures (lengths on the device: operations unknown, bytes of all rows)
+        const double nb = a->cu_q ? 1 : a->batch, nq = (double)a->q_len, nk = (double)a->k_len;
+        const double bytes = nb * a->dim * es * (nq * a->q_heads + nk * a->k_heads);
+        const double flops = a->cu_q || a->q_lengths || a->k_lengths ? 0.0 : 2.0 * nb * visible_pairs(nq, nk, a->causal) * a->q_heads * a->dim;
         return run_any(Call{a, (int64_t*)ws, direct, flops, bytes, (hipStream_t)stream});
     });
 }

@@ -314,3 +314,24 @@ def test_refusals_on_the_gpu():
         nso.embedding(tok, w.half())
     torch.cuda.synchronize()
     assert bool((w == 1).all())
+
+
+def test_profiled_bytes_of_the_gradient():
+    """Many tokens on few rows: the rows are read once, the gradient's zeros and
+    its at most `vocab` sums written once each."""
+    import newton_schulz_orthogonalized_amd as nso
+    from newton_schulz_orthogonalized_amd import _lib
+    n, vocab, dim = 4000, 10, 256
+    tok = torch.from_numpy(_tokens("uniform", n, vocab, 1)).cuda()
+    rows = torch.ones(n, dim, dtype=BF, device="cuda")
+    for accumulate in (False, True):
+        out = torch.zeros(vocab, dim, device="cuda")
+        _lib.mu_profile_enable(True)
+        try:
+            nso.embedding_grad(tok, rows, vocab, out=out, accumulate=accumulate)
+            torch.cuda.synchronize()
+        finally:
+            _lib.mu_profile_enable(False)
+        p = _lib.mu_profile_read(_lib.MU_K_ROWGRAD)
+        # tokens 8 bytes, sorted words 8 written and read
+        assert p["bytes"] == n * (8 + 8 + 8) + n * dim * 2 + 2 * vocab * dim * 4 and p["launches"] == 3

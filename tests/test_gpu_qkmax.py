@@ -392,3 +392,32 @@ def test_refusals_on_the_gpu():
         nso.qk_max_logits(q.transpose(2, 3), q.transpose(2, 3))
     with pytest.raises(TypeError):
         nso.qk_max_logits(q.half(), q.half())
+
+
+def _profiled(call):
+    from newton_schulz_orthogonalized_amd import _lib
+    _lib.mu_profile_enable(True)
+    try:
+        call()
+        torch.cuda.synchronize()
+    finally:
+        _lib.mu_profile_enable(False)
+    return _lib.mu_profile_read(_lib.MU_K_QKMAX)
+
+
+def test_profiled_operations_are_those_of_visible_pairs():
+    """Dense calls report 2 dim operations a visible pair and query head; with
+    lengths on the device the pairs are unknown and none are reported."""
+    import newton_schulz_orthogonalized_amd as nso
+    for nq, nk in ((300, 300), (200, 333), (333, 200), (1, 70)):
+        q, k = _qk(3, nq, nk, 4, 2, 64, BF, 90100)
+        for causal in (True, False):
+            seen = np.ones((nq, nk)) if not causal else np.arange(nk)[None, :] <= np.arange(nq)[:, None] + nk - nq
+            p = _profiled(lambda: nso.qk_max_logits(q, k, causal=causal))
+            assert p["flops"] == 2.0 * 3 * 4 * 64 * seen.sum() and p["ms"] > 0, (nq, nk, causal)
+            assert p["bytes"] == 2.0 * 64 * 3 * (nq * 4 + nk * 2)
+    q, k = _qk(1, 500, 500, 4, 2, 64, BF, 90200)
+    cu = torch.tensor([0, 100, 500], dtype=torch.int32, device="cuda")
+    for call in (lambda: nso.qk_max_logits(q[0], k[0], cu_seqlens=cu), lambda: nso.qk_max_logits(q, k, lengths=cu[1:2])):
+        p = _profiled(call)
+        assert p["flops"] == 0.0 and p["bytes"] == 2.0 * 64 * 500 * 6
