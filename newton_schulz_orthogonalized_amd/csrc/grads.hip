@@ -67,36 +67,6 @@ struct ClipArgs {
 };
 static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments");
 
-// Vectors at element alignment: gfx950 takes global vector accesses at any
-// address, so tensors that start anywhere in an allocation need no other path.
-typedef bf16x8 bf16x8u __attribute__((aligned(2)));
-typedef f32x4 f32x4u __attribute__((aligned(4)));
-
-template <typename T>
-__device__ __forceinline__ void load8(const MU_GLOBAL T* p, float v[8]) {
-    if constexpr (sizeof(T) == 2) {
-        const bf16x8 q = *(const MU_GLOBAL bf16x8u*)p;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)q[e];
-    } else {
-        const f32x4 a = *(const MU_GLOBAL f32x4u*)p, b = *(const MU_GLOBAL f32x4u*)(p + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) { v[e] = a[e]; v[e + 4] = b[e]; }
-    }
-}
-template <typename T>
-__device__ __forceinline__ void store8(MU_GLOBAL T* p, const float v[8]) {
-    if constexpr (sizeof(T) == 2) {
-        bf16x8 q;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = (bf16)v[e];
-        *(MU_GLOBAL bf16x8u*)p = q;
-    } else {
-        *(MU_GLOBAL f32x4u*)p = f32x4{v[0], v[1], v[2], v[3]};
-        *(MU_GLOBAL f32x4u*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    }
-}
-
 __device__ __forceinline__ double block_sum(double v, double* red) {
     v = wave_sum(v);
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -112,6 +82,9 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
 // and non-temporal (Llama-1B-shaped set, 2.68 GB of bfloat16: 529 us with loads
 // as they come, 440 with all of a chunk's first, 393 non-temporal (NT), 6.8 TB/s;
 // one run of chunks for each XCD 414-418, 2048 workgroups 432).
+// (Vectors at element alignment here and below: gfx950 takes global vector
+// accesses at any address, so tensors that start anywhere in an allocation need
+// no other path.)
 template <bool NT, typename T>
 __device__ __forceinline__ double sumsq_chunk(const void* base, int64_t i0, int64_t n, int tid) {
     const MU_GLOBAL T* p = (const MU_GLOBAL T*)base + i0;
@@ -289,6 +262,7 @@ __global__ __launch_bounds__(NTHR) void k_clip(ClipArgs A) {
 // and 14.2 us, of 32 11.8 and 14.3, of 64 26.2 and 14.3; clipping of 12 chunks
 // 12.9 and 15.8, of 16 17.3 and 15.7, of 32 32.1 and 15.8.
 constexpr int FEW_NORM = 32, FEW_CLIP = 12, FEW_THR = 4 * NTHR;
+static_assert(FEW_NORM <= CLIP_SEGS && FEW_CLIP <= CLIP_SEGS, "one launch takes the segments of so few chunks");
 template <bool CLIP>
 __global__ __launch_bounds__(FEW_THR) void k_few(ClipArgs A) {
     __shared__ double red[FEW_THR / 64];
@@ -354,23 +328,21 @@ int check_list(const mu_grad* gs, int32_t n, bool with_out, const float* norm_ou
 
 int64_t chunks_of(int64_t numel) { return (numel + GRAD_CHUNK - 1) / GRAD_CHUNK; }
 
-// Launches of at most `segs` tensors and 2^31 - 1 chunks each: fn(first list
-// entry's index in `order`, count, chunks).
+// The list's tensors that hold elements, in launches of at most `segs` of them
+// and 2^30 chunks in all (a tensor of 2^42 elements has 2^29).
 struct Batch {
     std::vector<int> items;
     int64_t chunks = 0;
 };
-int batches(const mu_grad* gs, int32_t n, int segs, std::vector<Batch>& out) {
+void batches(const mu_grad* gs, int32_t n, int segs, std::vector<Batch>& out) {
     out.clear();
     for (int i = 0; i < n; ++i) {
         if (gs[i].numel == 0) continue;
         const int64_t c = chunks_of(gs[i].numel);
-        if (c > 0x3fffffff) return fail(MU_ERR_INVALID_ARG, "gradient %d is too large for one launch", i);
-        if (out.empty() || (int)out.back().items.size() == segs || out.back().chunks + c > 0x3fffffff) out.emplace_back();
+        if (out.empty() || (int)out.back().items.size() == segs || out.back().chunks + c > (1 << 30)) out.emplace_back();
         out.back().items.push_back(i);
         out.back().chunks += c;
     }
-    return MU_OK;
 }
 
 // Workgroups of a launch over so many chunks: a multiple of 8, so that every XCD has some.
@@ -390,8 +362,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
     if (!clip && !norm_out && !scale_out) return fail(MU_ERR_INVALID_ARG, "norm_out and scale_out are both null");
     if (!aligned(norm_out, 4) || !aligned(scale_out, 4)) return fail(MU_ERR_LAYOUT, "misaligned norm_out or scale_out");
     std::vector<Batch> bs;
-    rc = batches(gs, n, SQ_SEGS, bs);
-    if (rc) return rc;
+    batches(gs, n, SQ_SEGS, bs);
     const size_t np = partials_of(bs), need = align_up(np * sizeof(double));
     if (np) {
         if (!ws) return fail(MU_ERR_WORKSPACE, "workspace is null (need %zu bytes)", need);
@@ -411,7 +382,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
         a.chunks = (int)c;
         return bytes;
     };
-    if (bs.size() == 1 && bs[0].chunks <= (clip ? FEW_CLIP : FEW_NORM) && bs[0].items.size() <= (size_t)CLIP_SEGS) {
+    if (bs.size() == 1 && bs[0].chunks <= (clip ? FEW_CLIP : FEW_NORM)) {
         ClipArgs a;
         const double bytes = clip_args(bs[0], a);
         a.no = NormOut{nullptr, 0, max_norm, eps, norm_out, scale_out};
@@ -456,8 +427,7 @@ int norm_and_clip(const mu_grad* gs, int32_t n, float max_norm, float eps, float
             return hipGetLastError();
         }, "gradient norm sum launch");
     }
-    rc = batches(gs, n, CLIP_SEGS, bs);
-    if (rc) return rc;
+    batches(gs, n, CLIP_SEGS, bs);
     for (auto& b : bs) {
         ClipArgs a;
         const double bytes = clip_args(b, a);
@@ -483,8 +453,7 @@ int mu_grad_norm_workspace_size(const mu_grad* gs, int32_t n, size_t* bytes) {
         int rc = check_list(gs, n, false, nullptr, nullptr);
         if (rc) return rc;
         std::vector<Batch> bs;
-        rc = batches(gs, n, SQ_SEGS, bs);
-        if (rc) return rc;
+        batches(gs, n, SQ_SEGS, bs);
         *bytes = align_up(partials_of(bs) * sizeof(double));
         return MU_OK;
     });

@@ -227,8 +227,8 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     constexpr int GR = NC % 16 == 0 ? 16 : NC % 8 == 0 ? 8 : NC % 4 == 0 ? 4 : 2;
     constexpr int SH = GR == 16 ? 0 : GR == 8 ? 1 : GR == 4 ? 2 : 3;
     constexpr int SLOTS = BN * NC;                     // chunks of a tile
-    constexpr int NL = (SLOTS / 64 + 3) / 4;           // direct loads of a wave and tile
-    static_assert(SLOTS % 64 == 0, "whole loads");
+    constexpr int NL = SLOTS / 256;                    // direct loads of a wave and tile
+    static_assert(SLOTS % 256 == 0, "the same number of whole loads for each wave");
     constexpr int TB = BN * ROWB, NB = BN / 32;
     constexpr int PD = NK <= 8 ? NK : NK % 8 == 0 ? 8 : 6;
     static_assert(NK % PD == 0, "a column block is whole rounds of the operand ring");
@@ -253,7 +253,7 @@ __global__ __launch_bounds__(NTHR, WPE) void k_qkmax(QkMaxArgs A) {
     int lrow[NL], lchk[NL], lpos[NL];
 #pragma unroll
     for (int j = 0; j < NL; ++j) {
-        lpos[j] = SLOTS % 256 == 0 ? wave + 4 * j : uni(min(wave + 4 * j, SLOTS / 64 - 1));   // a last odd load is done twice
+        lpos[j] = wave + 4 * j;
         const int q = lpos[j] * 64 + lane;
         lrow[j] = q / NC;
         lchk[j] = (q % NC) ^ ((lrow[j] >> SH) & (GR - 1));
