@@ -335,3 +335,31 @@ def test_profiled_bytes_of_the_gradient():
         p = _lib.mu_profile_read(_lib.MU_K_ROWGRAD)
         # tokens 8 bytes, sorted words 8 written and read
         assert p["bytes"] == n * (8 + 8 + 8) + n * dim * 2 + 2 * vocab * dim * 4 and p["launches"] == 3
+
+
+@pytest.mark.parametrize("grad_t,accumulate", [(FP, False), (FP, True), (BF, False)])
+@pytest.mark.parametrize("n,vocab,dim", [(12289, 3, 24), (70000, 9, 16), (100003, 5000, 3), (131073, 4, 2), (262144, 300, 600),
+                                         (524289, 40000, 3), (65536, 7, 1030), (2200001, 70, 1)])
+def test_every_token_of_long_batches_counts(n, vocab, dim, grad_t, accumulate):
+    """Small positive integers, whose float32 sums are exact in any order (all
+    below 2^24), so one row left out, counted twice or put elsewhere shows: runs
+    over thousands of chunks and of chunks longer than 16, joined by quarters."""
+    import newton_schulz_orthogonalized_amd as nso
+    print(f"[rowgrad] exact {n} {vocab} {dim} {grad_t} {accumulate}", flush=True)
+    rows = (np.arange(n)[:, None] * (np.arange(dim)[None, :] + 3) % 5 + 1).astype(np.float32)
+    assert 5 * n + 9 < 2 ** 24
+    r = torch.from_numpy(rows).to(BF).cuda()
+    for kind in ("one", "skewed", "sorted", "outside"):
+        tok = _tokens(kind, n, vocab, n + 1)
+        t = torch.from_numpy(tok).cuda()
+        base = np.zeros((vocab, dim))
+        out = torch.full((vocab, dim), float("nan"), dtype=grad_t, device="cuda")
+        if accumulate:
+            base = (np.arange(vocab * dim).reshape(vocab, dim) % 9).astype(np.float64)
+            out.copy_(torch.from_numpy(base))
+        nso.embedding_grad(t, r, vocab, out=out, accumulate=accumulate)
+        torch.cuda.synchronize()
+        ok = (tok >= 0) & (tok < vocab)
+        want = base + np.stack([np.bincount(tok[ok], weights=rows[ok, c], minlength=vocab) for c in range(dim)], 1)
+        got = to_np(out)
+        assert np.array_equal(got, O.bf16_round(want) if grad_t == BF else want), kind
