@@ -444,3 +444,51 @@ def test_optimizer_keeps_no_dense_gradient_of_a_sparse_one(clip):
     torch.cuda.synchronize()
     # the two moments, nothing else of the table's size
     assert abs(torch.cuda.memory_allocated() - before - 2 * table) < table // 2
+
+
+@pytest.mark.parametrize("dtype,precision", [(FP, "f32"), (BF, "bf16")])
+def test_replayed_steps_follow_the_factor(dtype, precision):
+    """One list of buffers, whose calls replay a graph from the second one on:
+    factors that change in place, a factor at another address, none, and back,
+    each step bit for bit the plain step of gradients times that power of two."""
+    import newton_schulz_orthogonalized_amd as nso
+    from newton_schulz_orthogonalized_amd import _lib
+    shapes = [(96, 160), (160, 96), (33, 77), (256, 256)]
+    mk = lambda seed, std, t: [as_dtype(host_normal(s, seed + i, std), t).cuda() for i, s in enumerate(shapes)]  # noqa: E731
+    w, g, m = mk(65000, 0.02, dtype), mk(65100, 1e-3, dtype), mk(65200, 1e-3, FP)
+    w2, g2, m2 = ([x.clone() for x in t] for t in (w, g, m))
+    ws = _lib.workspace(nso.muon_workspace_bytes(w, g, m, precision=precision), "cuda")
+    a, b = torch.zeros((), device="cuda"), torch.zeros(1, device="cuda")
+    kw = dict(lr=0.02, weight_decay=0.01, precision=precision)
+    for step, (t, c) in enumerate([(a, 0.5), (a, 0.5), (a, 0.25), (a, 1.0), (b, 0.125), (b, 0.5), (None, 1.0), (a, 0.25),
+                                   (None, 1.0), (b, 2.0), (a, 0.5)]):
+        if t is not None:
+            a.fill_(-1.0), b.fill_(-1.0)     # what the step must not read
+            t.fill_(c)
+        for x, y in zip(g, g2):
+            y.copy_(x * c)
+        nso.muon_step(w, g, m, grad_scale=t, workspace=ws, **kw)
+        nso.muon_step(w2, g2, m2, **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(w + m, w2 + m2)), (step, c)
+
+
+def test_thousands_of_tensors():
+    """Lists of dozens of launches of both kernels, of large and small tensors;
+    the sums in float64 and the one product and rounding exactly."""
+    import newton_schulz_orthogonalized_amd as nso
+    sizes = [1 + (i * 7919) % 997 if i % 50 else 30000 + i for i in range(5000)]
+    flat = (((torch.arange(sum(sizes), device="cuda") * 7919) % 2003 - 1001).float() / 4096)
+    g = list(flat.split(sizes))
+    for i in range(0, 5000, 3):
+        g[i] = g[i].to(BF)
+    want = math.sqrt(sum(float(x.double().square().sum()) for x in g))
+    assert abs(float(nso.grad_norm(g)) - want) <= want * ULP * 1.001
+    outs = [torch.zeros(x.numel(), dtype=(FP, BF)[i % 2], device="cuda") for i, x in enumerate(g)]
+    scale = torch.zeros((), device="cuda")
+    norm = nso.clip_grads(g, 3.0, outs=outs, scale_out=scale)
+    torch.cuda.synchronize()
+    assert abs(float(norm) - want) <= want * ULP * 1.001
+    assert abs(float(scale) - 3.0 / (want + 1e-6)) <= 3.0 / want * ULP * 1.001
+    for i, (x, o) in enumerate(zip(g, outs)):
+        assert torch.equal(o, (x.float() * scale).to(o.dtype)), i
