@@ -421,3 +421,34 @@ def test_profiled_operations_are_those_of_visible_pairs():
     for call in (lambda: nso.qk_max_logits(q[0], k[0], cu_seqlens=cu), lambda: nso.qk_max_logits(q, k, lengths=cu[1:2])):
         p = _profiled(call)
         assert p["flops"] == 0.0 and p["bytes"] == 2.0 * 64 * 500 * 6
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("d", [16, 32, 40, 64, 80, 96, 128, 160, 192, 256])
+def test_long_runs_of_every_width(d, dtype):
+    """So many tiles for each workgroup that every slot of the ring is filled
+    again and read: against float64 products (on the GPU, a head at a time), and
+    single large logits, each at its own key and column, nothing else in sight."""
+    import newton_schulz_orthogonalized_amd as nso
+    print(f"[qkmax] long runs {dtype} {d}", flush=True)
+    n, hq, hk = 2050, 8, 2
+    q, k = _qk(1, n, n, hq, hk, d, dtype, 90300 + d)
+    for causal in (True, False):
+        got = nso.qk_max_logits(q, k, causal=causal)
+        torch.cuda.synchronize()
+        for h in range(hq):
+            a, b = q[0, :, h].double(), k[0, :, h * hk // hq].double().t().contiguous()
+            s, mag = (a @ b).abs(), a.abs() @ b.abs()
+            if causal:
+                s, mag = s.tril(), mag.tril()
+            off = abs(float(got[h]) - float(s.max()) * d ** -0.5)
+            assert off <= (d + 2) * 2.0 ** -23 * float(mag.max()) * d ** -0.5, (causal, h)
+    q.zero_(), k.zero_()
+    for step in range(24):
+        j, h = 85 * step + step % 31, step % hq          # keys all along, at every place of a tile
+        i, c = min(n - 1, j + (step * 37) % 500), (step * 29) % d
+        q[0, i, h, c], k[0, j, h * hk // hq, c] = -3.0, 5.0
+        for causal in (True, False):
+            got = nso.qk_max_logits(q, k, causal=causal, scale=1.0).tolist()
+            assert got == [15.0 if x == h else 0.0 for x in range(hq)], (causal, i, j, c)
+        q[0, i, h, c], k[0, j, h * hk // hq, c] = 0.0, 0.0
