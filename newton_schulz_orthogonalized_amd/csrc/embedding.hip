@@ -75,14 +75,21 @@ __device__ __forceinline__ void store8(MU_GLOBAL T* p, int cnt, const float v[8]
 // ---------------------------------------------------------------------------
 // Lookup. A group of `lanes` lanes copies one 16-byte piece a lane of TOK rows,
 // all loads before the first store. Bound by memory: the rows read once and the
-// output written (16384 rows of 8 KB: 39.5 us, 33.2 us with non-temporal stores,
-// 191 MB at 5.7 TB/s; 8 rows a group 42.7, non-temporal loads 43.2).
+// output written (16384 rows of 8 KB: 33 us, 191 MB at 5.7 TB/s; 8 rows a group, or
+// loads that go past the caches, took 3 to 4 us more).
 //
-// Outputs of 128 MB (half the last-level cache) and more are written past the
-// caches: alone 43 and 40 us at 128 MB, 196 and 157 at 512, with a norm that reads
-// them next 110 and 113, 446 and 437. Smaller ones gain nothing alone (64 MB 21.1
-// and 20.9) and the norm finds them in the caches (48 and 54).
+// Outputs of PAST_CACHES (half the last-level cache) and more are written past the
+// caches: from there on what reads them next gains too, or loses little. Past them
+// and not, in us, alone / with a norm / an elementwise product / a matrix product
+// that reads them next (rows of 8 KB, a batch and an output of 3 GB in turn, as a
+// training loop comes back to an output only after a whole step): 64 MB 21 and 24 /
+// 38 and 39 / 48 and 45 / 87 and 85; 96 MB 30 and 33 / 52 and 53 / 67 and 65 / 118
+// and 115; 128 MB 39 and 42 / 65 and 65 / 87 and 87 / 149 and 145; 160 MB 48 and 51 /
+// 79 and 81 / 107 and 107 / 200 and 195; 192 MB 57 and 60 / 92 and 93 / 126 and 128 /
+// 230 and 226; 256 MB 75 and 78 / 120 and 136 / 164 and 171 / 291 and 289; 512 MB 146
+// and 149 / 228 and 229 / 317 and 328 / 573 and 574.
 // ---------------------------------------------------------------------------
+constexpr double PAST_CACHES = 128 << 20;
 constexpr int TOK = 4;
 struct LookupArgs {
     mu_lookup e;
@@ -828,7 +835,7 @@ int mu_embedding(const mu_lookup* e, void* stream) {
         if (ranges_overlap(in) || ranges_overlap(tk)) return fail(MU_ERR_LAYOUT, "out overlaps an input");
         hipStream_t s = (hipStream_t)stream;
         const double bytes = (double)e->n_tokens * (2.0 * (double)e->dim * es + e->token_bits / 8);
-        LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es >= (double)(128 << 20)};
+        LookupArgs a{*e, 64, 0, (double)e->n_tokens * e->dim * es >= PAST_CACHES};
         const int epv = (int)(16 / es);
         while (a.lanes > 1 && (int64_t)a.lanes / 2 * epv >= e->dim) a.lanes /= 2;
         a.slices = (int)((e->dim + (int64_t)a.lanes * epv - 1) / (a.lanes * epv));

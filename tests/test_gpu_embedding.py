@@ -97,6 +97,29 @@ def test_lookup(n, vocab, dim, dtype, bits):
         assert np.isnan(got[~ok]).all()
 
 
+@pytest.mark.parametrize("dtype,dim", [(BF, 4096), (BF, 4101), (FP, 2048), (FP, 2051)])
+def test_lookups_beyond_the_caches(dtype, dim):
+    """Outputs just below and above the size from which they are written past
+    the caches (128 MB), guarded at both ends; the rows bit for bit, or one
+    float32 product and rounding; a token outside the table is a row of NaN."""
+    import newton_schulz_orthogonalized_amd as nso
+    w = as_dtype(host_normal((37, dim), 70500), dtype).cuda()
+    size = dim * w.element_size()
+    for n in ((128 << 20) // size - 1, (128 << 20) // size + 1, (300 << 20) // size):
+        print(f"[lookup] {n} x {dim} {dtype}", flush=True)
+        tok = (torch.arange(n, device="cuda") * 7919) % 37
+        buf = torch.full((n * dim + 16,), 7.0, dtype=dtype, device="cuda")
+        out = buf[8:-8].view(n, dim)
+        for scale in (1.0, -0.3):
+            nso.embedding(tok, w, scale=scale, out=out)
+            assert torch.equal(out, (w if scale == 1.0 else (w.float() * scale).to(dtype))[tok])
+        tok[n // 2], tok[n - 1] = 37, -1
+        nso.embedding(tok, w, out=out)
+        bad = out.isnan().any(1)
+        assert int(bad.sum()) == 2 and bool(out[n // 2].isnan().all()) and bool(out[n - 1].isnan().all())
+        assert bool((buf[:8] == 7).all()) and bool((buf[-8:] == 7).all())
+
+
 def test_lookup_copies_every_bit_and_takes_any_alignment():
     """Scale 1 copies infinities, NaN payloads and negative zeros; views that
     start at odd elements; tokens of any shape; an output buffer of one's own."""
