@@ -41,7 +41,13 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // three times as long: 6 and 2, the best of 1, 2, 3, 6 and 12 (8192 tokens,
 // 16 heads of 64: 66, 62, 62, 59, 61 us; 4 x 1024 tokens, 12 heads of 64 in
 // float32: 37.4, 37.2, 38.4, 42.4, 51.4 us) and of 4, 6, 8, 10 and 14 (23 packed
-// sequences: 68.8, 65.9, 69.1, 70.0, 75.7 us).
+// sequences: 68.8, 65.9, 69.1, 70.0, 75.7 us). The bfloat16 instances with tiles of
+// 32 keys have the same 6, which is within 5 % of the best of 2, 3, 4, 6, 12 and 20
+// (16 heads; one sequence of 8192 tokens: dim 100 290, 288, 289, 295, 308, 316 us,
+// dim 192 173, 166, 163, 160, 159, 164, dim 256 243, 241, 237, 231, 223, 227; the 23
+// packed sequences: 174, 168, 166, 168, 178, 205, then 91, 88, 85, 84, 85, 92 and
+// 130, 126, 122, 120, 120, 128; 4 x 1024 tokens: 41, 41, 41, 43, 48, 53, then 25, 24,
+// 22, 24, 24, 26 and 32, 31, 31, 31, 32, 33).
 template <typename T> constexpr int COST_OF = sizeof(T) == 2 ? 6 : 2;
 // How a workgroup finds its run: it takes all of a head; by arithmetic, as
 // sequences are of one length; from up to 64 sequences, one a lane; from the
@@ -632,10 +638,14 @@ int run_direct(const Call& c) {
 // them leave two workgroups a compute unit. float32 matrix instructions are so
 // long that one operand read for each suffices: 32 rows a wave and 32 keys, whose
 // finer tiles follow the causal border closer (12 heads of 64, 1024 tokens 18.6
-// against 22.5 us). RAGGED rows pass through registers, so 32 keys a tile: dim
-// 100, 4 x 2048 tokens, 16 heads 104 us, 136 with 32 rows a wave, 463 (spilled)
-// with 64 rows and 64 keys; their whole chunks are loaded as vectors at any
-// address (dim 100, 2 x 1024 tokens, 32 rows a wave 27 us, 56 by elements).
+// against 22.5 us). RAGGED rows pass through registers, so 32 keys a tile; 64
+// rows a wave, as each piece that is loaded and stored then feeds two matrix
+// instructions: dim 100, 16 heads, against 32 rows a wave, 4 x 2048 tokens 105 and
+// 156 us, 8192 tokens 296 and 501, 1024 tokens 22.4 and 24.2, but 2 x 1024 tokens 31.6
+// and 29.4. What bounds them: a tile's loads are stored to LDS at once, so every tile
+// waits for memory, where direct loads stay in flight over two tiles. Their whole
+// chunks are loaded as vectors at any address (dim 100, 2 x 1024 tokens, 32 rows a
+// wave 27 us, 56 by elements).
 int run_any(const Call& c) {
     const int d = c.p->dim;
     if (c.p->dtype == MU_BF16) {
