@@ -44,7 +44,7 @@
  *
  * Layout rules common to every entry point:
  *   - every tensor is dense, row-major, with no padding between rows (q and k
- *     of mu_qk_max_logits have strides);
+ *     of mu_qk_max_logits and the tensors of mu_rotary have strides);
  *   - parameter, gradient and state buffers of one entry must not overlap each
  *     other or any other entry's buffers;
  *   - bfloat16 buffers are 2-byte aligned, float32 buffers 4-byte aligned (16-
@@ -60,8 +60,9 @@
  * without enqueuing anything (each call stages its descriptor table through
  * pinned host memory that later calls reuse, so a replayed capture would read
  * another call's table). mu_grad_norm, mu_clip_grads, mu_embedding,
- * mu_embedding_grad and mu_qk_max_logits carry their lists in the kernels'
- * arguments and can be captured; a replay works on the buffers of the captured
+ * mu_embedding_grad, mu_qk_max_logits, mu_rotary, mu_residual_norm(_grad) and
+ * mu_gated_mlp(_grad) carry their lists in the kernels' arguments and can be
+ * captured; a replay works on the buffers of the captured
  * call, the workspace among them, which must live as long as the graph.
  */
 #ifndef MUON_MI355X_H
@@ -398,6 +399,186 @@ typedef struct mu_qk_logits {
 int mu_qk_max_logits_workspace_size(const mu_qk_logits* a, size_t* bytes);
 int mu_qk_max_logits(const mu_qk_logits* a, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Rotary positions of up to two tensors (queries and keys) in one launch. The
+ * first `part` elements of every head turn by their row's position p:
+ *   (a, b) -> scale * (a cos(p f_i) - b sin(p f_i), b cos(p f_i) + a sin(p f_i))
+ * for the pairs (i, i + part / 2), or (2 i, 2 i + 1) where interleaved = 1;
+ * elements behind them are copied. inverse = 1 turns by -p f_i: with the same
+ * scale that is also the gradient of the call. Angles are reduced in float64,
+ * sines and products are float32, rounded once to dtype.
+ *
+ * freqs      device float64 [part / 2]: f_i in radians a position
+ * positions  device int32 or int64 (position_bits 32 | 64), [batch, len], or
+ *            [len] where shared_positions = 1; NULL: 0 .. len - 1. `offset` is
+ *            added to each (|offset| <= 2^52)
+ * x, out     element (b, s, h, d) at b * stride_b + s * stride_s + h * stride_h
+ *            + d (strides in elements, >= 0), of dtype; out is x itself (the
+ *            same strides: in place, elements from `part` on are not touched)
+ *            or shares no element with an input, nor with another output
+ * part is even, 2 <= part <= dim <= MU_ROTARY_MAX_DIM. No workspace.
+ */
+#define MU_ROTARY_MAX_DIM 1024
+typedef struct mu_rotary_tensor {
+    const void* x;
+    void* out;
+    int64_t x_stride_b, x_stride_s, x_stride_h;
+    int64_t out_stride_b, out_stride_s, out_stride_h;
+    int32_t heads;
+    int32_t pad0;
+} mu_rotary_tensor;
+typedef struct mu_rotary_args {
+    mu_rotary_tensor x[2];
+    const double* freqs;
+    const void* positions;
+    int64_t offset;
+    int64_t batch;
+    int64_t len;
+    int32_t n;
+    int32_t dim;
+    int32_t part;
+    int32_t position_bits;
+    int32_t shared_positions;
+    int32_t interleaved;
+    int32_t inverse;
+    int32_t dtype;
+    float scale;
+    int32_t pad0;
+} mu_rotary_args;
+int mu_rotary(const mu_rotary_args* a, void* stream);
+
+/*
+ * The norms around a block, its gate and the residual sum:
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) * w
+ *   r' = residual_scale * r + gate * N(y; post)        (new_residual)
+ *   n  = N(r'; pre)                                    (normed)
+ * over rows of dim elements, in float32, each result rounded once (n is that of
+ * the unrounded r'). The squares are float32 sums: elements below 1e18.
+ *
+ * residual, new_residual [rows, dim] residual_dtype; update (y) and normed
+ *            [rows, dim] dtype: one type, or a float32 residual with bfloat16
+ * post_norm  1: y passes through N with post_weight (NULL: weights of 1); 0: as
+ *            it is, and post_weight is NULL
+ * pre_weight NULL: weights of 1
+ * gate       [groups, dim], row i taking gate row i / (rows / groups) (groups
+ *            divides rows: 1 for all rows, the batch's sequences, or every row);
+ *            NULL: no gate (groups 1)
+ * update     NULL: n = N(residual_scale * r; pre) alone; then new_residual,
+ *            gate and post_weight are NULL
+ * weight_dtype is that of the weights and the gate. new_residual may be the
+ * residual itself and normed the update itself (in place); outputs overlap
+ * nothing else. dim <= MU_RESNORM_MAX_DIM. No workspace.
+ */
+#define MU_RESNORM_MAX_DIM 16384
+typedef struct mu_resnorm {
+    const void* residual;
+    const void* update;
+    const void* gate;
+    const void* post_weight;
+    const void* pre_weight;
+    void* new_residual;
+    void* normed;
+    int64_t rows;
+    int64_t dim;
+    int64_t groups;
+    int32_t residual_dtype;
+    int32_t dtype;
+    int32_t weight_dtype;
+    int32_t post_norm;
+    float residual_scale;
+    float eps;
+} mu_resnorm;
+int mu_residual_norm(const mu_resnorm* a, void* stream);
+
+/*
+ * The gradients of mu_residual_norm. Of `fwd` it reads new_residual, update
+ * and the weights and gate, and the options (update NULL: residual in the place
+ * of new_residual); residual and normed are not used.
+ *
+ * grad_residual [rows, dim] residual_dtype: that of new_residual, NULL: zero
+ * grad_normed   [rows, dim] dtype: that of normed, NULL: zero
+ * d_residual, d_update        of their inputs' shapes and types
+ * d_gate [groups, dim], d_post, d_pre [dim], of weight_dtype: float32 sums over
+ *            the rows in a fixed order (the same call gives the same bits)
+ * Any result may be NULL. Results overlap neither each other nor an input.
+ */
+typedef struct mu_resnorm_grad {
+    mu_resnorm fwd;
+    const void* grad_residual;
+    const void* grad_normed;
+    void* d_residual;
+    void* d_update;
+    void* d_gate;
+    void* d_post;
+    void* d_pre;
+} mu_resnorm_grad;
+int mu_residual_norm_grad_workspace_size(const mu_resnorm_grad* a, size_t* bytes);
+int mu_residual_norm_grad(const mu_resnorm_grad* a, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The projections, activation and product of a gated feed-forward block:
+ *   g = x w_gate^T,  u = x w_up^T,  h = act(g) * u
+ * x [tokens, dim], w_gate and w_up [hidden, dim], h [tokens, hidden], all of
+ * dtype; products accumulate in float32 and h is rounded once from unrounded g
+ * and u. gate_out and up_out (both or neither) receive g and u, rounded, for
+ * the gradient. activation: MU_ACT_SILU g / (1 + e^-g), MU_ACT_GELU (the normal
+ * distribution's), MU_ACT_GELU_TANH (its tanh form), MU_ACT_RELU.
+ * Outputs overlap neither each other nor an input. dim and hidden up to
+ * MU_GATED_MAX_DIM.
+ */
+#define MU_ACT_SILU 0
+#define MU_ACT_GELU 1
+#define MU_ACT_GELU_TANH 2
+#define MU_ACT_RELU 3
+#define MU_GATED_MAX_DIM (1 << 20)
+typedef struct mu_gated {
+    const void* x;
+    const void* w_gate;
+    const void* w_up;
+    void* h;
+    void* gate_out;
+    void* up_out;
+    int64_t tokens;
+    int64_t dim;
+    int64_t hidden;
+    int32_t dtype;
+    int32_t activation;
+} mu_gated;
+int mu_gated_mlp_workspace_size(const mu_gated* a, size_t* bytes);
+int mu_gated_mlp(const mu_gated* a, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients from grad_h [tokens, hidden]:
+ *   dg = grad_h * u * act'(g),  du = grad_h * act(g)     (rounded to dtype)
+ *   dx = dg w_gate + du w_up,  d_gate = dg^T x,  d_up = du^T x
+ * gate and up are the forward call's gate_out and up_out; both NULL: they are
+ * computed again (unrounded) from x and the weights. dx [tokens, dim] of dtype;
+ * d_gate and d_up [hidden, dim] of grad_dtype (dtype or float32; both or
+ * neither), accumulate = 1: added to what they hold, in float32, rounded once.
+ * dx, or d_gate and d_up, may be NULL. Results overlap neither each other nor an
+ * input; the same call gives the same bits.
+ */
+typedef struct mu_gated_grad {
+    const void* grad_h;
+    const void* x;
+    const void* w_gate;
+    const void* w_up;
+    const void* gate;
+    const void* up;
+    void* dx;
+    void* d_gate;
+    void* d_up;
+    int64_t tokens;
+    int64_t dim;
+    int64_t hidden;
+    int32_t dtype;
+    int32_t grad_dtype;
+    int32_t accumulate;
+    int32_t activation;
+} mu_gated_grad;
+int mu_gated_mlp_grad_workspace_size(const mu_gated_grad* a, size_t* bytes);
+int mu_gated_mlp_grad(const mu_gated_grad* a, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace bytes mu_muon_step needs for this list (n == 0 gives 0). */
 int mu_muon_workspace_size(const mu_matrix* mats, int32_t n, const mu_muon_hparams* hp, size_t* bytes);
 
@@ -473,7 +654,12 @@ int mu_version(void);
                          /* all tokens are valid and name as many rows as they can) */
 #define MU_K_QKMAX 15    /* attention max logits (lengths or cu_q given, which lie on the device: */
                          /* operations 0, bytes of all rows) */
-#define MU_K_COUNT 16
+#define MU_K_ROTARY 16   /* rotary positions */
+#define MU_K_RESNORM 17  /* norms around a block, gate and residual sum */
+#define MU_K_RESNORM_GRAD 18   /* their gradients */
+#define MU_K_GATED 19    /* gated feed-forward: both projections, activation and product */
+#define MU_K_GATED_GRAD 20     /* its gradients */
+#define MU_K_COUNT 21
 int mu_profile_enable(int on);
 int mu_profile_read(int kernel, double* total_ms, int64_t* launches, double* flops, double* bytes);
 const char* mu_kernel_name(int kernel);

@@ -33,8 +33,9 @@ MU_ERR_WORKSPACE = 4
 MU_ERR_HIP = 5
 
 (MU_K_PREP, MU_K_NORM, MU_K_GRAM, MU_K_GRAM2, MU_K_APPLY, MU_K_FINISH, MU_K_ADAMW, MU_K_QKCLIP, MU_K_FUSED,
- MU_K_RESCALE, MU_K_TILEMAP, MU_K_GRADNORM, MU_K_CLIP, MU_K_LOOKUP, MU_K_ROWGRAD, MU_K_QKMAX) = range(16)
-MU_K_COUNT = 16
+ MU_K_RESCALE, MU_K_TILEMAP, MU_K_GRADNORM, MU_K_CLIP, MU_K_LOOKUP, MU_K_ROWGRAD, MU_K_QKMAX, MU_K_ROTARY,
+ MU_K_RESNORM, MU_K_RESNORM_GRAD, MU_K_GATED, MU_K_GATED_GRAD) = range(21)
+MU_K_COUNT = 21
 
 EXPORTED = (
     "mu_muon_workspace_size", "mu_muon_step", "mu_muon_step_noalloc", "mu_ortho_workspace_size",
@@ -42,7 +43,8 @@ EXPORTED = (
     "mu_adamw_workspace_size", "mu_adamw_step", "mu_qk_clip_workspace_size", "mu_qk_clip",
     "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm", "mu_clip_grads",
     "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad", "mu_qk_max_logits_workspace_size",
-    "mu_qk_max_logits",
+    "mu_qk_max_logits", "mu_rotary", "mu_residual_norm", "mu_residual_norm_grad_workspace_size", "mu_residual_norm_grad",
+    "mu_gated_mlp_workspace_size", "mu_gated_mlp", "mu_gated_mlp_grad_workspace_size", "mu_gated_mlp_grad",
     "mu_status_string", "mu_last_error", "mu_version", "mu_profile_enable", "mu_profile_read", "mu_kernel_name",
 )
 
@@ -126,6 +128,50 @@ class MuQkLogits(ctypes.Structure):
                 ("accumulate", ctypes.c_int32), ("scale", ctypes.c_float), ("max_logit", ctypes.c_void_p)]
 
 
+class MuRotaryTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("x_stride_b", ctypes.c_int64), ("x_stride_s", ctypes.c_int64), ("x_stride_h", ctypes.c_int64),
+                ("out_stride_b", ctypes.c_int64), ("out_stride_s", ctypes.c_int64), ("out_stride_h", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("pad0", ctypes.c_int32)]
+
+
+class MuRotaryArgs(ctypes.Structure):
+    _fields_ = [("x", MuRotaryTensor * 2), ("freqs", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("offset", ctypes.c_int64), ("batch", ctypes.c_int64), ("len", ctypes.c_int64), ("n", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("part", ctypes.c_int32), ("position_bits", ctypes.c_int32),
+                ("shared_positions", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float), ("pad0", ctypes.c_int32)]
+
+
+class MuResnorm(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("update", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p), ("new_residual", ctypes.c_void_p),
+                ("normed", ctypes.c_void_p), ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("groups", ctypes.c_int64),
+                ("residual_dtype", ctypes.c_int32), ("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class MuResnormGrad(ctypes.Structure):
+    _fields_ = [("fwd", MuResnorm), ("grad_residual", ctypes.c_void_p), ("grad_normed", ctypes.c_void_p),
+                ("d_residual", ctypes.c_void_p), ("d_update", ctypes.c_void_p), ("d_gate", ctypes.c_void_p),
+                ("d_post", ctypes.c_void_p), ("d_pre", ctypes.c_void_p)]
+
+
+class MuGated(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("gate_out", ctypes.c_void_p), ("up_out", ctypes.c_void_p), ("tokens", ctypes.c_int64),
+                ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
+class MuGatedGrad(ctypes.Structure):
+    _fields_ = [("grad_h", ctypes.c_void_p), ("x", ctypes.c_void_p), ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("d_gate", ctypes.c_void_p),
+                ("d_up", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("dim", ctypes.c_int64), ("hidden", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("activation", ctypes.c_int32)]
+
+
 class MuonError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__(f"{_status_text(status)} (status {status}): {detail}")
@@ -162,6 +208,11 @@ def _load() -> ctypes.CDLL:
     lib.mu_embedding_grad.argtypes = [P(MuRowgrad), vp, sz, vp]
     lib.mu_qk_max_logits_workspace_size.argtypes = [P(MuQkLogits), P(sz)]
     lib.mu_qk_max_logits.argtypes = [P(MuQkLogits), vp, sz, vp]
+    lib.mu_rotary.argtypes = [P(MuRotaryArgs), vp]
+    lib.mu_residual_norm.argtypes = [P(MuResnorm), vp]
+    for name, args in (("mu_residual_norm_grad", MuResnormGrad), ("mu_gated_mlp", MuGated), ("mu_gated_mlp_grad", MuGatedGrad)):
+        getattr(lib, name + "_workspace_size").argtypes = [P(args), P(sz)]
+        getattr(lib, name).argtypes = [P(args), vp, sz, vp]
     lib.mu_status_string.argtypes = [ctypes.c_int]
     lib.mu_status_string.restype = ctypes.c_char_p
     lib.mu_last_error.argtypes = []
@@ -177,7 +228,9 @@ def _load() -> ctypes.CDLL:
                  "mu_adamw_workspace_size", "mu_adamw_step", "mu_profile_enable", "mu_profile_read",
                  "mu_muon_step_scaled", "mu_adamw_step_scaled", "mu_grad_norm_workspace_size", "mu_grad_norm",
                  "mu_clip_grads", "mu_embedding", "mu_embedding_grad_workspace_size", "mu_embedding_grad",
-                 "mu_qk_max_logits_workspace_size", "mu_qk_max_logits"):
+                 "mu_qk_max_logits_workspace_size", "mu_qk_max_logits", "mu_rotary", "mu_residual_norm",
+                 "mu_residual_norm_grad_workspace_size", "mu_residual_norm_grad", "mu_gated_mlp_workspace_size",
+                 "mu_gated_mlp", "mu_gated_mlp_grad_workspace_size", "mu_gated_mlp_grad"):
         getattr(lib, name).restype = ctypes.c_int
     return lib
 
@@ -437,12 +490,12 @@ def mu_clip_grads(gs, n, max_norm: float, eps: float, norm_out, scale_out, works
     _check(LIB.mu_clip_grads(gs, n, max_norm, eps, _ptr(norm_out), _ptr(scale_out), ws, nb, _stream(stream)))
 
 
-def _token_bits(t: torch.Tensor) -> int:
+def _token_bits(t: torch.Tensor, what: str = "tokens") -> int:
     if t.dtype == torch.int64:
         return 64
     if t.dtype == torch.int32:
         return 32
-    raise TypeError(f"tokens must be int32 or int64 (got {t.dtype})")
+    raise TypeError(f"{what} must be int32 or int64 (got {t.dtype})")
 
 
 def lookup(tokens, weight, out, scale: float) -> MuLookup:
@@ -541,6 +594,212 @@ def mu_qk_max_logits(a: MuQkLogits, workspace: Optional[torch.Tensor], stream=No
     ws = 0 if workspace is None else workspace.data_ptr()
     nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(LIB.mu_qk_max_logits(ctypes.byref(a), ws, nb, _stream(stream)))
+
+
+def rotary_args(xs, outs, freqs, positions, offset: int, interleaved: bool, inverse: bool, scale: float) -> MuRotaryArgs:
+    first = xs[0]
+    a = MuRotaryArgs()
+    shape = first.shape
+    packed = len(shape) == 3   # [rows, heads, dim]: one sequence
+    if len(shape) not in (3, 4):
+        raise ValueError("q and k must be [batch, length, heads, dim] or [rows, heads, dim]")
+    for i, (x, o) in enumerate(zip(xs, outs)):
+        if x.dtype != first.dtype or o.dtype != first.dtype:
+            raise TypeError("q, k and their outputs must share a dtype")
+        if x.shape[:-2] != shape[:-2] or x.shape[-1] != shape[-1]:
+            raise ValueError("q and k must agree in batch, length and dim")
+        if o.shape != x.shape:
+            raise ValueError("an output must have its input's shape")
+        sx, so = x.stride(), o.stride()
+        if shape[-1] > 1 and (sx[-1] != 1 or so[-1] != 1):
+            raise ValueError("the last dimension of q, k and their outputs must be contiguous")
+        if packed:
+            sx, so = (0, *sx), (0, *so)
+        a.x[i] = MuRotaryTensor(x.data_ptr(), o.data_ptr(), *sx[:3], *so[:3], x.shape[-2], 0)
+    if freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise TypeError("freqs must be a float64 vector (rotary_frequencies)")
+    _require(freqs, "freqs")
+    a.batch, a.len = (1, shape[0]) if packed else shape[:2]
+    if positions is not None:
+        rows = shape[:-2]
+        if positions.shape != rows and positions.shape != rows[-1:]:
+            raise ValueError(f"positions must be {list(rows)} or {list(rows[-1:])}")
+        a.position_bits = _token_bits(positions, "positions")
+        a.shared_positions = 1 if positions.shape != rows else 0
+        _require(positions, "positions")
+        a.positions = positions.data_ptr()
+    a.freqs, a.offset, a.n, a.dim, a.part = freqs.data_ptr(), int(offset), len(xs), shape[-1], 2 * freqs.numel()
+    a.interleaved, a.inverse, a.dtype, a.scale = 1 if interleaved else 0, 1 if inverse else 0, _dtype_code(first), float(scale)
+    return a
+
+
+def mu_rotary(a: MuRotaryArgs, stream=None) -> None:
+    _check(LIB.mu_rotary(ctypes.byref(a), _stream(stream)))
+
+
+def resnorm(residual, update, gate, post_weight, pre_weight, new_residual, normed, post_norm: bool, residual_scale: float,
+            eps: float) -> MuResnorm:
+    """residual [..., dim] is the residual, or in a gradient call the shape and
+    type of it (new_residual then)."""
+    base = residual if residual is not None else new_residual
+    dim = base.shape[-1]
+    rows = base.numel() // dim if dim else 0
+    for t, what in ((residual, "residual"), (update, "update"), (new_residual, "new_residual"), (normed, "normed")):
+        if t is None:
+            continue
+        _require(t, what)
+        if t.shape != base.shape:
+            raise ValueError(f"{what} must have the residual's shape")
+    if new_residual is not None and new_residual.dtype != base.dtype:
+        raise TypeError("new_residual must share the residual's dtype")
+    kind = update if update is not None else normed if normed is not None else base
+    if normed is not None and normed.dtype != kind.dtype:
+        raise TypeError("normed must share the update's dtype")
+    first = None   # of the weights and the gate
+    for t, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight"), (gate, "gate")):
+        if t is None:
+            continue
+        _require(t, what)
+        if first is not None and t.dtype != first.dtype:
+            raise TypeError("the weights and the gate must share a dtype")
+        first = t
+        if t is not gate and t.shape != (dim,):
+            raise ValueError(f"{what} must be [{dim}]")
+    groups = 1
+    if gate is not None:
+        if gate.dim() not in (1, 2) or gate.shape[-1] != dim:
+            raise ValueError(f"gate must be [{dim}] or [groups, {dim}]")
+        groups = gate.numel() // dim if dim else 0
+    return MuResnorm(_ptr(residual), _ptr(update), _ptr(gate), _ptr(post_weight), _ptr(pre_weight), _ptr(new_residual),
+                     _ptr(normed), rows, dim, groups, _dtype_code(base), _dtype_code(kind),
+                     MU_F32 if first is None else _dtype_code(first),
+                     1 if post_norm else 0, float(residual_scale), float(eps))
+
+
+def mu_residual_norm(a: MuResnorm, stream=None) -> None:
+    _check(LIB.mu_residual_norm(ctypes.byref(a), _stream(stream)))
+
+
+def resnorm_grad(grad_residual, grad_normed, r, update, gate, post_weight, pre_weight, post_norm: bool, residual_scale: float,
+                 eps: float, results) -> MuResnormGrad:
+    """r is new_residual, or x without an update; results (d_residual, d_update,
+    d_gate, d_post, d_pre) are new tensors of their inputs' shapes and types."""
+    for t, what in ((grad_residual, "grad_residual"), (grad_normed, "grad_normed")):
+        if t is not None:
+            _require(t, what)
+            if t.shape != r.shape:
+                raise ValueError(f"{what} must have the residual's shape")
+    if grad_residual is not None and grad_residual.dtype != r.dtype:
+        raise TypeError("grad_residual must share the residual's dtype")
+    if update is None:
+        f = resnorm(r, None, gate, post_weight, pre_weight, None, None, post_norm, residual_scale, eps)
+        if grad_normed is not None:
+            f.dtype = _dtype_code(grad_normed)
+    else:
+        f = resnorm(None, update, gate, post_weight, pre_weight, r, None, post_norm, residual_scale, eps)
+        if grad_normed is not None and grad_normed.dtype != update.dtype:
+            raise TypeError("grad_normed must share the update's dtype")
+    return MuResnormGrad(f, _ptr(grad_residual), _ptr(grad_normed), *map(_ptr, results))
+
+
+def mu_residual_norm_grad_workspace_size(a: MuResnormGrad) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_residual_norm_grad_workspace_size(ctypes.byref(a), ctypes.byref(out)))
+    return out.value
+
+
+def mu_residual_norm_grad(a: MuResnormGrad, workspace: Optional[torch.Tensor], stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_residual_norm_grad(ctypes.byref(a), ws, nb, _stream(stream)))
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)} (got {name!r})")
+    return ACTIVATIONS[name]
+
+
+def _gated_sizes(x, w_gate, w_up):
+    for t, what in ((x, "x"), (w_gate, "w_gate"), (w_up, "w_up")):
+        _require(t, what)
+        if t.dtype != x.dtype:
+            raise TypeError("x, w_gate and w_up must share a dtype")
+    if w_gate.dim() != 2 or w_up.shape != w_gate.shape:
+        raise ValueError("w_gate and w_up must be 2-D and of one shape")
+    if x.dim() < 1 or x.shape[-1] != w_gate.shape[1]:
+        raise ValueError("x must be [..., dim] with the weights' row length")
+    hidden, dim = w_gate.shape
+    return x.numel() // dim if dim else 0, dim, hidden
+
+
+def gated(x, w_gate, w_up, h, gates, activation: str) -> MuGated:
+    tokens, dim, hidden = _gated_sizes(x, w_gate, w_up)
+    _require(h, "out")
+    if h.shape != x.shape[:-1] + (hidden,) or h.dtype != x.dtype:
+        raise ValueError("out must have x's dtype and shape with hidden in the last place")
+    if gates is not None:
+        _require(gates, "gates")
+        if gates.shape != (2,) + h.shape or gates.dtype != x.dtype:
+            raise ValueError("gates must be [2, *out's shape] of x's dtype")
+    half = 0 if gates is None else tokens * hidden * gates.element_size()
+    base = _ptr(gates)
+    return MuGated(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), base, base + half if base else None, tokens, dim, hidden,
+                   _dtype_code(x), _activation(activation))
+
+
+def mu_gated_mlp_workspace_size(a: MuGated) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_gated_mlp_workspace_size(ctypes.byref(a), ctypes.byref(out)))
+    return out.value
+
+
+def mu_gated_mlp(a: MuGated, workspace: Optional[torch.Tensor], stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_gated_mlp(ctypes.byref(a), ws, nb, _stream(stream)))
+
+
+def gated_grad(grad, x, w_gate, w_up, gates, dx, d_gate, d_up, accumulate: bool, activation: str) -> MuGatedGrad:
+    tokens, dim, hidden = _gated_sizes(x, w_gate, w_up)
+    _require(grad, "grad")
+    if grad.shape != x.shape[:-1] + (hidden,) or grad.dtype != x.dtype:
+        raise ValueError("grad must have x's dtype and shape with hidden in the last place")
+    if gates is not None:
+        _require(gates, "gates")
+        if gates.shape != (2,) + grad.shape or gates.dtype != x.dtype:
+            raise ValueError("gates must be [2, *grad's shape] of x's dtype")
+    if dx is not None:
+        _require(dx, "dx")
+        if dx.shape != x.shape or dx.dtype != x.dtype:
+            raise ValueError("dx must have x's shape and dtype")
+    for t, what in ((d_gate, "d_gate"), (d_up, "d_up")):
+        if t is not None:
+            _require(t, what)
+            if t.shape != w_gate.shape:
+                raise ValueError(f"{what} must have the weights' shape")
+    if d_gate is not None and d_up is not None and d_gate.dtype != d_up.dtype:
+        raise TypeError("d_gate and d_up must share a dtype")
+    half = 0 if gates is None else tokens * hidden * gates.element_size()
+    base = _ptr(gates)
+    return MuGatedGrad(_ptr(grad), _ptr(x), _ptr(w_gate), _ptr(w_up), base, base + half if base else None, _ptr(dx),
+                       _ptr(d_gate), _ptr(d_up), tokens, dim, hidden, _dtype_code(x),
+                       _dtype_code(x if d_gate is None else d_gate), 1 if accumulate else 0, _activation(activation))
+
+
+def mu_gated_mlp_grad_workspace_size(a: MuGatedGrad) -> int:
+    out = ctypes.c_size_t(0)
+    _check(LIB.mu_gated_mlp_grad_workspace_size(ctypes.byref(a), ctypes.byref(out)))
+    return out.value
+
+
+def mu_gated_mlp_grad(a: MuGatedGrad, workspace: Optional[torch.Tensor], stream=None) -> None:
+    ws = 0 if workspace is None else workspace.data_ptr()
+    nb = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(LIB.mu_gated_mlp_grad(ctypes.byref(a), ws, nb, _stream(stream)))
 
 
 def qk_pairs(wqs, wks, max_logits, q_heads, k_heads, gamma_outs=None):

@@ -1,6 +1,7 @@
 """Tensor-level calls over the C ABI: one Muon step, orthogonalise-only, AdamW,
 QK-Clip, and what feeds them (gradient norm and clipping, the embedding and its
-gradient, attention max logits).
+gradient, attention max logits, and the parts of a block between its products:
+rotary positions, the norms around the block, the gated feed-forward product).
 
 Each function marshals torch tensors into the library's descriptor lists,
 allocates the workspace the library asks for (unless one is passed in) and
@@ -9,8 +10,9 @@ results allocated here come from `stream`'s share of the caching allocator, so
 that neither the work that used their memory before nor the work that gets it
 next overlaps the library's kernels; a result is recorded on the current stream
 too. The caller orders `stream` behind what made the inputs, and its own use of
-the results behind `stream`. Nothing here computes. Of the results only
-embedding's carries a gradient.
+the results behind `stream`. Nothing here computes. Of the results those of
+embedding, rotary, residual_norm, rms_norm and gated_mlp carry gradients (not in
+forward mode, which they refuse, and once: a gradient of a gradient is refused).
 """
 
 from __future__ import annotations
@@ -139,6 +141,25 @@ def _new(shape, dtype, device: int, stream) -> torch.Tensor:
                          returned=True)
 
 
+def _no_tangents(what: str, *tensors):
+    if forward_ad._current_level >= 0 and any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError(f"{what} has no forward-mode derivative")
+
+
+def _differentiable(what: str, tensors, *outs) -> bool:
+    """Whether a call needs autograd; then it writes no buffers of the caller's."""
+    _no_tangents(what, *tensors)
+    if not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)):
+        return False
+    if any(o is not None for o in outs):
+        raise ValueError("outputs of the caller's take no gradient: call under torch.no_grad()")
+    return True
+
+
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    return None if t is None else t.contiguous()   # autograd hands in expanded or transposed gradients too
+
+
 def grad_norm(grads: Sequence[torch.Tensor], *, max_norm: float = math.inf, eps: float = 1e-6,
               norm_out: Optional[torch.Tensor] = None, scale_out: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -186,8 +207,7 @@ def embedding(tokens: torch.Tensor, weight: torch.Tensor, *, scale: float = 1.0,
     asks of any: no eager graph of the same leaf alive meanwhile."""
     if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
         raise ValueError("padding_idx must name a row of the weight")
-    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(weight).tangent is not None:
-        raise NotImplementedError("embedding has no forward-mode derivative")
+    _no_tangents("embedding", weight)
     if torch.is_grad_enabled() and weight.requires_grad:
         if out is not None:
             raise ValueError("out takes no gradient: call under torch.no_grad()")
@@ -280,4 +300,273 @@ def qk_max_logits(q: torch.Tensor, k: torch.Tensor, *, scale: Optional[float] = 
         ws = _lib.scratch(_lib.mu_qk_max_logits_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_qk_max_logits(a, ws, st)
         return o
+    return _on(device, stream, call)
+
+
+def rotary_frequencies(part: int, *, base: float = 10000.0, factor: float = 1.0, original_length: Optional[float] = None,
+                       low: float = 1.0, high: float = 32.0, device=None) -> torch.Tensor:
+    """The frequencies f_i = base ** (-2 i / part), i < part / 2, that rotary
+    takes: radians a position, float64, on `device` (default: the current GPU).
+
+    For contexts `factor` times as long as those a model was trained on: without
+    original_length every frequency is divided by factor; with it, by parts. A
+    frequency that makes r = original_length f / 2 pi turns over the original
+    length is divided by factor where r <= low, kept where r >= high, and
+    between them f (y + (1 - y) / factor) with y = (r - low) / (high - low)."""
+    if part < 2 or part % 2:
+        raise ValueError("part must be even and at least 2")
+    if not base > 0 or not factor > 0 or math.isinf(base) or math.isinf(factor):
+        raise ValueError("base and factor must be > 0 and finite")
+    f = float(base) ** (-torch.arange(0, part, 2, dtype=torch.float64) / part)
+    if original_length is None:
+        f = f / factor
+    else:
+        if not original_length > 0 or not high > low:
+            raise ValueError("original_length must be > 0 and high above low")
+        y = ((original_length * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (y + (1 - y) / factor)
+    return f.to("cuda" if device is None else device)
+
+
+def rotary(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, freqs: torch.Tensor,
+           positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False, scale: float = 1.0,
+           inverse: bool = False, out=None, stream=None):
+    """Rotary positions: the first 2 * len(freqs) elements of every head of q
+    (and k) turn by position * freqs, pair by pair, times scale; the rest of the
+    head is copied. Returns the turned q, or (q, k).
+
+    q [batch, length, heads, dim] and k [batch, length, k_heads, dim], or packed
+    [rows, heads, dim], may be strided views (of a fused projection) with a
+    contiguous last dimension. Pairs are (i, i + half) of that part, or (2 i,
+    2 i + 1) with interleaved. positions (int32 or int64, [batch, length], [length]
+    or [rows]) default to 0, 1, ..; offset is added to them. inverse turns back.
+    freqs: float64 (rotary_frequencies). `out` (q's, or a pair) may be the inputs
+    themselves. Differentiable in q and k unless `out` is given."""
+    xs = (q,) if k is None else (q, k)
+    if out is not None:
+        out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
+        if len(out) != len(xs):
+            raise ValueError("out must have one tensor for each of q and k")
+    if _differentiable("rotary", xs, out):
+        res = _Rotary.apply(q, k, freqs, positions, int(offset), interleaved, float(scale), inverse, stream)
+        return res[0] if k is None else res
+    res = _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stream)
+    return res[0] if k is None else res
+
+
+def _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stream):
+    device = _lib.device_of((*xs, *(out or ()), freqs, positions), "q, k, freqs, positions and out")
+
+    def call(st):
+        outs = out if out is not None else tuple(_new(x.shape, x.dtype, device, stream) for x in xs)
+        _lib.mu_rotary(_lib.rotary_args(xs, outs, freqs, positions, offset, interleaved, inverse, scale), st)
+        return outs
+    return _on(device, stream, call)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, freqs, positions, offset, interleaved, scale, inverse, stream):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(freqs, positions)
+        ctx.spec = (offset, interleaved, scale, not inverse)
+        return _rotary((q,) if k is None else (q, k), freqs, positions, offset, interleaved, scale, inverse, None, stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        freqs, positions = ctx.saved_tensors
+        offset, interleaved, scale, inverse = ctx.spec
+        wanted = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
+        res = [None, None]
+        if wanted:
+            xs = tuple(g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous() for g in (grads[i] for i in wanted))
+            for i, g in zip(wanted, _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, None, None)):
+                res[i] = g
+        return (*res, None, None, None, None, None, None, None)
+
+
+def residual_norm(residual: torch.Tensor, update: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                  post_norm: bool = False, post_weight: Optional[torch.Tensor] = None,
+                  pre_weight: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                  out: Optional[torch.Tensor] = None, normed_out: Optional[torch.Tensor] = None, stream=None):
+    """What stands between two blocks, in one pass, with N(v; w) = v /
+    sqrt(mean(v ** 2) + eps) * w over the last dimension:
+
+        new_residual = residual_scale * residual + gate * N(update; post_weight)
+        normed       = N(new_residual; pre_weight)          (the next block's input)
+
+    Returns (new_residual, normed). The norm of the update is taken with
+    post_norm=True or a post_weight; absent weights are 1. gate is [dim], or
+    [groups, dim] whose rows apply to equal runs of the rows in turn (a gate for
+    each sequence of a batch, or for each token). normed has the update's dtype;
+    residual is of the same or float32 beside a bfloat16 update; weights and gate
+    share either dtype. `out` may be the residual itself, normed_out the update.
+    Differentiable in all tensors unless buffers are given."""
+    if update is None:
+        raise TypeError("update must be a tensor (rms_norm normalises without one)")
+    post_norm = bool(post_norm) or post_weight is not None
+    tensors = (residual, update, gate, post_weight, pre_weight)
+    if _differentiable("residual_norm", tensors, out, normed_out):
+        return _ResidualNorm.apply(*tensors, post_norm, float(residual_scale), float(eps), None, stream)
+    return _residual_norm(*tensors, post_norm, residual_scale, eps, None, out, normed_out, stream)
+
+
+def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+             dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x / sqrt(mean(x ** 2) + eps) * weight over the last dimension: the norm
+    before the first block. dtype is the result's (default: x's; bfloat16 beside a
+    float32 x). Differentiable in x and weight unless `out` is given."""
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise TypeError("dtype differs from out's")
+    dtype = out.dtype if out is not None else x.dtype if dtype is None else dtype
+    if _differentiable("rms_norm", (x, weight), out):
+        return _ResidualNorm.apply(x, None, None, None, weight, False, 1.0, float(eps), dtype, stream)
+    return _residual_norm(x, None, None, None, weight, False, 1.0, eps, dtype, None, out, stream)
+
+
+def _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, out, normed_out,
+                   stream):
+    device = _lib.device_of((residual, update, gate, post_weight, pre_weight, out, normed_out),
+                            "residual, update, weights, gate and outputs")
+
+    def call(st):
+        r = out
+        if r is None and update is not None:
+            r = _new(residual.shape, residual.dtype, device, stream)
+        n = normed_out
+        if n is None:
+            n = _new(residual.shape, dtype if update is None else update.dtype, device, stream)
+        _lib.mu_residual_norm(_lib.resnorm(residual, update, gate, post_weight, pre_weight, r, n, post_norm,
+                                           residual_scale, eps), st)
+        return n if update is None else (r, n)
+    return _on(device, stream, call)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, stream):
+        ctx.set_materialize_grads(False)
+        ctx.spec = (post_norm, residual_scale, eps, update is not None)
+        res = _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, None,
+                             None, stream)
+        ctx.save_for_backward(residual if update is None else res[0], update, gate, post_weight, pre_weight)
+        return res
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        r, update, gate, post_weight, pre_weight = ctx.saved_tensors
+        post_norm, residual_scale, eps, has_update = ctx.spec
+        dr, dn = grads if has_update else (None, grads[0])
+        res = (None,) * 5
+        if dr is not None or dn is not None:
+            res = _residual_norm_grad(_dense(dr), _dense(dn), r, update, gate, post_weight, pre_weight, post_norm,
+                                      residual_scale, eps, ctx.needs_input_grad[:5], None, None)
+        return (*res, None, None, None, None, None)
+
+
+def residual_norm_grad(grad_residual: Optional[torch.Tensor], grad_normed: Optional[torch.Tensor],
+                       new_residual: torch.Tensor, update: Optional[torch.Tensor], *, gate: Optional[torch.Tensor] = None,
+                       post_norm: bool = False, post_weight: Optional[torch.Tensor] = None,
+                       pre_weight: Optional[torch.Tensor] = None, residual_scale: float = 1.0, eps: float = 1e-6,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gradients (residual, update, gate, post_weight, pre_weight) of
+    residual_norm from those of its results (None: zero) and the new_residual it
+    returned; None where there is no such tensor. Of rms_norm: update None and x
+    in the place of new_residual. Sums over rows are float32 in a fixed order."""
+    return _residual_norm_grad(grad_residual, grad_normed, new_residual, update, gate, post_weight, pre_weight,
+                               bool(post_norm) or post_weight is not None, residual_scale, eps, (True,) * 5, workspace, stream)
+
+
+def _residual_norm_grad(dr, dn, r, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, need, workspace,
+                        stream):
+    device = _lib.device_of((dr, dn, r, update, gate, post_weight, pre_weight, workspace), "gradients, inputs and weights")
+
+    def call(st):
+        res = tuple(_new(t.shape, t.dtype, device, stream) if t is not None and wanted else None
+                    for t, wanted in zip((r, update, gate, post_weight, pre_weight), need))
+        a = _lib.resnorm_grad(dr, dn, r, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, res)
+        ws = _lib.scratch(_lib.mu_residual_norm_grad_workspace_size(a), device, stream) if workspace is None else workspace
+        _lib.mu_residual_norm_grad(a, ws, st)
+        return res
+    return _on(device, stream, call)
+
+
+def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, activation: str = "silu",
+              save_gates: bool = True, out: Optional[torch.Tensor] = None, gates_out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(x @ w_gate.T) * (x @ w_up.T), the input of a gated feed-forward
+    block's last projection, in one kernel: x [..., dim], weights [hidden, dim],
+    result [..., hidden], of one dtype. activation: "silu", "gelu", "gelu_tanh" or
+    "relu". gates_out [2, ..., hidden] receives both products, which gated_mlp_grad
+    reads. Differentiable in x and the weights unless buffers are given;
+    save_gates=False keeps no products for it and computes them again."""
+    if _differentiable("gated_mlp", (x, w_gate, w_up), out, gates_out):
+        return _GatedMlp.apply(x, w_gate, w_up, activation, bool(save_gates), workspace, stream)
+    return _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream)
+
+
+def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, save=False):
+    device = _lib.device_of((x, w_gate, w_up, out, gates_out, workspace), "x, weights and outputs")
+
+    def call(st):
+        shape = x.shape[:-1] + w_gate.shape[:1]
+        h = _new(shape, x.dtype, device, stream) if out is None else out
+        gates = _new((2, *shape), x.dtype, device, stream) if save else gates_out
+        a = _lib.gated(x, w_gate, w_up, h, gates, activation)
+        ws = _lib.scratch(_lib.mu_gated_mlp_workspace_size(a), device, stream) if workspace is None else workspace
+        _lib.mu_gated_mlp(a, ws, st)
+        return (h, gates) if save else h
+    return _on(device, stream, call)
+
+
+class _GatedMlp(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w_gate, w_up, activation, save_gates, workspace, stream):
+        ctx.activation = activation
+        h, gates = _gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream, save=True) if save_gates else \
+            (_gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream), None)
+        ctx.save_for_backward(x, w_gate, w_up, gates)
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        x, w_gate, w_up, gates = ctx.saved_tensors
+        need_x, need_gate, need_up = ctx.needs_input_grad[:3]
+        dx, d_gate, d_up = gated_mlp_grad(grad.contiguous(), x, w_gate, w_up, gates, activation=ctx.activation, need_x=need_x,
+                                          need_weights=need_gate or need_up)
+        return dx, d_gate if need_gate else None, d_up if need_up else None, None, None, None, None
+
+
+def gated_mlp_grad(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                   gates: Optional[torch.Tensor] = None, *, activation: str = "silu", need_x: bool = True,
+                   need_weights: bool = True, d_gate: Optional[torch.Tensor] = None, d_up: Optional[torch.Tensor] = None,
+                   dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                   workspace: Optional[torch.Tensor] = None, stream=None):
+    """The gradients (dx, d_gate, d_up) of gated_mlp from its result's. gates is
+    the forward call's gates_out (None: both products are computed again). d_gate
+    and d_up receive the weights' gradients, of x's dtype or float32
+    (accumulate=True: added to them, over the micro-batches of a step); dtype is
+    that of new ones (default: x's). The same call gives the same bits."""
+    if (d_gate is None) != (d_up is None):
+        raise ValueError("d_gate and d_up go together")
+    if d_gate is not None and not need_weights:
+        raise ValueError("d_gate and d_up without need_weights")
+    if accumulate and d_gate is None:
+        raise ValueError("accumulate=True needs d_gate and d_up")
+    if d_gate is not None and dtype is not None and d_gate.dtype != dtype:
+        raise TypeError("dtype differs from d_gate's")
+    device = _lib.device_of((grad, x, w_gate, w_up, gates, d_gate, d_up, workspace), "grad, x, weights and results")
+
+    def call(st):
+        dx = _new(x.shape, x.dtype, device, stream) if need_x else None
+        dg, du = d_gate, d_up
+        if dg is None and need_weights:
+            dg, du = (_new(w_gate.shape, x.dtype if dtype is None else dtype, device, stream) for _ in range(2))
+        a = _lib.gated_grad(grad, x, w_gate, w_up, gates, dx, dg, du, accumulate, activation)
+        ws = _lib.scratch(_lib.mu_gated_mlp_grad_workspace_size(a), device, stream) if workspace is None else workspace
+        _lib.mu_gated_mlp_grad(a, ws, st)
+        return dx, dg, du
     return _on(device, stream, call)

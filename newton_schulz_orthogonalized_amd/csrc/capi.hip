@@ -1779,6 +1779,11 @@ const char* mu_kernel_name(int k) {
         case MU_K_LOOKUP: return "embedding";
         case MU_K_ROWGRAD: return "embedding_grad";
         case MU_K_QKMAX: return "qk_max_logits";
+        case MU_K_ROTARY: return "rotary";
+        case MU_K_RESNORM: return "residual_norm";
+        case MU_K_RESNORM_GRAD: return "residual_norm_grad";
+        case MU_K_GATED: return "gated_mlp";
+        case MU_K_GATED_GRAD: return "gated_mlp_grad";
         default: return "unknown";
     }
 }
