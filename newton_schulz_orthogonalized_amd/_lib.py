@@ -637,6 +637,30 @@ def mu_rotary(a: MuRotaryArgs, stream=None) -> None:
     _check(LIB.mu_rotary(ctypes.byref(a), _stream(stream)))
 
 
+def rotary_call(stream, a: MuRotaryArgs) -> None:
+    status = LIB.mu_rotary(ctypes.byref(a), stream)
+    if status:
+        _check(status)
+
+
+def rotary_grad(t: MuRotaryTensor, g):
+    """Point one tensor of a backward call at its result's gradient and at a new
+    tensor for its own: (the gradient as it is read, the new tensor). Both have the
+    layout of the forward call's result, which t's out_stride_* are, if the
+    gradient is dense."""
+    if not g.is_contiguous():
+        if g.shape[-1] > 1 and g.stride(-1) != 1:
+            g = g.contiguous()
+    d = torch.empty_like(g, memory_format=torch.contiguous_format)
+    if g.is_contiguous():
+        t.x_stride_b, t.x_stride_s, t.x_stride_h = t.out_stride_b, t.out_stride_s, t.out_stride_h
+    else:
+        s = g.stride()
+        t.x_stride_b, t.x_stride_s, t.x_stride_h = s[:3] if len(s) == 4 else (0, *s[:2])
+    t.x, t.out = g.data_ptr(), d.data_ptr()
+    return g, d
+
+
 def resnorm(residual, update, gate, post_weight, pre_weight, new_residual, normed, post_norm: bool, residual_scale: float,
             eps: float) -> MuResnorm:
     """residual [..., dim] is the residual, or in a gradient call the shape and
@@ -700,6 +724,36 @@ def resnorm_grad(grad_residual, grad_normed, r, update, gate, post_weight, pre_w
         if grad_normed is not None and grad_normed.dtype != update.dtype:
             raise TypeError("grad_normed must share the update's dtype")
     return MuResnormGrad(f, _ptr(grad_residual), _ptr(grad_normed), *map(_ptr, results))
+
+
+def resnorm_backward(args: MuResnorm, saved, need, dr, dn):
+    """(MuResnormGrad, gradients) of a forward call's struct: saved (r, update,
+    gate, post_weight, pre_weight), need which of their gradients, dr and dn those
+    of the results, dense."""
+    r, update, gate, post, pre = saved
+    f = MuResnorm.from_buffer_copy(args)
+    f.residual = f.new_residual = f.normed = None
+    if update is None:
+        f.residual = r.data_ptr()
+    else:
+        f.new_residual, f.update = r.data_ptr(), update.data_ptr()
+    if gate is not None:
+        f.gate = gate.data_ptr()
+    if post is not None:
+        f.post_weight = post.data_ptr()
+    if pre is not None:
+        f.pre_weight = pre.data_ptr()
+    res = [torch.empty_like(t) if t is not None and w else None for t, w in zip(saved, need)]
+    return MuResnormGrad(f, dr.data_ptr() if dr is not None else None, dn.data_ptr() if dn is not None else None,
+                         *[None if t is None else t.data_ptr() for t in res]), res
+
+
+def resnorm_grad_call(stream, a: MuResnormGrad, like) -> None:
+    need = ctypes.c_size_t(0)
+    ref = ctypes.byref(a)
+    _check(LIB.mu_residual_norm_grad_workspace_size(ref, ctypes.byref(need)))
+    ws = scratch(need.value, like.get_device())
+    _check(LIB.mu_residual_norm_grad(ref, _ptr(ws), need.value, stream))
 
 
 def mu_residual_norm_grad_workspace_size(a: MuResnormGrad) -> int:
@@ -788,6 +842,33 @@ def gated_grad(grad, x, w_gate, w_up, gates, dx, d_gate, d_up, accumulate: bool,
     return MuGatedGrad(_ptr(grad), _ptr(x), _ptr(w_gate), _ptr(w_up), base, base + half if base else None, _ptr(dx),
                        _ptr(d_gate), _ptr(d_up), tokens, dim, hidden, _dtype_code(x),
                        _dtype_code(x if d_gate is None else d_gate), 1 if accumulate else 0, _activation(activation))
+
+
+def gated_backward(args: MuGatedGrad, saved, need, grad):
+    """(MuGatedGrad, gradients of x and the weights) with a forward call's sizes:
+    saved (x, w_gate, w_up, gates or None), need which gradients, grad dense."""
+    x, w_gate, w_up, gates = saved
+    a = MuGatedGrad.from_buffer_copy(args)
+    a.grad_h, a.x, a.w_gate, a.w_up = grad.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
+    if gates is not None:
+        a.gate = gates.data_ptr()
+        a.up = a.gate + grad.numel() * grad.element_size() if a.gate else None
+    dx = dg = du = None
+    if need[0]:
+        dx = torch.empty_like(x)
+        a.dx = dx.data_ptr()
+    if need[1] or need[2]:
+        dg, du = torch.empty_like(w_gate), torch.empty_like(w_up)
+        a.d_gate, a.d_up = dg.data_ptr(), du.data_ptr()
+    return a, (dx, dg if need[1] else None, du if need[2] else None, dg, du)
+
+
+def gated_grad_call(stream, a: MuGatedGrad, like) -> None:
+    need = ctypes.c_size_t(0)
+    ref = ctypes.byref(a)
+    _check(LIB.mu_gated_mlp_grad_workspace_size(ref, ctypes.byref(need)))
+    ws = scratch(need.value, like.get_device())
+    _check(LIB.mu_gated_mlp_grad(ref, _ptr(ws), need.value, stream))
 
 
 def mu_gated_mlp_grad_workspace_size(a: MuGatedGrad) -> int:

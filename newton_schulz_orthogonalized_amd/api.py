@@ -137,6 +137,8 @@ def _on(device: int, stream, call, *args):
 
 
 def _new(shape, dtype, device: int, stream) -> torch.Tensor:
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     return _lib.allocate(lambda: torch.empty(shape, dtype=dtype, device=torch.device("cuda", device)), device, stream,
                          returned=True)
 
@@ -154,6 +156,16 @@ def _differentiable(what: str, tensors, *outs) -> bool:
     if any(o is not None for o in outs):
         raise ValueError("outputs of the caller's take no gradient: call under torch.no_grad()")
     return True
+
+
+def _once(backward):
+    """torch's once_differentiable, whose own work is a good part of a small
+    call's, only where a graph of the gradient is asked for."""
+    guarded = torch.autograd.function.once_differentiable(backward)
+
+    def call(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+    return call
 
 
 def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
@@ -348,9 +360,9 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, freqs: torch.Te
         if len(out) != len(xs):
             raise ValueError("out must have one tensor for each of q and k")
     if _differentiable("rotary", xs, out):
-        res = _Rotary.apply(q, k, freqs, positions, int(offset), interleaved, float(scale), inverse, stream)
-        return res[0] if k is None else res
-    res = _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stream)
+        res = _Rotary.apply(q, k, freqs, positions, offset, interleaved, scale, inverse, stream)
+    else:
+        res = _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stream)[0]
     return res[0] if k is None else res
 
 
@@ -358,32 +370,49 @@ def _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stre
     device = _lib.device_of((*xs, *(out or ()), freqs, positions), "q, k, freqs, positions and out")
 
     def call(st):
-        outs = out if out is not None else tuple(_new(x.shape, x.dtype, device, stream) for x in xs)
-        _lib.mu_rotary(_lib.rotary_args(xs, outs, freqs, positions, offset, interleaved, inverse, scale), st)
-        return outs
+        outs = out if out is not None else tuple([_new(x.shape, x.dtype, device, stream) for x in xs])
+        a = _lib.rotary_args(xs, outs, freqs, positions, offset, interleaved, inverse, scale)
+        _lib.mu_rotary(a, st)
+        return outs, a
     return _on(device, stream, call)
 
 
+# The backward passes below run on a thread of autograd's, where every Python
+# object that the forward call touched on its own thread costs a transfer between
+# cores: they start from the structs that the forward calls filled and set
+# addresses alone (the saved tensors', as they may have been moved meanwhile).
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, freqs, positions, offset, interleaved, scale, inverse, stream):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(freqs, positions)
-        ctx.spec = (offset, interleaved, scale, not inverse)
-        return _rotary((q,) if k is None else (q, k), freqs, positions, offset, interleaved, scale, inverse, None, stream)
+        outs, a = _rotary((q,) if k is None else (q, k), freqs, positions, offset, interleaved, scale, inverse, None, stream)
+        a.inverse ^= 1
+        ctx.args = a
+        return outs
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, *grads):
+    @_once
+    def backward(ctx, gq, gk=None):
         freqs, positions = ctx.saved_tensors
-        offset, interleaved, scale, inverse = ctx.spec
-        wanted = [i for i, g in enumerate(grads) if g is not None and ctx.needs_input_grad[i]]
-        res = [None, None]
-        if wanted:
-            xs = tuple(g if g.stride(-1) == 1 or g.shape[-1] == 1 else g.contiguous() for g in (grads[i] for i in wanted))
-            for i, g in zip(wanted, _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, None, None)):
-                res[i] = g
-        return (*res, None, None, None, None, None, None, None)
+        a = _lib.MuRotaryArgs.from_buffer_copy(ctx.args)
+        a.freqs = freqs.data_ptr()
+        if positions is not None:
+            a.positions = positions.data_ptr()
+        dq = dk = None
+        n = 0
+        if gq is not None and ctx.needs_input_grad[0]:
+            gq, dq = _lib.rotary_grad(a.x[0], gq)
+            n = 1
+        if gk is not None and ctx.needs_input_grad[1]:
+            gk, dk = _lib.rotary_grad(a.x[1], gk)
+            if n == 0:
+                a.x[0] = a.x[1]
+            n += 1
+        if n:
+            a.n = n
+            _on(freqs.get_device(), None, _lib.rotary_call, a)
+        return dq, dk, None, None, None, None, None, None, None
 
 
 def residual_norm(residual: torch.Tensor, update: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
@@ -408,8 +437,8 @@ def residual_norm(residual: torch.Tensor, update: torch.Tensor, *, gate: Optiona
     post_norm = bool(post_norm) or post_weight is not None
     tensors = (residual, update, gate, post_weight, pre_weight)
     if _differentiable("residual_norm", tensors, out, normed_out):
-        return _ResidualNorm.apply(*tensors, post_norm, float(residual_scale), float(eps), None, stream)
-    return _residual_norm(*tensors, post_norm, residual_scale, eps, None, out, normed_out, stream)
+        return _ResidualNorm.apply(*tensors, post_norm, residual_scale, eps, None, stream)
+    return _residual_norm(*tensors, post_norm, residual_scale, eps, None, out, normed_out, stream)[:2]
 
 
 def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
@@ -421,8 +450,8 @@ def rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *, eps: flo
         raise TypeError("dtype differs from out's")
     dtype = out.dtype if out is not None else x.dtype if dtype is None else dtype
     if _differentiable("rms_norm", (x, weight), out):
-        return _ResidualNorm.apply(x, None, None, None, weight, False, 1.0, float(eps), dtype, stream)
-    return _residual_norm(x, None, None, None, weight, False, 1.0, eps, dtype, None, out, stream)
+        return _ResidualNorm.apply(x, None, None, None, weight, False, 1.0, eps, dtype, stream)
+    return _residual_norm(x, None, None, None, weight, False, 1.0, eps, dtype, None, out, stream)[1]
 
 
 def _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, out, normed_out,
@@ -437,9 +466,9 @@ def _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, r
         n = normed_out
         if n is None:
             n = _new(residual.shape, dtype if update is None else update.dtype, device, stream)
-        _lib.mu_residual_norm(_lib.resnorm(residual, update, gate, post_weight, pre_weight, r, n, post_norm,
-                                           residual_scale, eps), st)
-        return n if update is None else (r, n)
+        a = _lib.resnorm(residual, update, gate, post_weight, pre_weight, r, n, post_norm, residual_scale, eps)
+        _lib.mu_residual_norm(a, st)
+        return r, n, a
     return _on(device, stream, call)
 
 
@@ -447,22 +476,21 @@ class _ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, stream):
         ctx.set_materialize_grads(False)
-        ctx.spec = (post_norm, residual_scale, eps, update is not None)
-        res = _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype, None,
-                             None, stream)
-        ctx.save_for_backward(residual if update is None else res[0], update, gate, post_weight, pre_weight)
-        return res
+        r, n, ctx.args = _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, residual_scale, eps, dtype,
+                                        None, None, stream)
+        ctx.save_for_backward(residual if update is None else r, update, gate, post_weight, pre_weight)
+        return n if update is None else (r, n)
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, *grads):
-        r, update, gate, post_weight, pre_weight = ctx.saved_tensors
-        post_norm, residual_scale, eps, has_update = ctx.spec
-        dr, dn = grads if has_update else (None, grads[0])
+    @_once
+    def backward(ctx, dr, dn=None):
+        saved, need = ctx.saved_tensors, ctx.needs_input_grad
+        if saved[1] is None:
+            dr, dn = None, dr
         res = (None,) * 5
         if dr is not None or dn is not None:
-            res = _residual_norm_grad(_dense(dr), _dense(dn), r, update, gate, post_weight, pre_weight, post_norm,
-                                      residual_scale, eps, ctx.needs_input_grad[:5], None, None)
+            a, res = _lib.resnorm_backward(ctx.args, saved, need, _dense(dr), _dense(dn))
+            _on(saved[0].get_device(), None, _lib.resnorm_grad_call, a, saved[0])
         return (*res, None, None, None, None, None)
 
 
@@ -503,8 +531,8 @@ def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, acti
     reads. Differentiable in x and the weights unless buffers are given;
     save_gates=False keeps no products for it and computes them again."""
     if _differentiable("gated_mlp", (x, w_gate, w_up), out, gates_out):
-        return _GatedMlp.apply(x, w_gate, w_up, activation, bool(save_gates), workspace, stream)
-    return _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream)
+        return _GatedMlp.apply(x, w_gate, w_up, activation, save_gates, workspace, stream)
+    return _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream)[0]
 
 
 def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, save=False):
@@ -517,27 +545,26 @@ def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, s
         a = _lib.gated(x, w_gate, w_up, h, gates, activation)
         ws = _lib.scratch(_lib.mu_gated_mlp_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_gated_mlp(a, ws, st)
-        return (h, gates) if save else h
+        return h, gates, a
     return _on(device, stream, call)
 
 
 class _GatedMlp(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w_gate, w_up, activation, save_gates, workspace, stream):
-        ctx.activation = activation
-        h, gates = _gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream, save=True) if save_gates else \
-            (_gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream), None)
+        h, gates, a = _gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream, save_gates)
+        ctx.args = _lib.MuGatedGrad(tokens=a.tokens, dim=a.dim, hidden=a.hidden, dtype=a.dtype, grad_dtype=a.dtype,
+                                    activation=a.activation)
         ctx.save_for_backward(x, w_gate, w_up, gates)
         return h
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, grad):
-        x, w_gate, w_up, gates = ctx.saved_tensors
-        need_x, need_gate, need_up = ctx.needs_input_grad[:3]
-        dx, d_gate, d_up = gated_mlp_grad(grad.contiguous(), x, w_gate, w_up, gates, activation=ctx.activation, need_x=need_x,
-                                          need_weights=need_gate or need_up)
-        return dx, d_gate if need_gate else None, d_up if need_up else None, None, None, None, None
+        saved = ctx.saved_tensors
+        a, res = _lib.gated_backward(ctx.args, saved, ctx.needs_input_grad, grad.contiguous())
+        _on(saved[0].get_device(), None, _lib.gated_grad_call, a, saved[0])
+        return (*res[:3], None, None, None, None)
 
 
 def gated_mlp_grad(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
