@@ -17,16 +17,16 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmuon_mi355x.so")
 SOURCES = ["capi.hip", "elementwise.hip", "ns_gemm.hip", "grads.hip", "embedding.hip", "qkmax.hip", "rotary.hip", "resnorm.hip",
-           "gated.hip"]
+           "gated.hip", "gated_wide.hip"]
 # The benchmark's ceiling probe (an MFMA loop with clock stamps), a library of
 # its own so that the optimizer library holds only the optimizer.
 PROBE_LIB = os.path.join(HERE, "libmuon_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 ARCH = "gfx950"
-# Per-source extra flags. The Newton-Schulz GEMMs keep 256 accumulator AGPRs
-# and two fragment buffers live; the register-minimising scheduler keeps the
+# Per-source extra flags. The Newton-Schulz GEMMs and the gated feed-forward's
+# wide tiles keep 256 accumulator AGPRs and two fragment buffers live; the register-minimising scheduler keeps the
 # accumulators in place (no spills, no copies in the K loop).
-EXTRA = {"ns_gemm.hip": ["-mllvm", "-amdgpu-sched-strategy=iterative-minreg"]}
+EXTRA = {name: ["-mllvm", "-amdgpu-sched-strategy=iterative-minreg"] for name in ("ns_gemm.hip", "gated_wide.hip")}
 
 
 def hipcc() -> str:

@@ -28,158 +28,17 @@
 #include "../../include/muon_mi355x.h"
 #include "capi_common.hpp"
 #include "common.hpp"
+#include "gated.hpp"
 #include "vec.hpp"
 
 using namespace mu;
 
+using namespace mu::gated;
+
 namespace {
 
-constexpr int NTHR = 256;
 constexpr int TILE = 128;   // tile edge
-#define LDSP __attribute__((address_space(3)))
-constexpr int BUF_RAW32 = 0x00020000;   // word 3 of a raw buffer resource
-constexpr int OUTSIDE = 0x7fffff00;     // an offset beyond every resource: reads zeros
 #define MU_WAIT_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
-
-enum Mode : int { FWD, RECOMP, DX, DW };
-
-// ---------------------------------------------------------------------------
-// Activations: act(g) and its derivative, float32
-// ---------------------------------------------------------------------------
-// 1 / (1 + e^-z); the exponential's overflow gives 0. FAST: the hardware's
-// exponential and reciprocal (each within 2^-22), where results become bfloat16.
-template <bool FAST>
-__device__ __forceinline__ float sigmoid(float z) {
-    if constexpr (FAST) return __builtin_amdgcn_rcpf(1.f + __expf(-z));
-    else return 1.f / (1.f + expf(-z));
-}
-template <bool FAST>
-__device__ __forceinline__ void act_of(int kind, float g, float& a, float& slope) {
-    switch (kind) {
-        case MU_ACT_SILU: {
-            const float s = sigmoid<FAST>(g);
-            a = g * s;
-            slope = s * (1.f + g * (1.f - s));
-            return;
-        }
-        case MU_ACT_GELU: {   // g Phi(g); slope Phi(g) + g phi(g)
-            const float c = 0.5f * erfcf(g * -0.70710678f);
-            a = g * c;
-            slope = c + g * 0.39894228f * (FAST ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
-            return;
-        }
-        case MU_ACT_GELU_TANH: {   // g (1 + tanh z) / 2 = g sigmoid(2 z)
-            const float k = 0.79788456f, q = 0.044715f;
-            const float s = sigmoid<FAST>(2.f * k * (g + q * g * g * g));
-            a = g * s;
-            slope = s + g * s * (1.f - s) * (2.f * k * (1.f + 3.f * q * g * g));
-            return;
-        }
-        default:
-            a = fmaxf(g, 0.f);
-            slope = g > 0.f ? 1.f : 0.f;
-            if (g != g) a = g;
-    }
-}
-
-// ---------------------------------------------------------------------------
-// The tiled product
-// ---------------------------------------------------------------------------
-struct TileArgs {
-    const void* a[2];
-    const void* b[2];
-    int64_t lda, ldb;          // row pitches in elements
-    int64_t m, n, k;           // rows, columns (FWD: of h), and k (DX: of each half)
-    int tiles_m, tiles_n;
-    int kt_split;              // k slices of a split (blockIdx.y)
-    int act;
-    void* out[2];              // FWD: h; RECOMP: dg, du; DX: dx; DW: dWg, dWu
-    int64_t ldo;
-    void* gates[2];            // FWD: g and u, or null
-    const void* dh;            // RECOMP
-    float* part;               // split: [splits][2 (DW)][m][n] float32 sums
-    bool out_f32;              // DW: float32 results
-    bool accumulate;           // DW
-};
-
-template <typename T> constexpr int bk() { return 128 / (int)sizeof(T); }
-
-template <typename T> struct Mma;
-template <> struct Mma<bf16> {
-    typedef bf16x8 Frag;   // k 8 (l >> 4) .. of row l & 15; two of them cover a slice
-};
-template <> struct Mma<float> {
-    typedef f32x4 Frag;    // k 4 (l >> 4) .. of row l & 15: one of each goes to each of four instructions
-};
-
-__device__ __forceinline__ f32x4 mma(const bf16x8& a, const bf16x8& b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mma(const f32x4& a, const f32x4& b, f32x4 c) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[i], b[i], c, 0, 0, 0);
-    return c;
-}
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)min(max(bytes, (int64_t)0), (int64_t)OUTSIDE), BUF_RAW32);
-}
-
-// Swizzle of the 16-byte chunks of LDS row k of an operand with k down its rows:
-// the four rows (of both types' reads) that one access touches, and for bfloat16
-// those of the neighbouring lane group, fall into different banks.
-template <typename T>
-__device__ __forceinline__ int swz_down(int k) {
-    return sizeof(T) == 2 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 4 * ((k >> 2) & 3);
-}
-
-template <typename T, int TS, bool DOWN>
-struct Operand {
-    static constexpr int ES = sizeof(T), NI = TS / 32;        // direct loads of a wave and slice
-    static constexpr int ROWB = DOWN ? TS * ES : 128;         // bytes of an LDS row
-    static constexpr int RPB = 1024 / ROWB, LPR = 64 / RPB;   // LDS rows of a load, lanes of a row
-
-    // Load instruction i: LDS row and global 16-byte chunk of this lane.
-    __device__ static __forceinline__ int lds_row(int i, int wave, int lane) { return (i * 4 + wave) * RPB + lane / LPR; }
-    __device__ static __forceinline__ int chunk(int row, int lane) {
-        const int p = lane % LPR;
-        return DOWN ? p ^ swz_down<T>(row) : p ^ (row & 7);
-    }
-    // Fragment `f` (16 rows or columns from base) of part kk of a slice.
-    __device__ static __forceinline__ typename Mma<T>::Frag read(const char* lds, int base, int f, int kk, int lane) {
-        if constexpr (!DOWN) {
-            const int row = base + f * 16 + (lane & 15), c = (kk * 4 + (lane >> 4)) ^ (row & 7);
-            return *(const typename Mma<T>::Frag*)(lds + row * 128 + c * 16);
-        } else if constexpr (ES == 2) {
-            // lane i of each 16-lane group addresses 4 elements of row i / 4 and
-            // receives column i of those four rows (see ds_read_b64_tr_b16)
-            const int i = lane & 15, r = kk * 32 + 8 * (lane >> 4) + (i >> 2);
-            const int c = (((base + f * 16) >> 3) + ((i >> 1) & 1)) ^ swz_down<T>(r);
-            const char* p = lds + r * ROWB + c * 16 + 8 * (i & 1);
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)p);
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)(p + 4 * ROWB));
-            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            f32x4 v;
-            const int col = base + f * 16 + (lane & 15);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = kk * 16 + 4 * (lane >> 4) + i, c = (col >> 2) ^ swz_down<T>(r);
-                v[i] = *(const float*)(lds + r * ROWB + c * 16 + (col & 3) * 4);
-            }
-            return v;
-        }
-    }
-};
-
-// Tiles in groups of eight rows, column by column inside a group: workgroups that
-// run together share eight strips of one operand and a few of the other.
-__device__ __forceinline__ void tile_of(int t, int tm, int tn, int& ti, int& tj) {
-    constexpr int G = 8;
-    const int per = G * tn, g = t / per, w = t - g * per, gm = min(G, tm - g * G);
-    ti = g * G + w % gm;
-    tj = w / gm;
-}
 
 template <typename T, int MODE, int TS>
 __global__ __launch_bounds__(NTHR, TS == 256 ? 1 : 2) void k_tile(TileArgs A) {
@@ -509,6 +368,19 @@ int pack(int kernel, const Source& s, char* ws, hipStream_t st) {
 
 template <typename T, int MODE>
 int product(int kernel, TileArgs a, int splits, double flops, double bytes, hipStream_t s) {
+    if (sizeof(T) == 2 && splits == 1) {
+        const int64_t tm = ceil_div(a.m, 256) * (MODE == DW ? 2 : 1), tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? 128 : 256);
+        if (tm * tn >= 224 && tm * tn <= (1 << 23)) {
+            a.tiles_m = (int)tm;
+            a.tiles_n = (int)tn;
+            a.aligned = a.n % 8 == 0 && a.ldo % 8 == 0;
+            for (const void* p : {(const void*)a.out[0], (const void*)a.out[1], (const void*)a.gates[0], (const void*)a.gates[1]})
+                a.aligned = a.aligned && aligned(p, 16);
+            return timed_launch(kernel, flops, bytes, s, [&] {
+                return launch_wide(MODE, a, (int)std::min<int64_t>(256, round_up(tm * tn, 8)), s);
+            }, "gated feed-forward product launch");
+        }
+    }
     const int64_t tm = ceil_div(a.m, TILE) * (MODE == DW ? 2 : 1), tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? TILE / 2 : TILE);
     if (tm * tn > (1 << 23)) return fail(MU_ERR_INVALID_ARG, "too many tiles for one launch");
     a.tiles_m = (int)tm;
