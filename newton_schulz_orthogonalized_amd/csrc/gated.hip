@@ -37,19 +37,42 @@ using namespace mu::gated;
 
 namespace {
 
-constexpr int TILE = 128;   // tile edge
-#define MU_WAIT_VMCNT(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
+// s_waitcnt with vmcnt and lgkmcnt(0) (gfx9 encoding: vmcnt[3:0] bits 3:0, [5:4] bits 15:14)
+#define MU_WAIT_VMCNT_LGKM0(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (((n) >> 4) << 14))
 
-template <typename T, int MODE, int TS>
-__global__ __launch_bounds__(NTHR, TS == 256 ? 1 : 2) void k_tile(TileArgs A) {
+// A workgroup of four waves (two by two) for a tile, its slices through a ring of NS LDS
+// slots that are loaded NS - 1 ahead, one barrier a slice. Slots are arrays of their own,
+// so that the compiler's waits can tell a load into one from reads of another.
+template <typename T, int MODE, int TS, int NS>
+__global__ __launch_bounds__(NTHR, 1) void k_tile(TileArgs A) {
     constexpr bool DUAL = MODE == FWD || MODE == RECOMP;
     constexpr int ES = sizeof(T), BK = bk<T>(), WT = TS / 2, F = WT / 16, TN = DUAL ? TS / 2 : TS;
     typedef Operand<T, TS, MODE == DW> OA;
     typedef Operand<T, TS, MODE == DX || MODE == DW> OB;
-    __shared__ __attribute__((aligned(1024))) char sA0[TS * 128];
-    __shared__ __attribute__((aligned(1024))) char sA1[TS * 128];
-    __shared__ __attribute__((aligned(1024))) char sB0[TS * 128];
-    __shared__ __attribute__((aligned(1024))) char sB1[TS * 128];
+    static_assert(NS == 2 || NS == 4, "ring of two or four");
+    constexpr int SLOT = TS * 128, SPARE = NS == 4 ? SLOT : 16;
+    __shared__ __attribute__((aligned(1024))) char sA0[SLOT];
+    __shared__ __attribute__((aligned(1024))) char sA1[SLOT];
+    __shared__ __attribute__((aligned(1024))) char sA2[SPARE];
+    __shared__ __attribute__((aligned(1024))) char sA3[SPARE];
+    __shared__ __attribute__((aligned(1024))) char sB0[SLOT];
+    __shared__ __attribute__((aligned(1024))) char sB1[SLOT];
+    __shared__ __attribute__((aligned(1024))) char sB2[SPARE];
+    __shared__ __attribute__((aligned(1024))) char sB3[SPARE];
+    auto slot_a = [&](auto st) -> char* {
+        constexpr int S = decltype(st)::value;
+        if constexpr (S == 0) return sA0;
+        else if constexpr (S == 1) return sA1;
+        else if constexpr (S == 2) return sA2;
+        else return sA3;
+    };
+    auto slot_b = [&](auto st) -> char* {
+        constexpr int S = decltype(st)::value;
+        if constexpr (S == 0) return sB0;
+        else if constexpr (S == 1) return sB1;
+        else if constexpr (S == 2) return sB2;
+        else return sB3;
+    };
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int total = A.tiles_m * A.tiles_n;
@@ -66,40 +89,60 @@ __global__ __launch_bounds__(NTHR, TS == 256 ? 1 : 2) void k_tile(TileArgs A) {
     const int kth = (int)((A.k + BK - 1) / BK), kts = MODE == DX ? 2 * kth : kth;
     const int kt0 = blockIdx.y * A.kt_split, kt1 = min(kts, kt0 + A.kt_split);
 
-    // Direct loads of slice kt into a slot.
-    auto dma = [&](char* sa, char* sb, int kt) {
-        const int seg = MODE == DX && kt >= kth ? 1 : 0;
-        const int64_t k0 = (int64_t)(kt - seg * kth) * BK;
-        {
-            const char* base = (const char*)A.a[MODE == DX ? seg : which];
-            __amdgpu_buffer_rsrc_t ra;
-            if (MODE == DW) ra = resource(base + (k0 * A.lda + m0) * ES, ((A.k - k0) * A.lda - m0) * ES);
-            else ra = resource(base + (m0 * A.lda + k0) * ES, ((A.m - m0) * A.lda - k0) * ES);
+    // Where the tile's operands begin (DX: in dg and Wg, du and Wu; DUAL: in both weights),
+    // the bytes of its rows (k along the rows) or what of a row lies before it (down the
+    // rows), the bytes from slice to slice, and this lane's offsets in a slice. (A tile's
+    // rows of at most 2^20 elements are within 2^30 bytes, so extents are 32 bits.)
+    constexpr bool DOWN_A = MODE == DW, DOWN_B = MODE == DX || MODE == DW;
+    const int64_t oa = DOWN_A ? m0 : m0 * A.lda, ob = DOWN_B ? n0 : n0 * A.ldb;
+    const char* pa0 = (const char*)A.a[MODE == DW ? which : 0] + oa * ES;
+    const char* pa1 = MODE == DX ? (const char*)A.a[1] + oa * ES : pa0;
+    const char* pb0 = (const char*)A.b[0] + ob * ES;
+    const char* pb1 = MODE == DX || DUAL ? (const char*)A.b[1] + ob * ES : pb0;
+    const int a_bytes = DOWN_A ? (int)m0 * ES : (int)min(A.m - m0, (int64_t)TS) * (int)A.lda * ES;
+    const int b_bytes = DOWN_B ? (int)n0 * ES : (int)min(A.n - n0, (int64_t)TN) * (int)A.ldb * ES;
+    const int row_a = (int)A.lda * ES, row_b = (int)A.ldb * ES;
+    int voA[OA::NI], voB[OB::NI];
 #pragma unroll
-            for (int i = 0; i < OA::NI; ++i) {
-                const int row = OA::lds_row(i, wave, lane), c = OA::chunk(row, lane);
-                int off = row * (int)A.lda * ES + c * 16;
-                if (MODE != DW && k0 + c * (16 / ES) >= A.k) off = OUTSIDE;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDSP void*)(sa + (i * 4 + wave) * 1024), 16, off, 0, 0, 0);
-            }
+    for (int i = 0; i < OA::NI; ++i) {
+        const int r = OA::lds_row(i, wave, lane);
+        voA[i] = r * row_a + OA::chunk(r, lane) * 16;
+    }
+#pragma unroll
+    for (int i = 0; i < OB::NI; ++i) {
+        const int r = OB::lds_row(i, wave, lane);
+        // DUAL: LDS rows are, for each half of the columns, those of the gate and of the up projection
+        voB[i] = (DUAL ? r / WT * (WT / 2) + r % (WT / 2) : r) * row_b + OB::chunk(r, lane) * 16;
+    }
+    const int chunk_k = (16 / ES) * ((lane & 7) ^ (lane >> 3));   // first k of this lane's chunk (k along the rows)
+    // Direct loads of slice kt into a slot; behind the last slice nothing is read.
+    auto dma = [&](auto st, int kt) {
+        char *sa = slot_a(st), *sb = slot_b(st);
+        const bool second = MODE == DX && kt >= kth;
+        const int ks = second ? kt - kth : kt, left = (int)A.k - ks * BK;
+        auto extent = [&](bool down, int row, int bytes) {
+            return kt >= kt1 ? 0 : down ? min(left, BK) * row - bytes : bytes - ks * 128;
+        };
+        const int step_a = DOWN_A ? BK * row_a : 128, step_b = DOWN_B ? BK * row_b : 128;
+        const int nb = extent(DOWN_B, row_b, b_bytes);
+        __amdgpu_buffer_rsrc_t ra, rb, rb2;
+        ra = resource((second ? pa1 : pa0) + (int64_t)ks * step_a, extent(DOWN_A, row_a, a_bytes));
+        rb = resource((second ? pb1 : pb0) + (int64_t)ks * step_b, nb);
+        rb2 = resource(pb1 + (int64_t)ks * step_b, nb);
+#pragma unroll
+        for (int i = 0; i < OA::NI; ++i) {
+            const int off = DOWN_A || chunk_k < left ? voA[i] : OUTSIDE;
+            char* dst = sa + (i * 4 + wave) * 1024;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LDSP void*)dst, 16, off, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < OB::NI; ++i) {
-            const int row = OB::lds_row(i, wave, lane), c = OB::chunk(row, lane);
-            __amdgpu_buffer_rsrc_t rb;
-            int off;
-            if constexpr (DUAL) {
-                // LDS rows: for each half of the columns, those of the gate and of the up projection
-                const int r0 = i * 32 + wave * 8, half = r0 / WT, in = r0 % WT, part = in / (WT / 2);
-                const int64_t f0 = n0 + half * (WT / 2) + in % (WT / 2);
-                rb = resource((const char*)A.b[part] + (f0 * A.ldb + k0) * ES, ((A.n - f0) * A.ldb - k0) * ES);
-                off = (lane >> 3) * (int)A.ldb * ES + c * 16;
-                if (k0 + c * (16 / ES) >= A.k) off = OUTSIDE;
-            } else {
-                rb = resource((const char*)A.b[MODE == DX ? seg : 0] + (k0 * A.ldb + n0) * ES, ((A.k - k0) * A.ldb - n0) * ES);
-                off = row * (int)A.ldb * ES + c * 16;
-            }
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDSP void*)(sb + (i * 4 + wave) * 1024), 16, off, 0, 0, 0);
+            const int off = DOWN_B || chunk_k < left ? voB[i] : OUTSIDE;
+            char* dst = sb + (i * 4 + wave) * 1024;
+            if (DUAL && (i * 32 + wave * 8) % WT / (WT / 2) == 1)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb2, (LDSP void*)dst, 16, off, 0, 0, 0);
+            else
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LDSP void*)dst, 16, off, 0, 0, 0);
         }
     };
 
@@ -109,125 +152,154 @@ __global__ __launch_bounds__(NTHR, TS == 256 ? 1 : 2) void k_tile(TileArgs A) {
     for (int i = 0; i < F; ++i)
 #pragma unroll
         for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int oa_r[4], ob_r[4];
+    OA::offsets(oa_r, wm, lane);
+    OB::offsets(ob_r, wn, lane);
     // (the weights' side first: a lane then holds four consecutive columns of a row)
     auto compute = [&](const char* sa, const char* sb) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
             typename Mma<T>::Frag af[F], bf[F];
 #pragma unroll
-            for (int f = 0; f < F; ++f) bf[f] = OB::read(sb, wn, f, kk, lane);
+            for (int f = 0; f < F; ++f) bf[f] = OB::read(sb, ob_r, f, kk);
 #pragma unroll
-            for (int f = 0; f < F; ++f) af[f] = OA::read(sa, wm, f, kk, lane);
+            for (int f = 0; f < F; ++f) af[f] = OA::read(sa, oa_r, f, kk);
 #pragma unroll
             for (int i = 0; i < F; ++i)
 #pragma unroll
                 for (int j = 0; j < F; ++j) acc[i][j] = mma(bf[j], af[i], acc[i][j]);
         }
     };
-    if (kt0 < kt1) dma(sA0, sB0, kt0);
-    for (int kt = kt0; kt < kt1; kt += 2) {
-        MU_WAIT_VMCNT(0);
-        __syncthreads();
-        if (kt + 1 < kt1) dma(sA1, sB1, kt + 1);
-        compute(sA0, sB0);
-        if (kt + 1 >= kt1) break;
-        MU_WAIT_VMCNT(0);
-        __syncthreads();
-        if (kt + 2 < kt1) dma(sA0, sB0, kt + 2);
-        compute(sA1, sB1);
+    constexpr int LOADS = OA::NI + OB::NI;
+    static_for<0, NS - 1>([&](auto s) { dma(s, kt0 + decltype(s)::value); });
+    int kt = kt0;
+    for (; kt + NS <= kt1; kt += NS) {
+        static_for<0, NS>([&](auto s) {
+            constexpr int S = decltype(s)::value;
+            // this slice has landed and this wave's reads of the one before are done; a barrier
+            // without __syncthreads' fence, which would wait for the loads on their way
+            MU_WAIT_VMCNT_LGKM0((NS - 2) * LOADS);
+            __builtin_amdgcn_s_barrier();
+            dma(Stage<(S + NS - 1) % NS>{}, kt + S + NS - 1);
+            compute(slot_a(s), slot_b(s));
+        });
     }
+    // the last few, all on their way
+    MU_WAIT_VMCNT_LGKM0(0);
+    __builtin_amdgcn_s_barrier();
+    static_for<0, NS - 1>([&](auto s) {
+        if (kt + decltype(s)::value < kt1) compute(slot_a(s), slot_b(s));
+    });
 
-    // Lane l holds columns 16 j + 4 (l >> 4) .. +3 of row 16 i + (l & 15) of each fragment.
+    // Results through LDS (a wave its own WT x WT block; the ring is done with), so that
+    // they leave in runs of 8 columns of a row. Lane l holds columns 16 j + 4 (l >> 4) ..
+    // +3 of row 16 i + (l & 15) of each fragment; 16-byte chunk c of row r lies at c ^ (r & 7).
+    MU_WAIT_VMCNT_LGKM0(0);
+    __syncthreads();
+    float* st = (float*)(wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1);
+    static_assert(WT * WT * 4 <= SLOT, "a wave's block fits an array");
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j)
+            *(f32x4*)(st + (i * 16 + (lane & 15)) * WT + (((j * 4 + (lane >> 4)) ^ (lane & 7)) << 2)) = acc[i][j];
+    constexpr int CW = DUAL ? WT / 2 : WT, LPR = CW / 8, RPP = 64 / LPR;   // columns of a row, lanes of it, rows of a pass
     constexpr bool FAST = ES == 2;
+    const int c = 2 * (lane % LPR);
+    const int64_t col = n0 + (wave & 1) * CW + 4 * c;
+    const int cnt = (int)min((int64_t)8, A.n - col);
+#pragma clang loop unroll(disable)
+    for (int p = 0; p < (WT + RPP - 1) / RPP; ++p) {
+        const int r = p * RPP + lane / LPR;
+        const int64_t row = m0 + wm + r;
+        if (row >= A.m || cnt <= 0 || r >= WT) continue;
+        const float* q = st + r * WT;
+        auto run = [&](int chunk, float (&v)[8]) {
+            const f32x4 x = *(const f32x4*)(q + ((chunk ^ (r & 7)) << 2)), y = *(const f32x4*)(q + (((chunk + 1) ^ (r & 7)) << 2));
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int64_t row = m0 + wm + i * 16 + (lane & 15);
-        if (row >= A.m) continue;
+            for (int e = 0; e < 4; ++e) { v[e] = x[e]; v[e + 4] = y[e]; }
+        };
+        float v[8], w[8];
+        run(c, v);
         if constexpr (DUAL) {
-#pragma unroll
-            for (int j = 0; j < F / 2; ++j) {
-                const int64_t col = n0 + wn / 2 + j * 16 + 4 * (lane >> 4);
-                // (RECOMP also writes the zeros behind its padded rows, which DX reads)
-                const int cnt = (int)min((int64_t)4, A.n - col);
-                const int put = MODE == RECOMP ? (int)min((int64_t)4, A.ldo - col) : cnt;
-                if (put <= 0) continue;
-                const f32x4 g = acc[i][j], u = acc[i][j + F / 2];
-                float o0[4], o1[4];
-                if constexpr (MODE == FWD) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float a, s;
-                        act_of<FAST>(A.act, g[e], a, s);
-                        o0[e] = a * u[e];
-                    }
-                    for (int e = 0; e < cnt; ++e) ((MU_GLOBAL T*)A.out[0])[row * A.ldo + col + e] = from_f32<T>(o0[e]);
-                    if (A.gates[0])
-                        for (int e = 0; e < cnt; ++e) {
-                            ((MU_GLOBAL T*)A.gates[0])[row * A.ldo + col + e] = from_f32<T>(g[e]);
-                            ((MU_GLOBAL T*)A.gates[1])[row * A.ldo + col + e] = from_f32<T>(u[e]);
-                        }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = e < cnt ? to_f32<T>(((const MU_GLOBAL T*)A.dh)[row * A.n + col + e]) : 0.f;
-                        float a, s;
-                        act_of<FAST>(A.act, g[e], a, s);
-                        o0[e] = d * u[e] * s;
-                        o1[e] = d * a;
-                    }
-                    for (int e = 0; e < put; ++e) {
-                        ((MU_GLOBAL T*)A.out[0])[row * A.ldo + col + e] = from_f32<T>(o0[e]);
-                        ((MU_GLOBAL T*)A.out[1])[row * A.ldo + col + e] = from_f32<T>(o1[e]);
-                    }
+            run(CW / 4 + c, w);
+            const int64_t at = row * A.ldo + col;
+            float o[8], s[8];
+            if constexpr (MODE == FWD) {
+                if (A.gates[0]) {
+                    store_run<T, 8>((T*)A.gates[0] + at, cnt, v);
+                    store_run<T, 8>((T*)A.gates[1] + at, cnt, w);
                 }
+                act_run<FAST>(A.act, v, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= w[e];
+                store_run<T, 8>((T*)A.out[0] + at, cnt, o);
+            } else {   // also the zeros behind rows that are padded to 16 bytes, which DX reads
+                float d[8];
+                load_run<T, 8>((const T*)A.dh + row * A.n + col, cnt, d);
+                slope_run<FAST>(A.act, v, o, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    s[e] *= d[e] * w[e];
+                    o[e] *= d[e];
+                }
+                const int put = (int)min((int64_t)8, A.ldo - col);
+                store_run<T, 8>((T*)A.out[0] + at, put, s);
+                store_run<T, 8>((T*)A.out[1] + at, put, o);
             }
         } else {
+            const int64_t at = row * A.n + col;
+            if (MODE == DX && A.part) {
+                store_run<float, 8>(A.part + (int64_t)blockIdx.y * A.m * A.n + at, cnt, v);
+            } else if (MODE == DW && (A.out_f32 || ES == 4)) {
+                float* o = (float*)A.out[which] + at;
+                if (A.accumulate) {
+                    load_run<float, 8>(o, cnt, w);
 #pragma unroll
-            for (int j = 0; j < F; ++j) {
-                const int64_t col = n0 + wn + j * 16 + 4 * (lane >> 4);
-                const int cnt = (int)min((int64_t)4, A.n - col);
-                if (cnt <= 0) continue;
-                const int64_t at = row * A.n + col;
-                if (A.part) {
-                    float* p = A.part + ((int64_t)blockIdx.y * (MODE == DW ? 2 : 1) + which) * A.m * A.n + at;
-                    for (int e = 0; e < cnt; ++e) gp(p)[e] = acc[i][j][e];
-                } else if (MODE == DW && (A.out_f32 || ES == 4)) {
-                    MU_GLOBAL float* p = (MU_GLOBAL float*)A.out[which] + at;
-                    for (int e = 0; e < cnt; ++e) p[e] = acc[i][j][e] + (A.accumulate ? p[e] : 0.f);
-                } else {
-                    MU_GLOBAL T* p = (MU_GLOBAL T*)A.out[which] + at;
-                    for (int e = 0; e < cnt; ++e) p[e] = from_f32<T>(acc[i][j][e] + (A.accumulate ? to_f32<T>(p[e]) : 0.f));
+                    for (int e = 0; e < 8; ++e) v[e] += w[e];
                 }
+                store_run<float, 8>(o, cnt, v);
+            } else {
+                T* o = (T*)A.out[which] + at;
+                if (MODE == DW && A.accumulate) {
+                    load_run<T, 8>(o, cnt, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += w[e];
+                }
+                store_run<T, 8>(o, cnt, v);
             }
         }
     }
 }
 
-// Sums of the splits' results, in order.
+// Sums of the splits of the gradient of x, in order; also zeros of both weights' gradients
+// where there are no tokens.
 struct JoinArgs {
     const float* part;
     void* out[2];
     int64_t n;        // elements of a result
-    int splits, nout;
-    bool out_f32, accumulate;
+    int splits;       // 0: zeros
+    bool out_f32;
 };
 __global__ __launch_bounds__(NTHR) void k_join(JoinArgs A) {
-    const int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x;
-    if (i >= A.n * A.nout) return;
-    const int which = i >= A.n;
-    const int64_t at = i - which * A.n;
-    float s = 0.f;
-    for (int k = 0; k < A.splits; ++k) s += gp(A.part)[(int64_t)k * A.nout * A.n + i];
-    if (A.out_f32) {
-        MU_GLOBAL float* o = (MU_GLOBAL float*)A.out[which] + at;
-        *o = A.accumulate ? *o + s : s;
-    } else {
-        MU_GLOBAL bf16* o = (MU_GLOBAL bf16*)A.out[which] + at;
-        *o = (bf16)(A.accumulate ? (float)*o + s : s);
+    const int64_t i = ((int64_t)blockIdx.x * NTHR + threadIdx.x) * 8;   // of one result (blockIdx.y)
+    const int cnt = (int)min((int64_t)8, A.n - i);
+    if (cnt <= 0) return;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[8];
+    for (int k = 0; k < A.splits; ++k) {
+        load_run<float, 8>(A.part + k * A.n + i, cnt, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
     }
+    void* out = blockIdx.y ? A.out[1] : A.out[0];
+    if (A.out_f32) store_run<float, 8>((float*)out + i, cnt, s);
+    else store_run<bf16, 8>((bf16*)out + i, cnt, s);
 }
 
 // dg and du from the saved g and u: rows of `n`, into rows of `pitch`, zeros behind.
+// Columns lie along blockIdx.x and rows along blockIdx.y (a division for each run took as
+// long as moving it; four rows a thread 238 us, one 204, for 8192 x 14336 bfloat16). HBM
+// bound: five elements moved for each, 5.8 TB/s there.
 struct SlopeArgs {
     const void *dh, *g, *u;
     void *dg, *du;
@@ -237,41 +309,46 @@ struct SlopeArgs {
 template <typename T>
 __global__ __launch_bounds__(NTHR) void k_slopes(SlopeArgs A) {
     constexpr int V = vec_of<T>();
-    const int64_t runs = A.pitch / V, total = A.rows * runs;
-    for (int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x; i < total; i += (int64_t)gridDim.x * NTHR) {
-        const int64_t row = i / runs, c = (i - row * runs) * V, at = row * A.n + c;
-        const int cnt = (int)min((int64_t)V, A.n - c);
-        float d[V], g[V], u[V];
+    const int64_t c = ((int64_t)blockIdx.x * NTHR + threadIdx.x) * V;
+    const int cnt = (int)min((int64_t)V, A.n - c);
+    if (c >= A.pitch) return;
+    for (int64_t row = blockIdx.y; row < A.rows; row += gridDim.y) {
+        const int64_t at = row * A.n + c;
+        float d[V], g[V], u[V], a[V], s[V];
         load_run<T, V>((const T*)A.dh + at, cnt, d);
         load_run<T, V>((const T*)A.g + at, cnt, g);
         load_run<T, V>((const T*)A.u + at, cnt, u);
+        slope_run<sizeof(T) == 2>(A.act, g, a, s);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            float a, s;
-            act_of<sizeof(T) == 2>(A.act, g[e], a, s);
-            g[e] = e < cnt ? d[e] * u[e] * s : 0.f;
-            u[e] = e < cnt ? d[e] * a : 0.f;
+            s[e] = d[e] * u[e] * s[e];
+            a[e] = d[e] * a[e];
         }
-        store_run<T, V>((T*)A.dg + row * A.pitch + c, V, g);
-        store_run<T, V>((T*)A.du + row * A.pitch + c, V, u);
+        store_run<T, V>((T*)A.dg + row * A.pitch + c, V, s);
+        store_run<T, V>((T*)A.du + row * A.pitch + c, V, a);
     }
 }
 
-// Rows of n elements into rows of `pitch`, zeros behind them.
+// Rows of n elements into rows of `pitch`, zeros behind them, of up to three matrices.
 struct PackArgs {
-    const void* src;
-    void* dst;
-    int64_t rows, n, pitch;
+    const void* src[3];
+    void* dst[3];
+    int64_t rows[3];
+    int64_t n, pitch;
 };
 template <typename T>
 __global__ __launch_bounds__(NTHR) void k_pack(PackArgs A) {
     constexpr int V = vec_of<T>();
-    const int64_t runs = A.pitch / V, total = A.rows * runs;
-    for (int64_t i = (int64_t)blockIdx.x * NTHR + threadIdx.x; i < total; i += (int64_t)gridDim.x * NTHR) {
-        const int64_t row = i / runs, c = (i - row * runs) * V;
+    const int64_t c = ((int64_t)blockIdx.x * NTHR + threadIdx.x) * V;
+    if (c >= A.pitch) return;
+    const int m = blockIdx.z;
+    const T* src = (const T*)(m == 0 ? A.src[0] : m == 1 ? A.src[1] : A.src[2]);
+    T* dst = (T*)(m == 0 ? A.dst[0] : m == 1 ? A.dst[1] : A.dst[2]);
+    const int64_t rows = m == 0 ? A.rows[0] : m == 1 ? A.rows[1] : A.rows[2];
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         float v[V];
-        load_run<T, V>((const T*)A.src + row * A.n + c, (int)min((int64_t)V, A.n - c), v);
-        store_run<T, V>((T*)A.dst + row * A.pitch + c, V, v);
+        load_run<T, V>(src + row * A.n + c, (int)min((int64_t)V, A.n - c), v);
+        store_run<T, V>(dst + row * A.pitch + c, V, v);
     }
 }
 
@@ -290,11 +367,16 @@ struct Source {
     size_t off;
 };
 
+// How a product is cut: the tile's edge, and the slices of k of a workgroup.
+struct Cut {
+    int edge, kt, splits;
+};
+
 struct Plan {
     Source x, wg, wu;
     size_t off_dg, off_du, off_part, bytes;
     int64_t pitch_h;                    // of dg and du
-    int kt_dx, splits_dx, kt_dw, splits_dw;
+    Cut fwd, dx, dw;
 };
 
 Source source(const void* p, int64_t rows, int64_t n, int es, Plan& pl) {
@@ -308,12 +390,32 @@ Source source(const void* p, int64_t rows, int64_t n, int es, Plan& pl) {
     return s;
 }
 
-// Splits of k where the tiles alone leave most of the chip idle.
-void split_k(int64_t tiles, int64_t kts, int& kt, int& splits) {
-    splits = 1;
-    if (tiles < 256) splits = (int)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, kts / 8, 16}));
-    kt = (int)ceil_div(kts, splits);
-    splits = (int)std::max<int64_t>(1, ceil_div(kts, kt));
+// Tiles of 256 (bfloat16) where they fill half the chip: they then run at twice the rate
+// of the others. Else 128 where those give every compute unit one, and 64. Measured on
+// kernels of 768 x 2048 (bfloat16, us, edge 64 against 128): forward of 1000 tokens
+// 15.4, 13.8 (256 tiles of 128), of 256 tokens 6.3, 11.1 (64); both weights' gradients
+// 15, 17 (192) and 4.4, 4.8 (192); 64 tokens of 4096 x 14336 131, 121 (7168).
+//
+// Only the gradient of x is split over k (2 * hidden): its tiles are few and their k long,
+// where the weights' gradients are large and few k deep (splitting those in two cost 1000
+// tokens 10 us, 512 tokens of 2048 x 8192 105). As many splits as fill the chip twice (two
+// workgroups of 64 a compute unit), at least eight slices each: 256 tokens of 768 x 2048,
+// 48 tiles, 1, 2, 4 splits 21.9, 18.1, 16.6 us, float32 78, 47, 31; 64 tokens of 4096 x
+// 14336, 64 tiles, 103, 60, 38.5; 1000 tokens of 768, float32, 192 tiles, 82, 78, 66.
+Cut cut_of(int64_t m, int64_t n, int nmat, bool dual, int64_t kts, int dtype, bool split) {
+    auto tiles = [&](int e) { return nmat * ceil_div(m, e) * ceil_div(n, dual ? e / 2 : e); };
+    Cut c{128, (int)kts, 1};
+    if (dtype == MU_BF16 && tiles(256) >= 128) c.edge = 256;
+    else if (tiles(128) < 256) c.edge = 64;
+    if (split && dtype == MU_BF16 && c.edge == 64 && tiles(128) >= 96 && kts >= 32) {
+        c.edge = 128;   // 2048 tokens of 1000 x 2500: two splits of 128 51 us, tiles of 64 60
+        c.splits = 2;
+    } else if (split && c.edge == 64 && tiles(64) < 384) {
+        c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(512, tiles(64)), kts / 8, 16}));
+    }
+    c.kt = (int)ceil_div(kts, c.splits);
+    c.splits = (int)ceil_div(kts, c.kt);
+    return c;
 }
 
 Plan plan_fwd(const mu_gated* a) {
@@ -322,6 +424,7 @@ Plan plan_fwd(const mu_gated* a) {
     p.x = source(a->x, a->tokens, a->dim, es, p);
     p.wg = source(a->w_gate, a->hidden, a->dim, es, p);
     p.wu = source(a->w_up, a->hidden, a->dim, es, p);
+    p.fwd = cut_of(a->tokens, a->hidden, 1, true, ceil_div(a->dim, 128 / es), a->dtype, false);
     return p;
 }
 
@@ -343,11 +446,11 @@ Plan plan_bwd(const mu_gated_grad* a) {
     p.off_du = p.bytes;
     p.bytes += align_up((size_t)(a->tokens * p.pitch_h) * es);
     const int64_t bk = 128 / es;
-    split_k(ceil_div(a->tokens, TILE) * ceil_div(a->dim, TILE), 2 * ceil_div(a->hidden, bk), p.kt_dx, p.splits_dx);
-    split_k(2 * ceil_div(a->hidden, TILE) * ceil_div(a->dim, TILE), ceil_div(a->tokens, bk), p.kt_dw, p.splits_dw);
+    p.fwd = cut_of(a->tokens, a->hidden, 1, true, ceil_div(a->dim, bk), a->dtype, false);
+    p.dx = cut_of(a->tokens, a->dim, 1, false, 2 * ceil_div(a->hidden, bk), a->dtype, true);
+    p.dw = cut_of(a->hidden, a->dim, 2, false, ceil_div(a->tokens, bk), a->dtype, false);
     size_t part = 0;
-    if (a->dx && p.splits_dx > 1) part = sizeof(float) * (size_t)(p.splits_dx * a->tokens * a->dim);
-    if (a->d_gate && p.splits_dw > 1) part = std::max(part, sizeof(float) * (size_t)(p.splits_dw * 2 * a->hidden * a->dim));
+    if (a->dx && p.dx.splits > 1) part = sizeof(float) * (size_t)(p.dx.splits * a->tokens * a->dim);
     p.off_part = p.bytes;
     p.bytes += align_up(part);
     return p;
@@ -355,58 +458,62 @@ Plan plan_bwd(const mu_gated_grad* a) {
 
 const void* at(const Source& s, const char* ws) { return s.copied ? ws + s.off : s.p; }
 
+// The padded copies of a call, one launch.
 template <typename T>
-int pack(int kernel, const Source& s, char* ws, hipStream_t st) {
-    if (!s.copied || s.rows == 0) return MU_OK;
+int pack(int kernel, const Plan& p, char* ws, hipStream_t st) {
+    PackArgs a{};
+    int n = 0;
+    int64_t rows = 0;
+    for (const Source* s : {&p.x, &p.wg, &p.wu}) {
+        if (!s->copied) continue;
+        a.src[n] = s->p;
+        a.dst[n] = ws + s->off;
+        a.rows[n++] = s->rows;
+        a.n = s->n;
+        a.pitch = s->pitch;
+        rows = std::max(rows, s->rows);
+    }
+    if (n == 0) return MU_OK;
     return timed_launch(kernel, 0.0, 0.0, st, [&] {
-        const int64_t wgs = ceil_div(s.rows * (s.pitch / vec_of<T>()), NTHR);
-        hipLaunchKernelGGL(k_pack<T>, dim3((unsigned)std::min<int64_t>(wgs, 1 << 16)), dim3(NTHR), 0, st,
-                           PackArgs{s.p, ws + s.off, s.rows, s.n, s.pitch});
+        const dim3 grid((unsigned)ceil_div(a.pitch, vec_of<T>() * NTHR), (unsigned)std::min<int64_t>(rows, 4096), (unsigned)n);
+        hipLaunchKernelGGL(k_pack<T>, grid, dim3(NTHR), 0, st, a);
         return hipGetLastError();
     }, "operand copy launch");
 }
 
 template <typename T, int MODE>
-int product(int kernel, TileArgs a, int splits, double flops, double bytes, hipStream_t s) {
-    if (sizeof(T) == 2 && splits == 1) {
-        const int64_t tm = ceil_div(a.m, 256) * (MODE == DW ? 2 : 1), tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? 128 : 256);
-        if (tm * tn >= 224 && tm * tn <= (1 << 23)) {
-            a.tiles_m = (int)tm;
-            a.tiles_n = (int)tn;
-            a.aligned = a.n % 8 == 0 && a.ldo % 8 == 0;
-            for (const void* p : {(const void*)a.out[0], (const void*)a.out[1], (const void*)a.gates[0], (const void*)a.gates[1]})
-                a.aligned = a.aligned && aligned(p, 16);
-            return timed_launch(kernel, flops, bytes, s, [&] {
-                return launch_wide(MODE, a, (int)std::min<int64_t>(256, round_up(tm * tn, 8)), s);
-            }, "gated feed-forward product launch");
-        }
-    }
-    const int64_t tm = ceil_div(a.m, TILE) * (MODE == DW ? 2 : 1), tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? TILE / 2 : TILE);
+int product(int kernel, TileArgs a, const Cut& c, double flops, double bytes, hipStream_t s) {
+    const int64_t tm = ceil_div(a.m, c.edge) * (MODE == DW ? 2 : 1);
+    const int64_t tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? c.edge / 2 : c.edge);
     if (tm * tn > (1 << 23)) return fail(MU_ERR_INVALID_ARG, "too many tiles for one launch");
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
+    a.kt_split = c.kt;
+    a.aligned = a.n % 8 == 0 && a.ldo % 8 == 0;
+    for (const void* p : {(const void*)a.out[0], (const void*)a.out[1], (const void*)a.gates[0], (const void*)a.gates[1]})
+        a.aligned = a.aligned && aligned(p, 16);
     return timed_launch(kernel, flops, bytes, s, [&] {
-        const dim3 grid((unsigned)round_up(tm * tn, 8), (unsigned)splits);
-        hipLaunchKernelGGL((k_tile<T, MODE, TILE>), grid, dim3(NTHR), 0, s, a);
+        if (c.edge == 256) return launch_wide(MODE, a, (int)std::min<int64_t>(256, round_up(tm * tn, 8)), s);
+        const dim3 grid((unsigned)round_up(tm * tn, 8), (unsigned)c.splits);
+        if (c.edge == 128) hipLaunchKernelGGL((k_tile<T, MODE, 128, sizeof(T) == 2 ? 4 : 2>), grid, dim3(NTHR), 0, s, a);
+        else hipLaunchKernelGGL((k_tile<T, MODE, 64, 4>), grid, dim3(NTHR), 0, s, a);
         return hipGetLastError();
     }, "gated feed-forward product launch");
 }
 
-int join(JoinArgs j, hipStream_t s) {
-    const int64_t wgs = ceil_div(j.n * j.nout, NTHR);
+int join(const JoinArgs& j, hipStream_t s) {
+    const int64_t wgs = ceil_div(j.n, 8 * NTHR);
     if (wgs > (1 << 24) - 1) return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
     return timed_launch(MU_K_GATED_GRAD, 0.0, 0.0, s, [&] {
-        hipLaunchKernelGGL(k_join, dim3((unsigned)wgs), dim3(NTHR), 0, s, j);
+        hipLaunchKernelGGL(k_join, dim3((unsigned)wgs, j.out[1] ? 2 : 1), dim3(NTHR), 0, s, j);
         return hipGetLastError();
     }, "gated feed-forward join launch");
 }
 
 template <typename T>
 int run_fwd(const mu_gated* a, const Plan& p, char* ws, hipStream_t s) {
-    for (const Source* q : {&p.x, &p.wg, &p.wu}) {
-        const int rc = pack<T>(MU_K_GATED, *q, ws, s);
-        if (rc) return rc;
-    }
+    const int rc = pack<T>(MU_K_GATED, p, ws, s);
+    if (rc) return rc;
     TileArgs t{};
     t.a[0] = at(p.x, ws);
     t.b[0] = at(p.wg, ws);
@@ -416,26 +523,22 @@ int run_fwd(const mu_gated* a, const Plan& p, char* ws, hipStream_t s) {
     t.m = a->tokens;
     t.n = a->hidden;
     t.k = a->dim;
-    t.kt_split = 1 << 30;
     t.act = a->activation;
     t.out[0] = a->h;
     t.ldo = a->hidden;
     t.gates[0] = a->gate_out;
     t.gates[1] = a->up_out;
     const double n = (double)a->tokens, d = (double)a->dim, f = (double)a->hidden;
-    return product<T, FWD>(MU_K_GATED, t, 1, 4.0 * n * d * f,
+    return product<T, FWD>(MU_K_GATED, t, p.fwd, 4.0 * n * d * f,
                            sizeof(T) * (n * d + 2 * d * f + (a->gate_out ? 3 : 1) * n * f), s);
 }
 
 template <typename T>
 int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
     const double n = (double)a->tokens, d = (double)a->dim, f = (double)a->hidden;
-    for (const Source* q : {&p.x, &p.wg, &p.wu}) {
-        const int rc = pack<T>(MU_K_GATED_GRAD, *q, ws, s);
-        if (rc) return rc;
-    }
+    int rc = pack<T>(MU_K_GATED_GRAD, p, ws, s);
+    if (rc) return rc;
     T *dg = (T*)(ws + p.off_dg), *du = (T*)(ws + p.off_du);
-    int rc = MU_OK;
     if (!a->gate) {
         TileArgs t{};
         t.a[0] = at(p.x, ws);
@@ -446,17 +549,17 @@ int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
         t.m = a->tokens;
         t.n = a->hidden;
         t.k = a->dim;
-        t.kt_split = 1 << 30;
         t.act = a->activation;
         t.dh = a->grad_h;
         t.out[0] = dg;
         t.out[1] = du;
         t.ldo = p.pitch_h;
-        rc = product<T, RECOMP>(MU_K_GATED_GRAD, t, 1, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 3 * n * f), s);
+        rc = product<T, RECOMP>(MU_K_GATED_GRAD, t, p.fwd, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 3 * n * f), s);
     } else {
         rc = timed_launch(MU_K_GATED_GRAD, 0.0, 5.0 * sizeof(T) * n * f, s, [&] {
-            const int64_t wgs = ceil_div(a->tokens * (p.pitch_h / vec_of<T>()), NTHR);
-            hipLaunchKernelGGL(k_slopes<T>, dim3((unsigned)std::min<int64_t>(wgs, 1 << 16)), dim3(NTHR), 0, s,
+            const dim3 grid((unsigned)ceil_div(p.pitch_h, vec_of<T>() * NTHR),
+                            (unsigned)std::min<int64_t>(a->tokens, 65535));
+            hipLaunchKernelGGL(k_slopes<T>, grid, dim3(NTHR), 0, s,
                                SlopeArgs{a->grad_h, a->gate, a->up, dg, du, a->tokens, a->hidden, p.pitch_h, a->activation});
             return hipGetLastError();
         }, "gated feed-forward slopes launch");
@@ -473,30 +576,25 @@ int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
         t.m = a->tokens;
         t.n = a->dim;
         t.k = a->hidden;
-        t.kt_split = p.kt_dx;
         t.out[0] = a->dx;
-        t.part = p.splits_dx > 1 ? (float*)(ws + p.off_part) : nullptr;
-        rc = product<T, DX>(MU_K_GATED_GRAD, t, p.splits_dx, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 2 * n * f), s);
-        if (!rc && t.part) rc = join(JoinArgs{t.part, {a->dx, nullptr}, a->tokens * a->dim, p.splits_dx, 1, sizeof(T) == 4, false}, s);
+        t.part = p.dx.splits > 1 ? (float*)(ws + p.off_part) : nullptr;
+        rc = product<T, DX>(MU_K_GATED_GRAD, t, p.dx, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 2 * n * f), s);
+        if (!rc && t.part) rc = join(JoinArgs{t.part, {a->dx, nullptr}, a->tokens * a->dim, p.dx.splits, sizeof(T) == 4}, s);
         if (rc) return rc;
     }
     if (a->d_gate) {
-        const bool f32 = a->grad_dtype == MU_F32;
         t.b[0] = at(p.x, ws);
         t.ldb = p.x.pitch;
         t.m = a->hidden;
         t.n = a->dim;
         t.k = a->tokens;
-        t.kt_split = p.kt_dw;
         t.out[0] = a->d_gate;
         t.out[1] = a->d_up;
-        t.out_f32 = f32;
+        t.out_f32 = a->grad_dtype == MU_F32;
         t.accumulate = a->accumulate;
-        t.part = p.splits_dw > 1 ? (float*)(ws + p.off_part) : nullptr;
-        rc = product<T, DW>(MU_K_GATED_GRAD, t, p.splits_dw, 4.0 * n * d * f,
+        t.part = nullptr;
+        rc = product<T, DW>(MU_K_GATED_GRAD, t, p.dw, 4.0 * n * d * f,
                             sizeof(T) * (n * d + 2 * n * f) + es_of(a->grad_dtype) * 2 * d * f, s);
-        if (!rc && t.part)
-            rc = join(JoinArgs{t.part, {a->d_gate, a->d_up}, a->hidden * a->dim, p.splits_dw, 2, f32, (bool)a->accumulate}, s);
     }
     return rc;
 }
@@ -615,7 +713,7 @@ int mu_gated_mlp_grad(const mu_gated_grad* a, void* ws, size_t ws_bytes, void* s
         hipStream_t s = (hipStream_t)stream;
         if (a->tokens == 0) {   // no rows: zero gradients
             if (!a->d_gate || a->accumulate) return MU_OK;
-            return join(JoinArgs{nullptr, {a->d_gate, a->d_up}, a->hidden * a->dim, 0, 2, a->grad_dtype == MU_F32, false}, s);
+            return join(JoinArgs{nullptr, {a->d_gate, a->d_up}, a->hidden * a->dim, 0, a->grad_dtype == MU_F32}, s);
         }
         const Plan p = plan_bwd(a);
         rc = check_workspace(ws, ws_bytes, p.bytes);

@@ -18,6 +18,19 @@ constexpr int OUTSIDE = 0x7fffff00;     // an offset beyond every resource: read
 
 enum Mode : int { FWD, RECOMP, DX, DW };
 
+template <int N>
+struct Stage {
+    static constexpr int value = N;
+};
+// fn(Stage<i>{}) for i = B .. E-1, every index a compile-time constant
+template <int B, int E, typename Fn>
+__device__ __forceinline__ void static_for(Fn&& fn) {
+    if constexpr (B < E) {
+        fn(Stage<B>{});
+        static_for<B + 1, E>(fn);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Activations: act(g) and its derivative, float32
 // ---------------------------------------------------------------------------
@@ -113,7 +126,7 @@ struct TileArgs {
     int64_t ldo;
     void* gates[2];            // FWD: g and u, or null
     const void* dh;            // RECOMP
-    float* part;               // split: [splits][2 (DW)][m][n] float32 sums
+    float* part;               // DX, split: [splits][m][n] float32 sums
     bool out_f32;              // DW: float32 results
     bool accumulate;           // DW
     bool aligned;              // the wide kernel: results' rows start at 16-byte steps
@@ -142,16 +155,18 @@ __device__ __forceinline__ f32x4 mma(const f32x4& a, const f32x4& b, f32x4 c) {
     return c;
 }
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, (int)min(max(bytes, (int64_t)0), (int64_t)OUTSIDE), BUF_RAW32);
+// A resource of `bytes` from p on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const char* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, BUF_RAW32);
 }
 
-// Swizzle of the 16-byte chunks of LDS row k of an operand with k down its rows:
-// the four rows (of both types' reads) that one access touches, and for bfloat16
-// those of the neighbouring lane group, fall into different banks.
+// Swizzle of the 16-byte chunks of LDS row k of an operand with k down its rows (of
+// `rowb` bytes): the four rows (of both types' reads) that one access touches, and for
+// bfloat16 those of the neighbouring lane group, fall into different banks.
 template <typename T>
-__device__ __forceinline__ int swz_down(int k) {
-    return sizeof(T) == 2 ? 2 * ((k & 3) | ((k >> 1) & 4)) : 4 * ((k >> 2) & 3);
+__device__ __forceinline__ int swz_down(int k, int rowb) {
+    if (sizeof(T) == 4) return 4 * ((k >> 2) & 3);
+    return rowb == 128 ? (k & 2) | ((k >> 1) & 4) : 2 * ((k & 3) | ((k >> 1) & 4));
 }
 
 template <typename T, int TS, bool DOWN>
@@ -164,30 +179,42 @@ struct Operand {
     __device__ static __forceinline__ int lds_row(int i, int wave, int lane) { return (i * 4 + wave) * RPB + lane / LPR; }
     __device__ static __forceinline__ int chunk(int row, int lane) {
         const int p = lane % LPR;
-        return DOWN ? p ^ swz_down<T>(row) : p ^ (row & 7);
+        return DOWN ? p ^ swz_down<T>(row, ROWB) : p ^ (row & 7);
     }
-    // Fragment `f` (16 rows or columns from base) of part kk of a slice.
-    __device__ static __forceinline__ typename Mma<T>::Frag read(const char* lds, int base, int f, int kk, int lane) {
+    // This lane's offsets in the reads of a slice's fragments from row or column `base` on:
+    // for each k half of rows, or for each 16 columns (DOWN). Opaque, so that each address is
+    // an array, one of these and a constant: the compiler's alias analysis follows an address
+    // over a few steps only, and where it loses it a read waits for every load on its way.
+    __device__ static __forceinline__ void offsets(int (&o)[4], int base, int lane) {
+        const int i = lane & 15, g = lane >> 4;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if constexpr (!DOWN) {
+                o[n] = (base + i) * 128 + ((((n & 1) * 4 + g) ^ (i & 7)) << 4);
+            } else if constexpr (ES == 2) {
+                // lane i of each 16-lane group addresses 4 elements of row i / 4 and
+                // receives column i of those four rows (see ds_read_b64_tr_b16)
+                const int r = 8 * g + (i >> 2);
+                o[n] = r * ROWB + ((((base + n * 16) >> 3) + ((i >> 1) & 1)) ^ swz_down<T>(r, ROWB)) * 16 + 8 * (i & 1);
+            } else {
+                const int col = base + n * 16 + i;
+                o[n] = 4 * g * ROWB + ((col >> 2) ^ swz_down<T>(4 * g, ROWB)) * 16 + (col & 3) * 4;
+            }
+            asm("" : "+v"(o[n]));
+        }
+    }
+    // Fragment f (16 rows or columns) of part kk of a slice.
+    __device__ static __forceinline__ typename Mma<T>::Frag read(const char* lds, const int (&o)[4], int f, int kk) {
         if constexpr (!DOWN) {
-            const int row = base + f * 16 + (lane & 15), c = (kk * 4 + (lane >> 4)) ^ (row & 7);
-            return *(const typename Mma<T>::Frag*)(lds + row * 128 + c * 16);
+            return *(const typename Mma<T>::Frag*)(lds + o[kk] + f * 2048);
         } else if constexpr (ES == 2) {
-            // lane i of each 16-lane group addresses 4 elements of row i / 4 and
-            // receives column i of those four rows (see ds_read_b64_tr_b16)
-            const int i = lane & 15, r = kk * 32 + 8 * (lane >> 4) + (i >> 2);
-            const int c = (((base + f * 16) >> 3) + ((i >> 1) & 1)) ^ swz_down<T>(r);
-            const char* p = lds + r * ROWB + c * 16 + 8 * (i & 1);
-            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)p);
-            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)(p + 4 * ROWB));
+            const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)(lds + o[f] + kk * 32 * ROWB));
+            const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDSP i16x4*)(lds + o[f] + (kk * 32 + 4) * ROWB));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             f32x4 v;
-            const int col = base + f * 16 + (lane & 15);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = kk * 16 + 4 * (lane >> 4) + i, c = (col >> 2) ^ swz_down<T>(r);
-                v[i] = *(const float*)(lds + r * ROWB + c * 16 + (col & 3) * 4);
-            }
+            for (int i = 0; i < 4; ++i) v[i] = *(const float*)(lds + o[f] + (kk * 16 + i) * ROWB);
             return v;
         }
     }

@@ -25,26 +25,12 @@
 //
 // A workgroup takes tile after tile (one fixed share each, those of an XCD next to
 // each other) and starts the loads of the next tile before it writes this one.
-#include <type_traits>
-
 #include "gated.hpp"
 
 namespace mu {
 namespace gated {
 
 namespace {
-
-template <int N>
-struct Stage {
-    static constexpr int value = N;
-};
-template <int B, int E, typename Fn>
-__device__ __forceinline__ void static_for(Fn&& fn) {
-    if constexpr (B < E) {
-        fn(Stage<B>{});
-        static_for<B + 1, E>(fn);
-    }
-}
 
 // s_waitcnt with vmcnt(0) and lgkmcnt(0)
 #define MU_WAIT_ALL() __builtin_amdgcn_s_waitcnt((7 << 4))
@@ -193,7 +179,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_wide(TileArgs A) {
         const bool second = MODE == DX && kt >= kth;
         const int ks = second ? kt - kth : kt, left = (int)A.k - ks * 64;
         const int n = down ? min(left, 64) * (step >> 6) - bytes : bytes - ks * 128;
-        fn(__builtin_amdgcn_make_buffer_rsrc((void*)((second ? p1 : p0) + (int64_t)ks * step), 0, kt < KT ? n : 0, BUF_RAW32), left);
+        fn(resource((second ? p1 : p0) + (int64_t)ks * step, kt < KT ? n : 0), left);
     };
     auto with_a = [&](int kt, auto&& fn) { with(DOWN_A, kt, pa0, pa1, step_a, a_bytes, fn); };
     auto with_b = [&](int kt, auto pc, auto&& fn) {
@@ -389,8 +375,7 @@ __global__ __launch_bounds__(NTHR, 1) void k_wide(TileArgs A) {
             // through a resource that ends with the result, at one offset a lane; else by address.
             auto rows_of = [&](void* p, int64_t ld, int es) {
                 const int rows = (int)max(min(A.m - row1, (int64_t)16), (int64_t)0);
-                return __builtin_amdgcn_make_buffer_rsrc((char*)p + (row1 * ld + col0) * es, 0,
-                                                         rows > 0 ? (rows * (int)ld - (int)col0) * es : 0, BUF_RAW32);
+                return resource((const char*)p + (row1 * ld + col0) * es, rows > 0 ? (rows * (int)ld - (int)col0) * es : 0);
             };
             auto put = [&](bf16* p, int64_t ld, int pass, int n, const float (&v)[8]) {
                 if (A.aligned) {

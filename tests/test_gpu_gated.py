@@ -93,32 +93,33 @@ def test_integers_are_exact(t, d, f, dtype):
             assert np.array_equal(to_np(c), _rounded(d_up + _rounded(d_up, wt), wt))
 
 
-# many tiles of 256: whole and ragged, even and odd numbers of slices of k, several tiles for a workgroup
-LARGE = [(4096, 192, 2048), (3900, 264, 2100), (4100, 64, 1999), (2050, 1000, 3500), (1030, 4096, 7000), (520, 2056, 14000)]
+# many tiles of each edge: whole and ragged, even and odd numbers of slices of k, several tiles for a workgroup
+LARGE = [(4096, 192, 2048), (3900, 264, 2100), (4100, 64, 1999), (2050, 1000, 3500), (1030, 4096, 7000), (520, 2056, 14000),
+         (1000, 768, 2048), (2050, 257, 1500), (90, 2048, 1000)]
 
 
-@pytest.mark.parametrize("wt", [BF, FP])
+@pytest.mark.parametrize("dtype,wt", [(BF, BF), (BF, FP), (FP, FP)])
 @pytest.mark.parametrize("t,d,f", LARGE)
-def test_integers_are_exact_over_many_tiles(t, d, f, wt):
-    """As above, in bfloat16, against float64 products on the GPU, every element."""
+def test_integers_are_exact_over_many_tiles(t, d, f, dtype, wt):
+    """As above, against float64 products on the GPU, every element."""
     import newton_schulz_orthogonalized_amd as nso
     keep = min(1.0, 10 / d)
-    x, wg, wu = _ints((t, d), 94050 + t, BF, 2), _ints((f, d), 94051 + d, BF, 2, keep), _ints((f, d), 94052 + f, BF, 2, keep)
-    dh = _ints((t, f), 94053, BF, 1, 0.2)
+    x, wg, wu = _ints((t, d), 94050 + t, dtype, 2), _ints((f, d), 94051 + d, dtype, 2, keep), _ints((f, d), 94052 + f, dtype, 2, keep)
+    dh = _ints((t, f), 94053, dtype, 1, 0.2)
     X, G, U, DH = (v.double() for v in (x, wg, wu, dh))
     g, u = X @ G.t(), X @ U.t()
     assert max(float((X.abs() @ W.abs().t()).max()) for W in (G, U)) <= 256
-    gates = torch.full((2, t, f), 7.0, dtype=BF, device="cuda")
+    gates = torch.full((2, t, f), 7.0, dtype=dtype, device="cuda")
     h = nso.gated_mlp(x, wg, wu, activation="relu", gates_out=gates)
     assert torch.equal(gates[0].double(), g) and torch.equal(gates[1].double(), u)
-    assert torch.equal(h, (g.clamp(min=0) * u).to(BF))
+    assert torch.equal(h, (g.clamp(min=0) * u).to(dtype))
     assert torch.equal(nso.gated_mlp(x, wg, wu, activation="relu"), h)
     dg, du = DH * u * (g > 0), DH * g.clamp(min=0)
     want = [dg @ G + du @ U, dg.t() @ X, du.t() @ X]
     assert max(float(v.abs().max()) for v in want) < 2 ** 24
     for saved in (gates, None):
         got = nso.gated_mlp_grad(dh, x, wg, wu, saved, activation="relu", dtype=wt)
-        assert torch.equal(got[0], want[0].to(BF))
+        assert torch.equal(got[0], want[0].to(dtype))
         assert torch.equal(got[1], want[1].to(wt)) and torch.equal(got[2], want[2].to(wt))
         nso.gated_mlp_grad(dh, x, wg, wu, saved, activation="relu", d_gate=got[1], d_up=got[2], accumulate=True, need_x=False)
         assert torch.equal(got[1], (want[1] + want[1].to(wt).double()).to(wt))
