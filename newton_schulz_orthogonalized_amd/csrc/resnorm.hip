@@ -43,11 +43,7 @@ template <int WPR> constexpr int threads() { return 64 * WPR * teams<WPR>(); }
 // sum's barrier.
 template <int WPR, int K>
 __device__ __forceinline__ void team_sums(float (&v)[K], float (*red)[K][16], int& turn) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off, 64);
-    }
+    wave_sums(v);
     if constexpr (WPR > 1) {
         float(*r)[16] = red[turn];
         turn ^= 1;
@@ -204,63 +200,90 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
 #pragma unroll
         for (int e = 0; e < V; ++e) apre[j][e] = apost[j][e] = agate[j][e] = 0.f;
 
+    // sixteen waves have half the registers: no weights and no next row are held
+    constexpr bool AHEAD = WPR < 16;
+    float wpre[NV][V], wpost[NV][V];
+    auto weights = [&](int j) {
+        const int c = (j * LANES + lane) * V, cnt = dim - c;
+        load_weight(P.pre_weight, wbf, c, cnt, wpre[j]);
+        load_weight(P.post_weight, wbf, c, cnt, wpost[j]);
+    };
+#pragma unroll
+    for (int j = 0; j < NV && AHEAD; ++j) weights(j);
     // cuts workgroups share a group; with one each, a workgroup takes every gridDim-th group
     const int64_t step = A.cuts > 1 ? A.groups : gridDim.x;
     for (int64_t group = A.cuts > 1 ? blockIdx.x / A.cuts : blockIdx.x; group < A.groups; group += step) {
         const int64_t lo = A.cuts > 1 ? (blockIdx.x % A.cuts) * A.chunk : 0;
         const int64_t hi = min(A.per_group, lo + A.chunk);
-        for (int64_t i0 = lo; i0 < hi; i0 += TEAMS) {
-            const int64_t i = i0 + team;
-            if (i >= hi) break;   // (TEAMS > 1 has no barrier in here)
-            const int64_t row = group * A.per_group + i;
-            float r[NV][V], y[NV][V], d[NV][V], n[NV][V];
+        // a row's loads are on their way while the row before it is summed
+        Run8<TR> nr[NV], nd[NV];
+        Run8<TY> ny[NV], nn[NV];
+        auto fetch = [&](int64_t row) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * LANES + lane) * V, cnt = dim - c;
-                load_run<TR, V>((const TR*)A.r + row * dim + c, cnt, r[j]);
-                if (P.update) load_run<TY, V>((const TY*)P.update + row * dim + c, cnt, y[j]);
-                else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y[j][e] = 0.f;
-                }
-                if (A.a.grad_residual) load_run<TR, V>((const TR*)A.a.grad_residual + row * dim + c, cnt, d[j]);
-                else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) d[j][e] = 0.f;
-                }
-                if (A.a.grad_normed) load_run<TY, V>((const TY*)A.a.grad_normed + row * dim + c, cnt, n[j]);
+                nr[j].load((const TR*)A.r + row * dim + c, cnt);
+                if (P.update) ny[j].load((const TY*)P.update + row * dim + c, cnt);
+                if (A.a.grad_residual) nd[j].load((const TR*)A.a.grad_residual + row * dim + c, cnt);
+                if (A.a.grad_normed) nn[j].load((const TY*)A.a.grad_normed + row * dim + c, cnt);
             }
+        };
+        if (AHEAD && lo + team < hi) fetch(group * A.per_group + lo + team);
+        for (int64_t i = lo + team; i < hi; i += TEAMS) {   // (TEAMS > 1 has no barrier in here)
+            const int64_t row = group * A.per_group + i;
+            if (!AHEAD) fetch(row);
+            Run8<TR> kr[NV], kd[NV];
+            Run8<TY> ky[NV], kn[NV];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) kr[j] = nr[j], kd[j] = nd[j], ky[j] = ny[j], kn[j] = nn[j];
+            if (AHEAD && i + TEAMS < hi) fetch(row + TEAMS);
             float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * LANES + lane) * V, cnt = dim - c;
-                float w[V];
-                if (A.a.grad_normed) load_weight(P.pre_weight, wbf, c, cnt, w);
+                const int cnt = dim - (j * LANES + lane) * V;
+                float r[V], y[V], n[V];
+                if (!AHEAD) weights(j);
+                if (A.a.grad_normed) {
+                    kr[j].widen(r);
+                    kn[j].widen(n);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    r[j][e] *= A.r_scale;
-                    if (A.a.grad_normed) {
-                        s[0] += r[j][e] * r[j][e];
-                        s[1] += e < cnt ? n[j][e] * w[e] * r[j][e] : 0.f;
+                    for (int e = 0; e < V; ++e) {
+                        r[e] *= A.r_scale;
+                        s[0] += r[e] * r[e];
+                        s[1] += e < cnt ? n[e] * wpre[j][e] * r[e] : 0.f;
                     }
-                    s[2] += y[j][e] * y[j][e];
+                }
+                if (P.post_norm) {
+                    ky[j].widen(y);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[2] += y[e] * y[e];
                 }
             }
             team_sums<WPR>(s, red3, turn3);
             const float f1 = P.post_norm ? 1.f / sqrtf(s[2] * A.inv_dim + P.eps) : 1.f;
             const float f2 = 1.f / sqrtf(s[0] * A.inv_dim + P.eps);
             const float c2 = f2 * (f2 * (f2 * (s[1] * A.inv_dim)));
-            float sv[1] = {0.f};
+            float d[NV][V], sv[1] = {0.f};
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * LANES + lane) * V, cnt = dim - c;
-                float w[V], g[V], o[V];
+                float y[V], g[V], o[V];
+                if (!AHEAD) weights(j);
+                kd[j].widen(d[j]);
+                if (!A.a.grad_residual) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) d[j][e] = 0.f;
+                }
                 if (A.a.grad_normed) {
-                    load_weight(P.pre_weight, wbf, c, cnt, w);
+                    float r[V], n[V];
+                    kr[j].widen(r);
+                    kn[j].widen(n);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        apre[j][e] += n[j][e] * r[j][e] * f2;
-                        d[j][e] += f2 * (n[j][e] * w[e]) - c2 * r[j][e];
+                        const float h = f2 * n[e];
+                        r[e] *= A.r_scale;
+                        apre[j][e] += h * r[e];
+                        d[j][e] += h * wpre[j][e] - c2 * r[e];
                     }
                 }
                 if (A.a.d_residual) {
@@ -268,16 +291,17 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
                     for (int e = 0; e < V; ++e) o[e] = d[j][e] * P.residual_scale;
                     store_run<TR, V>((TR*)A.a.d_residual + row * dim + c, cnt, o);
                 }
-                load_weight(P.post_weight, wbf, c, cnt, w);
+                if (!P.update) continue;
                 load_weight(P.gate, wbf, P.gate ? group * dim + c : 0, cnt, g);
+                ky[j].widen(y);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    const float h = y[j][e] * f1;          // y, normed
-                    agate[j][e] += d[j][e] * (h * w[e]);
+                    const float h = y[e] * f1;          // y, normed
+                    agate[j][e] += d[j][e] * (h * wpost[j][e]);
                     d[j][e] *= g[e];
                     apost[j][e] += d[j][e] * h;
-                    d[j][e] *= w[e];
-                    sv[0] += e < cnt ? d[j][e] * y[j][e] : 0.f;
+                    d[j][e] *= wpost[j][e];
+                    sv[0] += e < cnt ? d[j][e] * y[e] : 0.f;
                 }
             }
             if (!A.a.d_update) continue;
@@ -289,9 +313,10 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * LANES + lane) * V, cnt = dim - c;
-                float o[V];
+                float y[V], o[V];
+                ky[j].widen(y);
 #pragma unroll
-                for (int e = 0; e < V; ++e) o[e] = f1 * d[j][e] - c1 * y[j][e];
+                for (int e = 0; e < V; ++e) o[e] = f1 * d[j][e] - c1 * y[e];
                 store_run<TY, V>((TY*)A.a.d_update + row * dim + c, cnt, o);
             }
         }
@@ -324,8 +349,18 @@ __global__ __launch_bounds__(64 * COL_WAVES) void k_colsum(ColArgs A) {
     const int64_t n = A.rows[kind], per = (n + COL_WAVES - 1) / COL_WAVES, group = kind == 2 ? y - 2 : 0;
     const MU_GLOBAL float* p = gp(A.part[kind]) + group * n * A.dim + c;
     float s = 0.f;
-    if (c < A.dim)
-        for (int64_t i = wave * per; i < min(n, (wave + 1) * per); ++i) s += p[i * A.dim];
+    if (c < A.dim) {
+        int64_t i = wave * per;
+        const int64_t end = min(n, i + per);
+        for (; i + 8 <= end; i += 8) {   // eight on their way at a time
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p[(i + k) * A.dim];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+        for (; i < end; ++i) s += p[i * A.dim];
+    }
     part[wave][lane] = s;
     __syncthreads();
     if (wave != 0 || c >= A.dim) return;
@@ -366,16 +401,21 @@ int check_common(const mu_resnorm* a) {
     return MU_OK;
 }
 
-// WPR and NV of a row: forward, and the gradient (whose rows are four runs and three sums).
+// Waves of a row and runs of a lane: forward, and the gradient, whose rows are four runs,
+// the next row's four and three sums (two runs a lane fill the registers of eight waves;
+// sixteen waves have half as many: past 8192 it keeps no row ahead and spills all the same).
 template <template <typename, typename, int, int> class L, typename TR, typename TY, bool GRAD, typename... X>
 hipError_t by_dim(int64_t dim, X&&... x) {
     if (dim <= 512) return L<TR, TY, 1, 1>::go(x...);
-    if constexpr (!GRAD) {
-        if (dim <= 1024) return L<TR, TY, 1, 2>::go(x...);
-    }
+    if (dim <= 1024) return L<TR, TY, 1, 2>::go(x...);
     if (dim <= 2048) return L<TR, TY, 4, 1>::go(x...);
-    if (dim <= 4096) return L<TR, TY, 4, 2>::go(x...);
-    if (dim <= 8192) return L<TR, TY, 16, 1>::go(x...);
+    if constexpr (GRAD) {
+        if (dim <= 4096) return L<TR, TY, 8, 1>::go(x...);
+        if (dim <= 8192) return L<TR, TY, 8, 2>::go(x...);
+    } else {
+        if (dim <= 4096) return L<TR, TY, 4, 2>::go(x...);
+        if (dim <= 8192) return L<TR, TY, 16, 1>::go(x...);
+    }
     return L<TR, TY, 16, 2>::go(x...);
 }
 template <template <typename, typename, int, int> class L, bool GRAD, typename... X>
@@ -408,15 +448,14 @@ struct GradPlan {
     bool part_gate;
     size_t off_pre, off_post, off_gate, bytes;
 };
-constexpr int TARGET_WGS = 512;   // two workgroups of four waves a compute unit
+constexpr int TARGET_WGS = 512;   // two workgroups of four waves a compute unit, one of eight
 constexpr int MIN_ROWS = 4;       // rows of a workgroup at least: its partial sums are three rows
 
 GradPlan plan_of(const mu_resnorm_grad* a) {
     const mu_resnorm& f = a->fwd;
     GradPlan p{};
-    const int64_t per_group = f.rows / f.groups, target = f.dim > 4096 ? TARGET_WGS / 2 : TARGET_WGS;
-    const int64_t rows_least = f.dim <= 512 ? 4 * MIN_ROWS : MIN_ROWS;
-    p.cuts = std::max<int64_t>(1, std::min(target / f.groups, (per_group + rows_least - 1) / rows_least));
+    const int64_t per_group = f.rows / f.groups, target = f.dim > 2048 ? TARGET_WGS / 2 : TARGET_WGS;
+    p.cuts = std::max<int64_t>(1, std::min(target / f.groups, (per_group + MIN_ROWS - 1) / MIN_ROWS));
     p.chunk = per_group > 0 ? (per_group + p.cuts - 1) / p.cuts : 1;
     if (per_group > 0) p.cuts = (per_group + p.chunk - 1) / p.chunk;
     p.grid = f.rows == 0 ? 0 : p.cuts > 1 ? f.groups * p.cuts : std::min(f.groups, target);

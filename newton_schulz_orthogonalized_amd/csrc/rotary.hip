@@ -32,6 +32,7 @@ namespace {
 constexpr int NTHR = 256;
 constexpr int MAX_CS = 2048;   // angles of a workgroup: 16 KB of LDS
 constexpr int MAX_TOK = 64;    // rows of a workgroup
+constexpr int PER = 4;         // vectors of a thread: all are on their way before the angles are computed
 
 struct RotArgs {
     mu_rotary_args a;
@@ -39,24 +40,57 @@ struct RotArgs {
     int rot;         // vectors (halves: of one half) that turn, of each head
     int items;       // vectors of a row: all heads of all tensors
     int per_head;    // vectors of a head: those that turn, then those that are copied
-    int chunk;       // vectors of a workgroup (blockIdx.y cuts the rows' vectors)
 };
 
 template <typename T, bool PAIRS>
 __global__ __launch_bounds__(NTHR) void k_rotary(RotArgs A) {
     constexpr int V = vec_of<T>();
+    typedef typename VecOf<T>::V Vec;
     __shared__ float2 cs[MAX_CS];
     const mu_rotary_args& R = A.a;
-    const int half = R.part >> 1;
-    const int64_t rows = R.batch * R.len, row0 = (int64_t)blockIdx.x * A.tok;
-    const int ntok = (int)min((int64_t)A.tok, rows - row0);
+    const uint32_t half = R.part >> 1, len = (uint32_t)R.len;
+    const uint32_t rows = (uint32_t)(R.batch * R.len), row0 = blockIdx.x * (uint32_t)A.tok;   // (up to 2^31)
+    const uint32_t ntok = min((uint32_t)A.tok, rows - row0);
 
-    for (int i = threadIdx.x; i < ntok * half; i += NTHR) {
-        const int t = i / half, f = i - t * half;
-        const int64_t row = row0 + t, s = row % R.len;
+    // this thread's vectors (blockIdx.y cuts the rows' vectors): where they lie, and the loads
+    const uint32_t total = ntok * A.items, first = blockIdx.y * (NTHR * PER) + threadIdx.x;
+    Vec x0[PER], x1[PER];
+    T* out[PER];
+    int cnt[PER];
+    uint32_t ang[PER];   // of its first element, or (copied) ~0
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const uint32_t i = first + j * NTHR;
+        cnt[j] = 0;
+        if (i >= total) continue;
+        const uint32_t t = i / (uint32_t)A.items, w = i - t * A.items;
+        uint32_t head = w / (uint32_t)A.per_head;
+        const int v = (int)(w - head * A.per_head);
+        const int which = R.n == 2 && head >= (uint32_t)R.x[0].heads ? 1 : 0;
+        const mu_rotary_tensor& X = R.x[which];
+        if (which) head -= R.x[0].heads;
+        const uint32_t row = row0 + t, b = row / len, s = row - b * len;
+        const T* x = (const T*)X.x + (int64_t)b * X.x_stride_b + (int64_t)s * X.x_stride_s + (int64_t)head * X.x_stride_h;
+        T* o = (T*)X.out + (int64_t)b * X.out_stride_b + (int64_t)s * X.out_stride_s + (int64_t)head * X.out_stride_h;
+        int e0 = v * V;
+        ang[j] = t * half + (PAIRS ? e0 / 2 : e0);
+        cnt[j] = min(V, (PAIRS ? R.part : (int)half) - e0);
+        if (v >= A.rot) {   // behind the part that turns
+            e0 = R.part + (v - A.rot) * V;
+            ang[j] = ~0u;
+            cnt[j] = min(V, R.dim - e0);
+        }
+        out[j] = o + e0;
+        x0[j] = load_vec<T>(x + e0, cnt[j]);
+        if (!PAIRS && ang[j] != ~0u) x1[j] = load_vec<T>(x + half + e0, cnt[j]);
+    }
+
+    for (uint32_t i = threadIdx.x; i < ntok * half; i += NTHR) {
+        const uint32_t t = i / half, f = i - t * half;
+        const uint32_t row = row0 + t, s = row % len;
         int64_t p = R.offset;
         if (R.positions) {
-            const int64_t at = R.shared_positions ? s : row;
+            const uint32_t at = R.shared_positions ? s : row;
             p += R.position_bits == 32 ? (int64_t)gp((const int32_t*)R.positions)[at] : gp((const int64_t*)R.positions)[at];
         } else {
             p += s;
@@ -69,50 +103,21 @@ __global__ __launch_bounds__(NTHR) void k_rotary(RotArgs A) {
     }
     __syncthreads();
 
-    const int total = ntok * A.items, first = blockIdx.y * A.chunk, last = min(total, first + A.chunk);
-    for (int i = first + threadIdx.x; i < last; i += NTHR) {
-        const int t = i / A.items, w = i - t * A.items;
-        int head = w / A.per_head;
-        const int v = w - head * A.per_head;
-        const int which = R.n == 2 && head >= R.x[0].heads ? 1 : 0;
-        const mu_rotary_tensor& X = R.x[which];
-        if (which) head -= R.x[0].heads;
-        const int64_t row = row0 + t, b = row / R.len, s = row - b * R.len;
-        const T* x = (const T*)X.x + b * X.x_stride_b + s * X.x_stride_s + head * X.x_stride_h;
-        T* o = (T*)X.out + b * X.out_stride_b + s * X.out_stride_s + head * X.out_stride_h;
-        const float2* ang = cs + t * half;
-        if (v >= A.rot) {   // behind the part that turns: the same bits
-            const int e0 = R.part + (v - A.rot) * V, cnt = min(V, R.dim - e0);
-            if (cnt == V) *(MU_GLOBAL typename VecOf<T>::U*)gp(o + e0) = *(const MU_GLOBAL typename VecOf<T>::U*)gp(x + e0);
-            else
-                for (int e = 0; e < cnt; ++e) gp(o)[e0 + e] = gp(x)[e0 + e];
-        } else if constexpr (PAIRS) {
-            const int e0 = v * V, cnt = min(V, R.part - e0);
-            float y[V];
-            load_run<T, V>(x + e0, cnt, y);
 #pragma unroll
-            for (int e = 0; e < V; e += 2) {
-                const float2 q = ang[min((e0 + e) >> 1, half - 1)];
-                const float a = y[e], c = y[e + 1];
-                y[e] = a * q.x - c * q.y;
-                y[e + 1] = c * q.x + a * q.y;
-            }
-            store_run<T, V>(o + e0, cnt, y);
-        } else {
-            const int e0 = v * V, cnt = min(V, half - e0);
-            float y[V], z[V];
-            load_run<T, V>(x + e0, cnt, y);
-            load_run<T, V>(x + half + e0, cnt, z);
+    for (int j = 0; j < PER; ++j) {
+        if (cnt[j] <= 0) continue;
+        if (ang[j] != ~0u) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float2 q = ang[min(e0 + e, half - 1)];
-                const float a = y[e], c = z[e];
-                y[e] = a * q.x - c * q.y;
-                z[e] = c * q.x + a * q.y;
+            for (int e = 0; e < V; e += PAIRS ? 2 : 1) {
+                const float2 q = cs[min(ang[j] + (PAIRS ? e / 2 : e), (uint32_t)MAX_CS - 1)];   // (behind cnt: any)
+                const float a = to_f32<T>(x0[j][e]), c = PAIRS ? to_f32<T>(x0[j][e + (PAIRS ? 1 : 0)]) : to_f32<T>(x1[j][e]);
+                x0[j][e] = from_f32<T>(a * q.x - c * q.y);
+                if (PAIRS) x0[j][e + (PAIRS ? 1 : 0)] = from_f32<T>(c * q.x + a * q.y);
+                else x1[j][e] = from_f32<T>(c * q.x + a * q.y);
             }
-            store_run<T, V>(o + e0, cnt, y);
-            store_run<T, V>(o + half + e0, cnt, z);
+            if (!PAIRS) store_vec<T>(out[j] + half, cnt[j], x1[j]);
         }
+        store_vec<T>(out[j], cnt[j], x0[j]);
     }
 }
 
@@ -166,8 +171,8 @@ int check(const mu_rotary_args* a) {
     if (!a) return fail(MU_ERR_INVALID_ARG, "argument is null");
     if (a->dtype != MU_F32 && a->dtype != MU_BF16) return fail(MU_ERR_DTYPE, "unknown dtype %d", a->dtype);
     if (a->n < 1 || a->n > 2) return fail(MU_ERR_INVALID_ARG, "n must be 1 or 2");
-    if (a->batch < 0 || a->len < 0 || a->batch > ((int64_t)1 << 31) || a->len > ((int64_t)1 << 31) ||
-        (a->len > 0 && a->batch > ((int64_t)1 << 31) / a->len))
+    if (a->batch < 0 || a->len < 0 || a->batch > 0x7fffffffLL || a->len > 0x7fffffffLL ||
+        (a->len > 0 && a->batch > 0x7fffffffLL / a->len))
         return fail(MU_ERR_INVALID_ARG, "bad batch or length");
     if (a->dim < 1 || a->dim > MU_ROTARY_MAX_DIM) return fail(MU_ERR_INVALID_ARG, "dim must be in [1, %d]", MU_ROTARY_MAX_DIM);
     if (a->part < 2 || a->part > a->dim || a->part % 2 != 0) return fail(MU_ERR_INVALID_ARG, "part must be even and in [2, dim]");
@@ -232,21 +237,18 @@ int mu_rotary(const mu_rotary_args* a, void* stream) {
         // in place the rest of each head stays where it is
         bool in_place = true;
         for (int i = 0; i < a->n; ++i) in_place = in_place && (a->x[i].heads == 0 || a->x[i].x == a->x[i].out);
-        RotArgs r{*a, 0, 0, 0, 0, 0};
+        RotArgs r{*a, 0, 0, 0, 0};
         r.rot = (turning + v - 1) / v;
         r.per_head = r.rot + (in_place ? 0 : (a->dim - a->part + v - 1) / v);
         if (heads * r.per_head > (1 << 24)) return fail(MU_ERR_INVALID_ARG, "too many elements in a row");
         r.items = (int)heads * r.per_head;
-        // some four vectors a thread, the angles of the rows within LDS
-        r.tok = std::max(1, std::min({MAX_TOK, MAX_CS / (a->part / 2), 4 * NTHR / r.items}));
-        r.tok = (int)std::min<int64_t>(r.tok, rows);
+        // as many rows as fill a workgroup's threads four times, their angles within LDS; few
+        // rows: one vector a thread, heads shared out over workgroups
+        const int64_t few = rows * r.items <= 256 * NTHR * PER ? 1 : PER;
+        r.tok = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_TOK, MAX_CS / (a->part / 2), few * NTHR / r.items, rows}));
         const int64_t wgs = (rows + r.tok - 1) / r.tok;
-        if (wgs > 0xffffffffLL / NTHR) return fail(MU_ERR_INVALID_ARG, "too many rows for one launch at this size");
-        // few rows: their heads are shared out over workgroups, a vector a thread
-        const int total = r.tok * r.items;
-        const int cuts = (int)std::max<int64_t>(1, std::min<int64_t>({(total + NTHR - 1) / NTHR, 512 / wgs, 65535}));
-        r.chunk = ((total + cuts - 1) / cuts + NTHR - 1) / NTHR * NTHR;
-        const int ny = (total + r.chunk - 1) / r.chunk;
+        const int ny = (r.tok * r.items + NTHR * PER - 1) / (NTHR * PER);
+        if (wgs > 0xffffffffLL / NTHR || ny > 65535) return fail(MU_ERR_INVALID_ARG, "too many rows for one launch at this size");
         const double cells = (double)rows * (double)heads;
         const double bytes = cells * 2.0 * (in_place ? a->part : a->dim) * (double)es + (a->positions ? rows * (a->position_bits / 8.0) : 0.0);
         hipStream_t s = (hipStream_t)stream;
