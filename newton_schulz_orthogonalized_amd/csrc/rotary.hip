@@ -32,7 +32,11 @@ namespace {
 constexpr int NTHR = 256;
 constexpr int MAX_CS = 2048;   // angles of a workgroup: 16 KB of LDS
 constexpr int MAX_TOK = 64;    // rows of a workgroup
-constexpr int PER = 4;         // vectors of a thread: all are on their way before the angles are computed
+
+// Units of a thread, a vector of pairs or one of each half: four vectors are on their way
+// before the angles are computed. Halves with two units 33.4 us, with four 36.1, one 36;
+// pairs with four 34, with two 35.9 (8192 rows of 32 + 8 heads of 128, bfloat16, cold).
+template <bool PAIRS> constexpr int per() { return PAIRS ? 4 : 2; }
 
 struct RotArgs {
     mu_rotary_args a;
@@ -44,7 +48,7 @@ struct RotArgs {
 
 template <typename T, bool PAIRS>
 __global__ __launch_bounds__(NTHR) void k_rotary(RotArgs A) {
-    constexpr int V = vec_of<T>();
+    constexpr int V = vec_of<T>(), PER = per<PAIRS>();
     typedef typename VecOf<T>::V Vec;
     __shared__ float2 cs[MAX_CS];
     const mu_rotary_args& R = A.a;
@@ -242,8 +246,9 @@ int mu_rotary(const mu_rotary_args* a, void* stream) {
         r.per_head = r.rot + (in_place ? 0 : (a->dim - a->part + v - 1) / v);
         if (heads * r.per_head > (1 << 24)) return fail(MU_ERR_INVALID_ARG, "too many elements in a row");
         r.items = (int)heads * r.per_head;
-        // as many rows as fill a workgroup's threads four times, their angles within LDS; few
-        // rows: one vector a thread, heads shared out over workgroups
+        // as many rows as fill a workgroup's threads `per` times, their angles within LDS; few
+        // rows: as many as fill them once, a long row's heads shared out over workgroups
+        const int PER = a->interleaved ? per<true>() : per<false>();
         const int64_t few = rows * r.items <= 256 * NTHR * PER ? 1 : PER;
         r.tok = (int)std::max<int64_t>(1, std::min<int64_t>({MAX_TOK, MAX_CS / (a->part / 2), few * NTHR / r.items, rows}));
         const int64_t wgs = (rows + r.tok - 1) / r.tok;
