@@ -249,8 +249,9 @@ __global__ __launch_bounds__(NTHR, 1) void k_tile(TileArgs A) {
             }
         } else {
             const int64_t at = row * A.n + col;
-            if (MODE == DX && A.part) {
-                store_run<float, 8>(A.part + (int64_t)blockIdx.y * A.m * A.n + at, cnt, v);
+            if (A.part) {
+                const int64_t piece = MODE == DW ? blockIdx.y * 2 + which : blockIdx.y;
+                store_run<float, 8>(A.part + piece * A.m * A.n + at, cnt, v);
             } else if (MODE == DW && (A.out_f32 || ES == 4)) {
                 float* o = (float*)A.out[which] + at;
                 if (A.accumulate) {
@@ -272,14 +273,14 @@ __global__ __launch_bounds__(NTHR, 1) void k_tile(TileArgs A) {
     }
 }
 
-// Sums of the splits of the gradient of x, in order; also zeros of both weights' gradients
-// where there are no tokens.
+// Sums of the splits of a gradient, in order (of both weights', side by side in `part`);
+// also zeros of both where there are no tokens.
 struct JoinArgs {
     const float* part;
     void* out[2];
     int64_t n;        // elements of a result
     int splits;       // 0: zeros
-    bool out_f32;
+    bool out_f32, accumulate;
 };
 __global__ __launch_bounds__(NTHR) void k_join(JoinArgs A) {
     const int64_t i = ((int64_t)blockIdx.x * NTHR + threadIdx.x) * 8;   // of one result (blockIdx.y)
@@ -287,11 +288,17 @@ __global__ __launch_bounds__(NTHR) void k_join(JoinArgs A) {
     if (cnt <= 0) return;
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, v[8];
     for (int k = 0; k < A.splits; ++k) {
-        load_run<float, 8>(A.part + k * A.n + i, cnt, v);
+        load_run<float, 8>(A.part + ((int64_t)k * gridDim.y + blockIdx.y) * A.n + i, cnt, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) s[e] += v[e];
     }
     void* out = blockIdx.y ? A.out[1] : A.out[0];
+    if (A.accumulate) {
+        if (A.out_f32) load_run<float, 8>((const float*)out + i, cnt, v);
+        else load_run<bf16, 8>((const bf16*)out + i, cnt, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] += v[e];
+    }
     if (A.out_f32) store_run<float, 8>((float*)out + i, cnt, s);
     else store_run<bf16, 8>((bf16*)out + i, cnt, s);
 }
@@ -396,10 +403,12 @@ Source source(const void* p, int64_t rows, int64_t n, int es, Plan& pl) {
 // 15.4, 13.8 (256 tiles of 128), of 256 tokens 6.3, 11.1 (64); both weights' gradients
 // 15, 17 (192) and 4.4, 4.8 (192); 64 tokens of 4096 x 14336 131, 121 (7168).
 //
-// Only the gradient of x is split over k (2 * hidden): its tiles are few and their k long,
-// where the weights' gradients are large and few k deep (splitting those in two cost 1000
-// tokens 10 us, 512 tokens of 2048 x 8192 105). As many splits as fill the chip twice (two
-// workgroups of 64 a compute unit), at least eight slices each: 256 tokens of 768 x 2048,
+// The gradient of x is split over k (2 * hidden): its tiles are few and their k long. The
+// weights' gradients are large and few k deep (splitting those in two cost 1000 tokens 10
+// us, 512 tokens of 2048 x 8192 105), unless their tiles leave half the chip idle: 16384
+// tokens of 256 x 512 (64 tiles of 64) 72 against 46 us, float32 299 against 108; 1024
+// tokens 11.3 against 12.5, so bfloat16 splits have sixteen slices at least. As many splits as fill the chip twice (two
+// workgroups of 64 a compute unit), else eight slices at least: 256 tokens of 768 x 2048,
 // 48 tiles, 1, 2, 4 splits 21.9, 18.1, 16.6 us, float32 78, 47, 31; 64 tokens of 4096 x
 // 14336, 64 tiles, 103, 60, 38.5; 1000 tokens of 768, float32, 192 tiles, 82, 78, 66.
 Cut cut_of(int64_t m, int64_t n, int nmat, bool dual, int64_t kts, int dtype, bool split) {
@@ -407,11 +416,11 @@ Cut cut_of(int64_t m, int64_t n, int nmat, bool dual, int64_t kts, int dtype, bo
     Cut c{128, (int)kts, 1};
     if (dtype == MU_BF16 && tiles(256) >= 128) c.edge = 256;
     else if (tiles(128) < 256) c.edge = 64;
-    if (split && dtype == MU_BF16 && c.edge == 64 && tiles(128) >= 96 && kts >= 32) {
+    if (split && nmat == 1 && dtype == MU_BF16 && c.edge == 64 && tiles(128) >= 96 && kts >= 32) {
         c.edge = 128;   // 2048 tokens of 1000 x 2500: two splits of 128 51 us, tiles of 64 60
         c.splits = 2;
-    } else if (split && c.edge == 64 && tiles(64) < 384) {
-        c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(512, tiles(64)), kts / 8, 16}));
+    } else if (split && c.edge == 64 && tiles(64) < (nmat == 2 ? 128 : 384)) {
+        c.splits = (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(512, tiles(64)), kts / (nmat == 2 && dtype == MU_BF16 ? 16 : 8), 16}));
     }
     c.kt = (int)ceil_div(kts, c.splits);
     c.splits = (int)ceil_div(kts, c.kt);
@@ -448,9 +457,10 @@ Plan plan_bwd(const mu_gated_grad* a) {
     const int64_t bk = 128 / es;
     p.fwd = cut_of(a->tokens, a->hidden, 1, true, ceil_div(a->dim, bk), a->dtype, false);
     p.dx = cut_of(a->tokens, a->dim, 1, false, 2 * ceil_div(a->hidden, bk), a->dtype, true);
-    p.dw = cut_of(a->hidden, a->dim, 2, false, ceil_div(a->tokens, bk), a->dtype, false);
+    p.dw = cut_of(a->hidden, a->dim, 2, false, ceil_div(a->tokens, bk), a->dtype, true);
     size_t part = 0;
     if (a->dx && p.dx.splits > 1) part = sizeof(float) * (size_t)(p.dx.splits * a->tokens * a->dim);
+    if (a->d_gate && p.dw.splits > 1) part = std::max(part, sizeof(float) * (size_t)(p.dw.splits * 2 * a->hidden * a->dim));
     p.off_part = p.bytes;
     p.bytes += align_up(part);
     return p;
@@ -579,7 +589,7 @@ int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
         t.out[0] = a->dx;
         t.part = p.dx.splits > 1 ? (float*)(ws + p.off_part) : nullptr;
         rc = product<T, DX>(MU_K_GATED_GRAD, t, p.dx, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 2 * n * f), s);
-        if (!rc && t.part) rc = join(JoinArgs{t.part, {a->dx, nullptr}, a->tokens * a->dim, p.dx.splits, sizeof(T) == 4}, s);
+        if (!rc && t.part) rc = join(JoinArgs{t.part, {a->dx, nullptr}, a->tokens * a->dim, p.dx.splits, sizeof(T) == 4, false}, s);
         if (rc) return rc;
     }
     if (a->d_gate) {
@@ -592,9 +602,11 @@ int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
         t.out[1] = a->d_up;
         t.out_f32 = a->grad_dtype == MU_F32;
         t.accumulate = a->accumulate;
-        t.part = nullptr;
+        t.part = p.dw.splits > 1 ? (float*)(ws + p.off_part) : nullptr;
         rc = product<T, DW>(MU_K_GATED_GRAD, t, p.dw, 4.0 * n * d * f,
                             sizeof(T) * (n * d + 2 * n * f) + es_of(a->grad_dtype) * 2 * d * f, s);
+        if (!rc && t.part)
+            rc = join(JoinArgs{t.part, {a->d_gate, a->d_up}, a->hidden * a->dim, p.dw.splits, t.out_f32, t.accumulate != 0}, s);
     }
     return rc;
 }
@@ -713,7 +725,7 @@ int mu_gated_mlp_grad(const mu_gated_grad* a, void* ws, size_t ws_bytes, void* s
         hipStream_t s = (hipStream_t)stream;
         if (a->tokens == 0) {   // no rows: zero gradients
             if (!a->d_gate || a->accumulate) return MU_OK;
-            return join(JoinArgs{nullptr, {a->d_gate, a->d_up}, a->hidden * a->dim, 0, a->grad_dtype == MU_F32}, s);
+            return join(JoinArgs{nullptr, {a->d_gate, a->d_up}, a->hidden * a->dim, 0, a->grad_dtype == MU_F32, false}, s);
         }
         const Plan p = plan_bwd(a);
         rc = check_workspace(ws, ws_bytes, p.bytes);

@@ -93,9 +93,11 @@ def test_integers_are_exact(t, d, f, dtype):
             assert np.array_equal(to_np(c), _rounded(d_up + _rounded(d_up, wt), wt))
 
 
-# many tiles of each edge: whole and ragged, even and odd numbers of slices of k, several tiles for a workgroup
+# many tiles of each edge: whole and ragged, even and odd numbers of slices of k, several tiles for a workgroup; and few
+# tiles over many tokens, whose weights' gradients are split
 LARGE = [(4096, 192, 2048), (3900, 264, 2100), (4100, 64, 1999), (2050, 1000, 3500), (1030, 4096, 7000), (520, 2056, 14000),
-         (1000, 768, 2048), (2050, 257, 1500), (90, 2048, 1000)]
+         (1000, 768, 2048), (2050, 257, 1500), (90, 2048, 1000),
+         (4100, 24, 16), (3000, 130, 70), (9000, 64, 128), (2049, 513, 200)]
 
 
 @pytest.mark.parametrize("dtype,wt", [(BF, BF), (BF, FP), (FP, FP)])
