@@ -375,7 +375,8 @@ __global__ __launch_bounds__(NTHR, 1) void k_wide(TileArgs A) {
             // through a resource that ends with the result, at one offset a lane; else by address.
             auto rows_of = [&](void* p, int64_t ld, int es) {
                 const int rows = (int)max(min(A.m - row1, (int64_t)16), (int64_t)0);
-                return resource((const char*)p + (row1 * ld + col0) * es, rows > 0 ? (rows * (int)ld - (int)col0) * es : 0);
+                // (nothing, where this wave's columns begin behind the last one)
+                return resource((const char*)p + (row1 * ld + col0) * es, max(rows * (int)ld - (int)col0, 0) * es);
             };
             auto put = [&](bf16* p, int64_t ld, int pass, int n, const float (&v)[8]) {
                 if (A.aligned) {

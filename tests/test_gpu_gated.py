@@ -99,6 +99,10 @@ LARGE = [(4096, 192, 2048), (3900, 264, 2100), (4100, 64, 1999), (2050, 1000, 35
          (1000, 768, 2048), (2050, 257, 1500), (90, 2048, 1000),
          (4100, 24, 16), (3000, 130, 70), (9000, 64, 128), (2049, 513, 200)]
 
+# tiles of 256 whose last strip is a single row and whose last columns are half a tile or less: of the forward
+# product and the gradient of x, of results narrower than half a tile, and of the weights' gradients
+LARGE += [(8193, 264, 2056), (32769, 8, 24), (700, 1032, 16385)]
+
 
 @pytest.mark.parametrize("dtype,wt", [(BF, BF), (BF, FP), (FP, FP)])
 @pytest.mark.parametrize("t,d,f", LARGE)
