@@ -194,11 +194,42 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
     const int dim = (int)P.dim, lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
     const bool wbf = P.weight_dtype == MU_BF16;
     int turn3 = 0, turn1 = 0;
+    // Column sums of rows past 4096: two of the three lie in LDS, each lane its own (two reads
+    // and two writes a run beside a row's six passes over HBM); registers are short of them.
+    constexpr bool IN_LDS = WPR * NV >= 16;
+    __shared__ f32x4 sums[IN_LDS ? 4 * NV * LANES : 1];
+    auto kept = [&](int which, int j, int half) -> f32x4& { return sums[((which * NV + j) * 2 + half) * LANES + lane]; };
     float apre[NV][V], apost[NV][V], agate[NV][V];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int e = 0; e < V; ++e) apre[j][e] = apost[j][e] = agate[j][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4 && IN_LDS; ++k) kept(k >> 1, j, k & 1) = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // which: 0 post, 1 gate
+    auto add = [&](int which, float (&acc)[NV][V], int j, const float (&v)[V]) {
+        if constexpr (IN_LDS) {
+            kept(which, j, 0) += f32x4{v[0], v[1], v[2], v[3]};
+            kept(which, j, 1) += f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[j][e] += v[e];
+        }
+    };
+    auto fetch_sums = [&](int which, float (&acc)[NV][V]) {
+        if constexpr (IN_LDS) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 x = kept(which, j, h);
+                    kept(which, j, h) = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][4 * h + e] = x[e];
+                }
+        }
+    };
 
     // sixteen waves have half the registers: no weights and no next row are held
     constexpr bool AHEAD = WPR < 16;
@@ -242,6 +273,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
             for (int j = 0; j < NV; ++j) {
                 const int cnt = dim - (j * LANES + lane) * V;
                 float r[V], y[V], n[V];
+                if (!AHEAD) __builtin_amdgcn_sched_barrier(0);   // one run's registers at a time
                 if (!AHEAD) weights(j);
                 if (A.a.grad_normed) {
                     kr[j].widen(r);
@@ -268,6 +300,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
             for (int j = 0; j < NV; ++j) {
                 const int c = (j * LANES + lane) * V, cnt = dim - c;
                 float y[V], g[V], o[V];
+                if (!AHEAD) __builtin_amdgcn_sched_barrier(0);
                 if (!AHEAD) weights(j);
                 kd[j].widen(d[j]);
                 if (!A.a.grad_residual) {
@@ -294,15 +327,18 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
                 if (!P.update) continue;
                 load_weight(P.gate, wbf, P.gate ? group * dim + c : 0, cnt, g);
                 ky[j].widen(y);
+                float sg[V], sp[V];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float h = y[e] * f1;          // y, normed
-                    agate[j][e] += d[j][e] * (h * wpost[j][e]);
+                    sg[e] = d[j][e] * (h * wpost[j][e]);
                     d[j][e] *= g[e];
-                    apost[j][e] += d[j][e] * h;
+                    sp[e] = d[j][e] * h;
                     d[j][e] *= wpost[j][e];
                     sv[0] += e < cnt ? d[j][e] * y[e] : 0.f;
                 }
+                if (!IN_LDS || A.a.d_gate) add(1, agate, j, sg);
+                if (!IN_LDS || A.post) add(0, apost, j, sp);
             }
             if (!A.a.d_update) continue;
             float c1 = 0.f;
@@ -320,11 +356,14 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
                 store_run<TY, V>((TY*)A.a.d_update + row * dim + c, cnt, o);
             }
         }
-        if (A.a.d_gate)
+        if (A.a.d_gate) {
+            fetch_sums(1, agate);
             flush<WPR, NV>(agate, A.gate ? A.gate + (int64_t)blockIdx.x * dim : nullptr,
                            (char*)A.a.d_gate + group * dim * (wbf ? 2 : 4), wbf, dim, lds);
+        }
     }
     if (A.pre) flush<WPR, NV>(apre, A.pre + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
+    fetch_sums(0, apost);
     if (A.post) flush<WPR, NV>(apost, A.post + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
 }
 
