@@ -4,7 +4,7 @@
 //   r' = a r + gate * N(y; post),  n = N(r'; pre),  N(v; w) = v s w,
 //   s = (mean(v^2) + eps)^(-1/2)
 //
-// A team of WPR waves holds a row in registers between its sums: every element is
+// A team of 8 to 1024 lanes holds a row in registers between its sums: every element is
 // read once and written once. Gradients, with t = dn * pre, s2 and s1 the factors
 // of r' and y, D the row length:
 //   d      = dr' + s2 t - s2^3 (sum t r') / D r'
@@ -34,17 +34,17 @@ namespace {
 
 constexpr int V = 8;   // elements of a run: one or two 16-byte accesses
 
-// A workgroup: TEAMS teams of WPR waves, a row each.
-template <int WPR> constexpr int teams() { return WPR == 1 ? 4 : 1; }
-template <int WPR> constexpr int threads() { return 64 * WPR * teams<WPR>(); }
+// A workgroup: teams of LANES lanes (part of a wave, one, or several), a row each.
+template <int LANES> constexpr int teams() { return LANES <= 64 ? 256 / LANES : 1; }
+template <int LANES> constexpr int threads() { return LANES * teams<LANES>(); }
 
 // Sums of K values over the team, in a fixed order. Alternating halves of `red`
 // make one barrier a sum enough: a half is written again only behind the next
 // sum's barrier.
-template <int WPR, int K>
+template <int LANES, int K>
 __device__ __forceinline__ void team_sums(float (&v)[K], float (*red)[K][16], int& turn) {
-    wave_sums(v);
-    if constexpr (WPR > 1) {
+    wave_sums<LANES < 64 ? LANES : 64>(v);
+    if constexpr (LANES > 64) {
         float(*r)[16] = red[turn];
         turn ^= 1;
         const int wave = threadIdx.x >> 6;
@@ -57,7 +57,7 @@ __device__ __forceinline__ void team_sums(float (&v)[K], float (*red)[K][16], in
         for (int k = 0; k < K; ++k) {
             float s = 0.f;
 #pragma unroll
-            for (int w = 0; w < WPR; ++w) s += r[k][w];
+            for (int w = 0; w < LANES / 64; ++w) s += r[k][w];
             v[k] = s;
         }
     }
@@ -81,9 +81,9 @@ struct FwdArgs {
     float inv_dim;
 };
 
-template <typename TR, typename TY, int WPR, int NV>
-__global__ __launch_bounds__(threads<WPR>()) void k_resnorm(FwdArgs A) {
-    constexpr int TEAMS = teams<WPR>(), LANES = 64 * WPR;
+template <typename TR, typename TY, int LANES, int NV>
+__global__ __launch_bounds__(threads<LANES>()) void k_resnorm(FwdArgs A) {
+    constexpr int TEAMS = teams<LANES>();
     __shared__ float red[2][1][16];
     const mu_resnorm& P = A.a;
     const int dim = (int)P.dim, lane = threadIdx.x % LANES;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm(FwdArgs A) {
             for (int j = 0; j < NV; ++j)
 #pragma unroll
                 for (int e = 0; e < V; ++e) s[0] += y[j][e] * y[j][e];
-            team_sums<WPR>(s, red, turn);
+            team_sums<LANES>(s, red, turn);
             f = 1.f / sqrtf(s[0] * A.inv_dim + P.eps);
         }
         float s[1] = {0.f};
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm(FwdArgs A) {
 #pragma unroll
             for (int e = 0; e < V; ++e) s[0] += e < cnt ? r[j][e] * r[j][e] : 0.f;
         }
-        team_sums<WPR>(s, red, turn);
+        team_sums<LANES>(s, red, turn);
         f = 1.f / sqrtf(s[0] * A.inv_dim + P.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -154,9 +154,9 @@ struct BwdArgs {
 };
 
 // Add the teams' sums up and write them: as a partial row, or finished.
-template <int WPR, int NV>
+template <int LANES, int NV>
 __device__ __forceinline__ void flush(float (&acc)[NV][V], float* part, void* out, bool out_bf16, int dim, float* lds) {
-    constexpr int TEAMS = teams<WPR>(), LANES = 64 * WPR;
+    constexpr int TEAMS = teams<LANES>();
     const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -184,9 +184,9 @@ __device__ __forceinline__ void flush(float (&acc)[NV][V], float* part, void* ou
     }
 }
 
-template <typename TR, typename TY, int WPR, int NV>
-__global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
-    constexpr int TEAMS = teams<WPR>(), LANES = 64 * WPR;
+template <typename TR, typename TY, int LANES, int NV>
+__global__ __launch_bounds__(threads<LANES>()) void k_resnorm_grad(BwdArgs A) {
+    constexpr int TEAMS = teams<LANES>();
     __shared__ float red3[2][3][16];
     __shared__ float red1[2][1][16];
     __shared__ float lds[TEAMS > 1 ? TEAMS * LANES * V : 1];
@@ -196,7 +196,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
     int turn3 = 0, turn1 = 0;
     // Column sums of rows past 4096: two of the three lie in LDS, each lane its own (two reads
     // and two writes a run beside a row's six passes over HBM); registers are short of them.
-    constexpr bool IN_LDS = WPR * NV >= 16;
+    constexpr bool IN_LDS = LANES * NV >= 1024;
     __shared__ f32x4 sums[IN_LDS ? 4 * NV * LANES : 1];
     auto kept = [&](int which, int j, int half) -> f32x4& { return sums[((which * NV + j) * 2 + half) * LANES + lane]; };
     float apre[NV][V], apost[NV][V], agate[NV][V];
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
     };
 
     // sixteen waves have half the registers: no weights and no next row are held
-    constexpr bool AHEAD = WPR < 16;
+    constexpr bool AHEAD = LANES < 1024;
     float wpre[NV][V], wpost[NV][V];
     auto weights = [&](int j) {
         const int c = (j * LANES + lane) * V, cnt = dim - c;
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
                     for (int e = 0; e < V; ++e) s[2] += y[e] * y[e];
                 }
             }
-            team_sums<WPR>(s, red3, turn3);
+            team_sums<LANES>(s, red3, turn3);
             const float f1 = P.post_norm ? 1.f / sqrtf(s[2] * A.inv_dim + P.eps) : 1.f;
             const float f2 = 1.f / sqrtf(s[0] * A.inv_dim + P.eps);
             const float c2 = f2 * (f2 * (f2 * (s[1] * A.inv_dim)));
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
             if (!A.a.d_update) continue;
             float c1 = 0.f;
             if (P.post_norm) {
-                team_sums<WPR>(sv, red1, turn1);
+                team_sums<LANES>(sv, red1, turn1);
                 c1 = f1 * (f1 * (f1 * (sv[0] * A.inv_dim)));
             }
 #pragma unroll
@@ -358,13 +358,13 @@ __global__ __launch_bounds__(threads<WPR>()) void k_resnorm_grad(BwdArgs A) {
         }
         if (A.a.d_gate) {
             fetch_sums(1, agate);
-            flush<WPR, NV>(agate, A.gate ? A.gate + (int64_t)blockIdx.x * dim : nullptr,
+            flush<LANES, NV>(agate, A.gate ? A.gate + (int64_t)blockIdx.x * dim : nullptr,
                            (char*)A.a.d_gate + group * dim * (wbf ? 2 : 4), wbf, dim, lds);
         }
     }
-    if (A.pre) flush<WPR, NV>(apre, A.pre + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
+    if (A.pre) flush<LANES, NV>(apre, A.pre + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
     fetch_sums(0, apost);
-    if (A.post) flush<WPR, NV>(apost, A.post + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
+    if (A.post) flush<LANES, NV>(apost, A.post + (int64_t)blockIdx.x * dim, nullptr, false, dim, lds);
 }
 
 // Column sums of partial rows, in order: a workgroup sums 64 columns of one
@@ -440,22 +440,26 @@ int check_common(const mu_resnorm* a) {
     return MU_OK;
 }
 
-// Waves of a row and runs of a lane: forward, and the gradient, whose rows are four runs,
-// the next row's four and three sums (two runs a lane fill the registers of eight waves;
-// sixteen waves have half as many: past 8192 it keeps no row ahead and spills all the same).
+// Lanes of a row and runs of a lane. Short rows share a wave: 510012 rows of 64 with a wave
+// each took 1.1 ms both ways. The gradient's rows are four runs, the next row's four and
+// three sums: two runs a lane fill the registers of eight waves, and sixteen waves have half
+// as many, so past 8192 it keeps no row ahead.
 template <template <typename, typename, int, int> class L, typename TR, typename TY, bool GRAD, typename... X>
 hipError_t by_dim(int64_t dim, X&&... x) {
-    if (dim <= 512) return L<TR, TY, 1, 1>::go(x...);
-    if (dim <= 1024) return L<TR, TY, 1, 2>::go(x...);
-    if (dim <= 2048) return L<TR, TY, 4, 1>::go(x...);
+    if (dim <= 64) return L<TR, TY, 8, 1>::go(x...);
+    if (dim <= 128) return L<TR, TY, 16, 1>::go(x...);
+    if (dim <= 256) return L<TR, TY, 32, 1>::go(x...);
+    if (dim <= 512) return L<TR, TY, 64, 1>::go(x...);
+    if (dim <= 1024) return L<TR, TY, 64, 2>::go(x...);
+    if (dim <= 2048) return L<TR, TY, 256, 1>::go(x...);
     if constexpr (GRAD) {
-        if (dim <= 4096) return L<TR, TY, 8, 1>::go(x...);
-        if (dim <= 8192) return L<TR, TY, 8, 2>::go(x...);
+        if (dim <= 4096) return L<TR, TY, 512, 1>::go(x...);
+        if (dim <= 8192) return L<TR, TY, 512, 2>::go(x...);
     } else {
-        if (dim <= 4096) return L<TR, TY, 4, 2>::go(x...);
-        if (dim <= 8192) return L<TR, TY, 16, 1>::go(x...);
+        if (dim <= 4096) return L<TR, TY, 256, 2>::go(x...);
+        if (dim <= 8192) return L<TR, TY, 1024, 1>::go(x...);
     }
-    return L<TR, TY, 16, 2>::go(x...);
+    return L<TR, TY, 1024, 2>::go(x...);
 }
 template <template <typename, typename, int, int> class L, bool GRAD, typename... X>
 hipError_t by_type(const mu_resnorm& a, X&&... x) {
@@ -464,19 +468,19 @@ hipError_t by_type(const mu_resnorm& a, X&&... x) {
     return by_dim<L, bf16, bf16, GRAD>(a.dim, x...);
 }
 
-template <typename TR, typename TY, int WPR, int NV>
+template <typename TR, typename TY, int LANES, int NV>
 struct Fwd {
     static hipError_t go(const FwdArgs& f, hipStream_t s) {
-        const int64_t teams_needed = (f.a.rows + teams<WPR>() - 1) / teams<WPR>();
+        const int64_t teams_needed = (f.a.rows + teams<LANES>() - 1) / teams<LANES>();
         const unsigned grid = (unsigned)std::min<int64_t>(teams_needed, 1 << 20);
-        hipLaunchKernelGGL((k_resnorm<TR, TY, WPR, NV>), dim3(grid), dim3(threads<WPR>()), 0, s, f);
+        hipLaunchKernelGGL((k_resnorm<TR, TY, LANES, NV>), dim3(grid), dim3(threads<LANES>()), 0, s, f);
         return hipGetLastError();
     }
 };
-template <typename TR, typename TY, int WPR, int NV>
+template <typename TR, typename TY, int LANES, int NV>
 struct Bwd {
     static hipError_t go(const BwdArgs& b, unsigned grid, hipStream_t s) {
-        hipLaunchKernelGGL((k_resnorm_grad<TR, TY, WPR, NV>), dim3(grid), dim3(threads<WPR>()), 0, s, b);
+        hipLaunchKernelGGL((k_resnorm_grad<TR, TY, LANES, NV>), dim3(grid), dim3(threads<LANES>()), 0, s, b);
         return hipGetLastError();
     }
 };
@@ -494,7 +498,8 @@ GradPlan plan_of(const mu_resnorm_grad* a) {
     const mu_resnorm& f = a->fwd;
     GradPlan p{};
     const int64_t per_group = f.rows / f.groups, target = f.dim > 2048 ? TARGET_WGS / 2 : TARGET_WGS;
-    p.cuts = std::max<int64_t>(1, std::min(target / f.groups, (per_group + MIN_ROWS - 1) / MIN_ROWS));
+    const int64_t least = f.dim <= 64 ? 32 : f.dim <= 128 ? 16 : f.dim <= 256 ? 8 : MIN_ROWS;   // a row for each team
+    p.cuts = std::max<int64_t>(1, std::min(target / f.groups, (per_group + least - 1) / least));
     p.chunk = per_group > 0 ? (per_group + p.cuts - 1) / p.cuts : 1;
     if (per_group > 0) p.cuts = (per_group + p.chunk - 1) / p.chunk;
     p.grid = f.rows == 0 ? 0 : p.cuts > 1 ? f.groups * p.cuts : std::min(f.groups, target);

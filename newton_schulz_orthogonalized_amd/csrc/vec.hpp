@@ -96,14 +96,14 @@ __device__ __forceinline__ void store_run(T* q, int cnt, const float (&v)[V]) {
     }
 }
 
-// Sums of K values over a wave in a fixed order, in every lane: pairs, quads, halves and
-// whole rows of 16 lanes, then rows of 16 and of 32 swapped. All in vector instructions
-// (shuffles through LDS took the norms' row sums 400 cycles).
+// Sums of K values over each run of N lanes (8 to 64) in a fixed order, in every lane: pairs,
+// quads, halves of a row of 16 lanes, rows, then rows of 16 and of 32 swapped. All in vector
+// instructions (shuffles through LDS made the norms' row sums 400 cycles longer).
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
     return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
 }
-template <int K>
+template <int N, int K>
 __device__ __forceinline__ void wave_sums(float (&v)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = dpp_add<0xb1>(v[k]);    // quad_perm 1 0 3 2
@@ -112,15 +112,15 @@ __device__ __forceinline__ void wave_sums(float (&v)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = dpp_add<0x141>(v[k]);   // row_half_mirror
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = dpp_add<0x140>(v[k]);   // row_mirror
+    for (int k = 0; k < K && N >= 16; ++k) v[k] = dpp_add<0x140>(v[k]);   // row_mirror
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < K && N >= 32; ++k) {
         const unsigned u = __builtin_bit_cast(unsigned, v[k]);
         const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
         v[k] = __builtin_bit_cast(float, (unsigned)p[0]) + __builtin_bit_cast(float, (unsigned)p[1]);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; k < K && N == 64; ++k) {
         const unsigned u = __builtin_bit_cast(unsigned, v[k]);
         const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
         v[k] = __builtin_bit_cast(float, (unsigned)p[0]) + __builtin_bit_cast(float, (unsigned)p[1]);

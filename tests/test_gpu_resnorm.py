@@ -81,7 +81,8 @@ def _check_grads(res, dr, dn, new, y, gate, post_norm, post, pre, a, eps):
 TYPES = [(BF, BF, BF), (FP, FP, FP), (FP, BF, BF), (BF, BF, FP), (FP, BF, FP)]
 # rows, dim, groups (0: no gate)
 SHAPES = [(1, 1, 0), (1, 7, 1), (3, 64, 0), (6, 513, 3), (9, 512, 9), (5, 1000, 0), (33, 1024, 1), (4, 1025, 2), (8, 2048, 4),
-          (7, 2050, 0), (6, 4096, 2), (3, 4097, 0), (4, 8192, 1), (2, 9001, 2), (2, 16384, 0), (130, 96, 2), (700, 24, 700)]
+          (7, 2050, 0), (6, 4096, 2), (3, 4097, 0), (4, 8192, 1), (2, 9001, 2), (2, 16384, 0), (130, 96, 2), (700, 24, 700),
+          (37, 64, 1), (1000, 65, 2), (257, 128, 0), (70, 129, 7), (300, 200, 1), (100, 256, 4), (41, 257, 0)]
 
 
 @pytest.mark.parametrize("rt,yt,wt", TYPES)
@@ -125,7 +126,7 @@ def test_rms_norm(rows, dim, xt, nt, wt):
             assert torch.equal(y, n)
 
 
-@pytest.mark.parametrize("rows,dim,groups", [(3000, 512, 2), (2048, 300, 1), (5000, 100, 5000), (1500, 2048, 3), (600, 6000, 600)])
+@pytest.mark.parametrize("rows,dim,groups", [(3000, 512, 2), (2048, 300, 1), (20000, 64, 1), (9000, 128, 3), (7000, 250, 100), (5000, 100, 5000), (1500, 2048, 3), (600, 6000, 600)])
 def test_sums_over_many_rows(rows, dim, groups):
     """Column sums of more rows than workgroups, and more gates than workgroups;
     the same call gives the same bits."""
