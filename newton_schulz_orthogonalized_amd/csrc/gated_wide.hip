@@ -25,6 +25,11 @@
 //
 // A workgroup takes tile after tile (one fixed share each, those of an XCD next to
 // each other) and starts the loads of the next tile before it writes this one.
+//
+// What bounds it: matrix instructions. A slice takes 2570 cycles, its instructions 2048; a
+// tile's results about 10 us. 8192 tokens of 4096 x 14336: gradient of x 1322 us and of both
+// weights 1331 (1.45 PFLOP/s), forward with both products kept 1527 (1.26). All of it in
+// tiles of 128 with two barriers a slice 6550, with these 4390.
 #include "gated.hpp"
 
 namespace mu {
