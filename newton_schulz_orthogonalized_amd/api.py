@@ -380,7 +380,10 @@ def _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stre
 # The backward passes below run on a thread of autograd's, where every Python
 # object that the forward call touched on its own thread costs a transfer between
 # cores: they start from the structs that the forward calls filled and set
-# addresses alone (the saved tensors', as they may have been moved meanwhile).
+# addresses alone (the saved tensors', as they may have been moved meanwhile). A
+# struct holds no tensor: what it points at, dense copies of gradients among it,
+# keeps a name here until the launch has been made, or the workspace that is
+# allocated before the launch may get its memory.
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, freqs, positions, offset, interleaved, scale, inverse, stream):
@@ -489,7 +492,8 @@ class _ResidualNorm(torch.autograd.Function):
             dr, dn = None, dr
         res = (None,) * 5
         if dr is not None or dn is not None:
-            a, res = _lib.resnorm_backward(ctx.args, saved, need, _dense(dr), _dense(dn))
+            dr, dn = _dense(dr), _dense(dn)
+            a, res = _lib.resnorm_backward(ctx.args, saved, need, dr, dn)
             _on(saved[0].get_device(), None, _lib.resnorm_grad_call, a, saved[0])
         return (*res, None, None, None, None, None)
 
@@ -561,8 +565,8 @@ class _GatedMlp(torch.autograd.Function):
     @staticmethod
     @_once
     def backward(ctx, grad):
-        saved = ctx.saved_tensors
-        a, res = _lib.gated_backward(ctx.args, saved, ctx.needs_input_grad, grad.contiguous())
+        saved, grad = ctx.saved_tensors, _dense(grad)
+        a, res = _lib.gated_backward(ctx.args, saved, ctx.needs_input_grad, grad)
         _on(saved[0].get_device(), None, _lib.gated_grad_call, a, saved[0])
         return (*res[:3], None, None, None, None)
 
