@@ -13,6 +13,8 @@ too. The caller orders `stream` behind what made the inputs, and its own use of
 the results behind `stream`. Nothing here computes. Of the results those of
 embedding, rotary, residual_norm, rms_norm and gated_mlp carry gradients (not in
 forward mode, which they refuse, and once: a gradient of a gradient is refused).
+Buffers of the caller's that rotary, the norms and the gated product write count
+as changed in place: a backward pass that saved one of them raises.
 """
 
 from __future__ import annotations
@@ -156,6 +158,14 @@ def _differentiable(what: str, tensors, *outs) -> bool:
     if any(o is not None for o in outs):
         raise ValueError("outputs of the caller's take no gradient: call under torch.no_grad()")
     return True
+
+
+def _wrote(*outs):
+    """Count the caller's buffers that a call wrote as changed in place, as torch's
+    own operations do: a backward pass that saved one of them then refuses."""
+    for o in outs:
+        if o is not None:
+            torch.autograd.graph.increment_version(o)
 
 
 def _once(backward):
@@ -373,6 +383,7 @@ def _rotary(xs, freqs, positions, offset, interleaved, scale, inverse, out, stre
         outs = out if out is not None else tuple([_new(x.shape, x.dtype, device, stream) for x in xs])
         a = _lib.rotary_args(xs, outs, freqs, positions, offset, interleaved, inverse, scale)
         _lib.mu_rotary(a, st)
+        _wrote(*(out or ()))
         return outs, a
     return _on(device, stream, call)
 
@@ -471,6 +482,7 @@ def _residual_norm(residual, update, gate, post_weight, pre_weight, post_norm, r
             n = _new(residual.shape, dtype if update is None else update.dtype, device, stream)
         a = _lib.resnorm(residual, update, gate, post_weight, pre_weight, r, n, post_norm, residual_scale, eps)
         _lib.mu_residual_norm(a, st)
+        _wrote(out, normed_out)
         return r, n, a
     return _on(device, stream, call)
 
@@ -549,6 +561,7 @@ def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, s
         a = _lib.gated(x, w_gate, w_up, h, gates, activation)
         ws = _lib.scratch(_lib.mu_gated_mlp_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_gated_mlp(a, ws, st)
+        _wrote(out, gates_out)
         return h, gates, a
     return _on(device, stream, call)
 
@@ -599,5 +612,6 @@ def gated_mlp_grad(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
         a = _lib.gated_grad(grad, x, w_gate, w_up, gates, dx, dg, du, accumulate, activation)
         ws = _lib.scratch(_lib.mu_gated_mlp_grad_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_gated_mlp_grad(a, ws, st)
+        _wrote(d_gate, d_up)
         return dx, dg, du
     return _on(device, stream, call)
