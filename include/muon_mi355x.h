@@ -415,7 +415,10 @@ int mu_qk_max_logits(const mu_qk_logits* a, void* workspace, size_t workspace_by
  * x, out     element (b, s, h, d) at b * stride_b + s * stride_s + h * stride_h
  *            + d (strides in elements, >= 0), of dtype; out is x itself (the
  *            same strides: in place, elements from `part` on are not touched)
- *            or shares no element with an input, nor with another output
+ *            or shares no element with an input, nor with another output. (Of
+ *            views that lie in one range of memory this is seen where their
+ *            strides agree, as those of one buffer's do, or where they are column
+ *            ranges of rows of one pitch; others are taken as overlapping.)
  * part is even, 2 <= part <= dim <= MU_ROTARY_MAX_DIM. No workspace.
  */
 #define MU_ROTARY_MAX_DIM 1024

@@ -160,17 +160,57 @@ struct View {
     }
 };
 
-// Views that share no element: apart in memory, or column ranges of rows of one pitch.
+// Whether delta + sum of x[i] * s[i] + e = 0 has a solution in whole numbers lo[i] <= x[i] <= hi[i]
+// and |e| < dim: whether two views of the same strides share an element, x being the differences
+// of their indices. Strides descend; where they nest at most two x of each are in reach of the
+// strides behind it. `left` bounds the search for any others, which then counts as a yes.
+struct Steps {
+    int64_t s[3], lo[3], hi[3];
+    int n;
+};
+bool meet(const Steps& t, int i, int64_t delta, int64_t dim, int& left) {
+    if (i == t.n) return delta > -dim && delta < dim;
+    int64_t reach = dim - 1;
+    for (int j = i + 1; j < t.n; ++j) reach += t.s[j] * std::max(-t.lo[j], t.hi[j]);
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0 ? 1 : 0); };
+    const int64_t lo = std::max(t.lo[i], -floor_div(delta + reach, t.s[i])), hi = std::min(t.hi[i], floor_div(reach - delta, t.s[i]));
+    for (int64_t x = lo; x <= hi; ++x)
+        if (--left < 0 || meet(t, i + 1, delta + x * t.s[i], dim, left)) return true;
+    return false;
+}
+
+// Views that share no element: apart in memory, of the same strides (of sizes above one) with
+// no element in common, or column ranges of rows of one pitch.
 bool apart(View a, View b) {
     if (a.empty() || b.empty() || a.hi() <= b.lo() || b.hi() <= a.lo()) return true;
+    const struct { int64_t na, nb, sa, sb; } d[3] = {{a.batch, b.batch, a.sb, b.sb}, {a.len, b.len, a.ss, b.ss}, {a.heads, b.heads, a.sh, b.sh}};
+    Steps t{{}, {}, {}, 0};
+    bool alike = true;
+    for (const auto& x : d) {
+        if (x.na == 1 && x.nb == 1) continue;
+        if (x.na > 1 && x.nb > 1 && x.sa != x.sb) alike = false;
+        const int64_t s = x.na > 1 ? x.sa : x.sb;
+        if (s == 0) continue;   // (an input's: one element for all indices)
+        int i = t.n++;
+        for (; i > 0 && t.s[i - 1] < s; --i) {
+            t.s[i] = t.s[i - 1];
+            t.lo[i] = t.lo[i - 1];
+            t.hi[i] = t.hi[i - 1];
+        }
+        t.s[i] = s;
+        t.lo[i] = 1 - x.na;
+        t.hi[i] = x.nb - 1;
+    }
+    int left = 64;
+    if (alike) return !meet(t, 0, ((int64_t)b.lo() - (int64_t)a.lo()) / (int64_t)a.es, a.dim, left);
     if (a.lo() > b.lo()) std::swap(a, b);
     for (View* v : {&a, &b})
         if (v->len == 1) { v->len = v->batch; v->ss = v->sb; v->batch = 1; }
     if (a.ss != b.ss || a.ss <= 0 || a.len == 1) return false;
     if ((a.batch > 1 && a.sb % a.ss != 0) || (b.batch > 1 && b.sb % b.ss != 0)) return false;
     const int64_t pitch = a.ss * (int64_t)a.es, ra = a.row() * (int64_t)a.es, rb = b.row() * (int64_t)b.es;
-    const int64_t d = (int64_t)((b.lo() - a.lo()) % pitch);   // b's first column behind a's
-    return d >= ra && d + rb <= pitch;
+    const int64_t c = (int64_t)((b.lo() - a.lo()) % pitch);   // b's first column behind a's
+    return c >= ra && c + rb <= pitch;
 }
 
 int check(const mu_rotary_args* a) {
