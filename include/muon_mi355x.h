@@ -464,8 +464,8 @@ int mu_rotary(const mu_rotary_args* a, void* stream);
  *            it is, and post_weight is NULL
  * pre_weight NULL: weights of 1
  * gate       [groups, dim], row i taking gate row i / (rows / groups) (groups
- *            divides rows: 1 for all rows, the batch's sequences, or every row);
- *            NULL: no gate (groups 1)
+ *            divides rows: 1 for all rows, the batch's sequences, or every row;
+ *            0 is possible where there are no rows); NULL: no gate (groups 1)
  * update     NULL: n = N(residual_scale * r; pre) alone; then new_residual,
  *            gate and post_weight are NULL
  * weight_dtype is that of the weights and the gate. new_residual may be the

@@ -435,13 +435,13 @@ int check_common(const mu_resnorm* a) {
         return fail(MU_ERR_DTYPE, "a bfloat16 residual takes no float32 update");
     if (a->dim < 1 || a->dim > MU_RESNORM_MAX_DIM) return fail(MU_ERR_INVALID_ARG, "dim must be in [1, %d]", MU_RESNORM_MAX_DIM);
     if (a->rows < 0 || a->rows > ((int64_t)1 << 40)) return fail(MU_ERR_INVALID_ARG, "bad row count");
-    if (a->groups < 1 || (a->rows > 0 && a->rows % a->groups != 0) || a->groups > ((int64_t)1 << 40))
-        return fail(MU_ERR_INVALID_ARG, "groups must be >= 1 and divide rows");
+    if (a->groups < (a->rows > 0 ? 1 : 0) || (a->rows > 0 && a->rows % a->groups != 0) || a->groups > ((int64_t)1 << 40))
+        return fail(MU_ERR_INVALID_ARG, "groups must be >= 1 (no rows: >= 0) and divide rows");
     if (a->post_norm != 0 && a->post_norm != 1) return fail(MU_ERR_INVALID_ARG, "post_norm must be 0 or 1");
     if (!std::isfinite(a->residual_scale)) return fail(MU_ERR_INVALID_ARG, "residual_scale must be finite");
     if (!(a->eps > 0.f) || !std::isfinite(a->eps)) return fail(MU_ERR_INVALID_ARG, "eps must be > 0 and finite");
     if (a->post_weight && !a->post_norm) return fail(MU_ERR_INVALID_ARG, "post_weight without post_norm");
-    if (!a->gate && a->groups != 1) return fail(MU_ERR_INVALID_ARG, "groups without a gate");
+    if (!a->gate && a->groups > 1) return fail(MU_ERR_INVALID_ARG, "groups without a gate");
     return MU_OK;
 }
 
@@ -502,9 +502,9 @@ constexpr int MIN_ROWS = 4;       // rows of a workgroup at least: its partial s
 GradPlan plan_of(const mu_resnorm_grad* a) {
     const mu_resnorm& f = a->fwd;
     GradPlan p{};
-    const int64_t per_group = f.rows / f.groups, target = f.dim > 2048 ? TARGET_WGS / 2 : TARGET_WGS;
+    const int64_t per_group = f.rows ? f.rows / f.groups : 0, target = f.dim > 2048 ? TARGET_WGS / 2 : TARGET_WGS;
     const int64_t least = f.dim <= 64 ? 32 : f.dim <= 128 ? 16 : f.dim <= 256 ? 8 : MIN_ROWS;   // a row for each team
-    p.cuts = std::max<int64_t>(1, std::min(target / f.groups, (per_group + least - 1) / least));
+    p.cuts = std::max<int64_t>(1, std::min(target / std::max<int64_t>(1, f.groups), (per_group + least - 1) / least));
     p.chunk = per_group > 0 ? (per_group + p.cuts - 1) / p.cuts : 1;
     if (per_group > 0) p.cuts = (per_group + p.chunk - 1) / p.chunk;
     p.grid = f.rows == 0 ? 0 : p.cuts > 1 ? f.groups * p.cuts : std::min(f.groups, target);
@@ -616,7 +616,7 @@ int mu_residual_norm_grad(const mu_resnorm_grad* a, void* ws, size_t ws_bytes, v
         b.a = *a;
         b.r = f.update ? f.new_residual : f.residual;
         b.r_scale = f.update ? 1.f : f.residual_scale;
-        b.per_group = f.rows / f.groups;
+        b.per_group = f.rows ? f.rows / f.groups : 0;
         b.groups = f.groups;
         b.chunk = p.chunk;
         b.cuts = p.cuts;
