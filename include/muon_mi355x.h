@@ -527,7 +527,8 @@ int mu_residual_norm_grad(const mu_resnorm_grad* a, void* workspace, size_t work
  * the gradient. activation: MU_ACT_SILU g / (1 + e^-g), MU_ACT_GELU (the normal
  * distribution's), MU_ACT_GELU_TANH (its tanh form), MU_ACT_RELU.
  * Outputs overlap neither each other nor an input. dim and hidden up to
- * MU_GATED_MAX_DIM.
+ * MU_GATED_MAX_DIM; a product of more than 2^23 tiles (of 64 to 256 rows and 32
+ * to 256 columns) is refused, here and in the gradient.
  */
 #define MU_ACT_SILU 0
 #define MU_ACT_GELU 1

@@ -403,6 +403,10 @@ Source source(const void* p, int64_t rows, int64_t n, int es, Plan& pl) {
     return s;
 }
 
+int64_t tiles_of(int64_t m, int64_t n, int nmat, bool dual, int edge) {
+    return nmat * ceil_div(m, edge) * ceil_div(n, dual ? edge / 2 : edge);
+}
+
 // Tiles of 256 (bfloat16) where they fill half the chip: they then run at twice the rate
 // of the others. Else 128 where those give every compute unit one, and 64. Measured on
 // kernels of 768 x 2048 (bfloat16, us, edge 64 against 128): forward of 1000 tokens
@@ -418,7 +422,7 @@ Source source(const void* p, int64_t rows, int64_t n, int es, Plan& pl) {
 // 48 tiles, 1, 2, 4 splits 21.9, 18.1, 16.6 us, float32 78, 47, 31; 64 tokens of 4096 x
 // 14336, 64 tiles, 103, 60, 38.5; 1000 tokens of 768, float32, 192 tiles, 82, 78, 66.
 Cut cut_of(int64_t m, int64_t n, int nmat, bool dual, int64_t kts, int dtype, bool split) {
-    auto tiles = [&](int e) { return nmat * ceil_div(m, e) * ceil_div(n, dual ? e / 2 : e); };
+    auto tiles = [&](int e) { return tiles_of(m, n, nmat, dual, e); };
     Cut c{128, (int)kts, 1};
     if (dtype == MU_BF16 && tiles(256) >= 128) c.edge = 256;
     else if (tiles(128) < 256) c.edge = 64;
@@ -472,6 +476,20 @@ Plan plan_bwd(const mu_gated_grad* a) {
     return p;
 }
 
+// What a call launches fits its grids: seen before the first of its launches.
+constexpr int64_t MAX_TILES = 1 << 23, MAX_JOIN_WGS = (1 << 24) - 1;
+int check_plan(const mu_gated* a, const Plan& p) {
+    if (tiles_of(a->tokens, a->hidden, 1, true, p.fwd.edge) > MAX_TILES) return fail(MU_ERR_INVALID_ARG, "too many tiles for one launch");
+    return MU_OK;
+}
+int check_plan(const mu_gated_grad* a, const Plan& p) {
+    if ((!a->gate && tiles_of(a->tokens, a->hidden, 1, true, p.fwd.edge) > MAX_TILES) ||
+        (a->dx && tiles_of(a->tokens, a->dim, 1, false, p.dx.edge) > MAX_TILES) ||
+        (a->d_gate && tiles_of(a->hidden, a->dim, 2, false, p.dw.edge) > MAX_TILES))
+        return fail(MU_ERR_INVALID_ARG, "too many tiles for one launch");
+    return MU_OK;
+}
+
 const void* at(const Source& s, const char* ws) { return s.copied ? ws + s.off : s.p; }
 
 // The padded copies of a call, one launch.
@@ -501,7 +519,6 @@ template <typename T, int MODE>
 int product(int kernel, TileArgs a, const Cut& c, double flops, double bytes, hipStream_t s) {
     const int64_t tm = ceil_div(a.m, c.edge) * (MODE == DW ? 2 : 1);
     const int64_t tn = ceil_div(a.n, MODE == FWD || MODE == RECOMP ? c.edge / 2 : c.edge);
-    if (tm * tn > (1 << 23)) return fail(MU_ERR_INVALID_ARG, "too many tiles for one launch");
     a.tiles_m = (int)tm;
     a.tiles_n = (int)tn;
     a.kt_split = c.kt;
@@ -518,8 +535,7 @@ int product(int kernel, TileArgs a, const Cut& c, double flops, double bytes, hi
 }
 
 int join(const JoinArgs& j, hipStream_t s) {
-    const int64_t wgs = ceil_div(j.n, 8 * NTHR);
-    if (wgs > (1 << 24) - 1) return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
+    const int64_t wgs = ceil_div(j.n, 8 * NTHR);   // (within MAX_JOIN_WGS: splits have few tiles, zeros are checked)
     return timed_launch(MU_K_GATED_GRAD, 0.0, 0.0, s, [&] {
         hipLaunchKernelGGL(k_join, dim3((unsigned)wgs, j.out[1] ? 2 : 1), dim3(NTHR), 0, s, j);
         return hipGetLastError();
@@ -673,6 +689,8 @@ int check_bwd(const mu_gated_grad* a) {
     if (!a->gate != !a->up) return fail(MU_ERR_INVALID_ARG, "gate and up go together");
     if (a->tokens > 0 && (!a->grad_h || !a->x || !a->w_gate || !a->w_up))
         return fail(MU_ERR_INVALID_ARG, "null grad_h, x, w_gate or w_up");
+    if (a->tokens == 0 && a->d_gate && !a->accumulate && ceil_div(a->hidden * a->dim, 8 * NTHR) > MAX_JOIN_WGS)
+        return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
     const size_t es = es_of(a->dtype), eg = es_of(a->grad_dtype);
     const int64_t nx = a->tokens * a->dim, nw = a->hidden * a->dim, nh = a->tokens * a->hidden;
     return check_buffers({Buf{a->grad_h, nh, es}, Buf{a->x, nx, es}, Buf{a->w_gate, nw, es}, Buf{a->w_up, nw, es},
@@ -697,8 +715,9 @@ int mu_gated_mlp_workspace_size(const mu_gated* a, size_t* bytes) {
         if (!bytes) return fail(MU_ERR_INVALID_ARG, "bytes is null");
         int rc = check_fwd(a);
         if (rc) return rc;
-        *bytes = a->tokens == 0 ? 0 : plan_fwd(a).bytes;
-        return MU_OK;
+        const Plan p = a->tokens == 0 ? Plan{} : plan_fwd(a);
+        *bytes = p.bytes;
+        return a->tokens == 0 ? MU_OK : check_plan(a, p);
     });
 }
 
@@ -707,7 +726,8 @@ int mu_gated_mlp(const mu_gated* a, void* ws, size_t ws_bytes, void* stream) {
         int rc = check_fwd(a);
         if (rc || a->tokens == 0) return rc;
         const Plan p = plan_fwd(a);
-        rc = check_workspace(ws, ws_bytes, p.bytes);
+        rc = check_plan(a, p);
+        if (!rc) rc = check_workspace(ws, ws_bytes, p.bytes);
         if (rc) return rc;
         hipStream_t s = (hipStream_t)stream;
         return a->dtype == MU_BF16 ? run_fwd<bf16>(a, p, (char*)ws, s) : run_fwd<float>(a, p, (char*)ws, s);
@@ -719,8 +739,9 @@ int mu_gated_mlp_grad_workspace_size(const mu_gated_grad* a, size_t* bytes) {
         if (!bytes) return fail(MU_ERR_INVALID_ARG, "bytes is null");
         int rc = check_bwd(a);
         if (rc) return rc;
-        *bytes = a->tokens == 0 ? 0 : plan_bwd(a).bytes;
-        return MU_OK;
+        const Plan p = a->tokens == 0 ? Plan{} : plan_bwd(a);
+        *bytes = p.bytes;
+        return a->tokens == 0 ? MU_OK : check_plan(a, p);
     });
 }
 
@@ -734,7 +755,8 @@ int mu_gated_mlp_grad(const mu_gated_grad* a, void* ws, size_t ws_bytes, void* s
             return join(JoinArgs{nullptr, {a->d_gate, a->d_up}, a->hidden * a->dim, 0, a->grad_dtype == MU_F32, false}, s);
         }
         const Plan p = plan_bwd(a);
-        rc = check_workspace(ws, ws_bytes, p.bytes);
+        rc = check_plan(a, p);
+        if (!rc) rc = check_workspace(ws, ws_bytes, p.bytes);
         if (rc) return rc;
         return a->dtype == MU_BF16 ? run_bwd<bf16>(a, p, (char*)ws, s) : run_bwd<float>(a, p, (char*)ws, s);
     });
