@@ -80,7 +80,9 @@ __device__ __forceinline__ void act_of(int kind, float g, float& a, float& slope
             const float k = 0.79788456f, q = 0.044715f;
             const float s = sigmoid<FAST>(2.f * k * (g + q * g * g * g));
             a = g * s;
-            slope = s + g * s * (1.f - s) * (2.f * k * (1.f + 3.f * q * g * g));
+            // (far from zero s is 1 or 0, and the factor's square may have left float32)
+            const float t = g * s * (1.f - s);
+            slope = t == 0.f ? s : s + t * (2.f * k * (1.f + 3.f * q * g * g));
             return;
         }
         default:
