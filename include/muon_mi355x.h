@@ -456,7 +456,8 @@ int mu_rotary(const mu_rotary_args* a, void* stream);
  *   r' = residual_scale * r + gate * N(y; post)        (new_residual)
  *   n  = N(r'; pre)                                    (normed)
  * over rows of dim elements, in float32, each result rounded once (n is that of
- * the unrounded r'). The squares are float32 sums: elements below 1e18.
+ * the unrounded r'). The sum of a row's squares, of y and of r', has to stay in
+ * float32: below 3.4e38, which elements up to 1e17 do at any length.
  *
  * residual, new_residual [rows, dim] residual_dtype; update (y) and normed
  *            [rows, dim] dtype: one type, or a float32 residual with bfloat16
