@@ -363,12 +363,16 @@ def rotary(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, freqs: torch.Te
     2 i + 1) with interleaved. positions (int32 or int64, [batch, length], [length]
     or [rows]) default to 0, 1, ..; offset is added to them. inverse turns back.
     freqs: float64 (rotary_frequencies). `out` (q's, or a pair) may be the inputs
-    themselves. Differentiable in q and k unless `out` is given."""
+    themselves. Differentiable in q and k unless `out` is given; freqs that ask for
+    a gradient are refused."""
     xs = (q,) if k is None else (q, k)
     if out is not None:
         out = (out,) if isinstance(out, torch.Tensor) else tuple(out)
         if len(out) != len(xs):
             raise ValueError("out must have one tensor for each of q and k")
+    _no_tangents("rotary", freqs)
+    if freqs.requires_grad and torch.is_grad_enabled():
+        raise NotImplementedError("rotary has no gradient of freqs")
     if _differentiable("rotary", xs, out):
         res = _Rotary.apply(q, k, freqs, positions, offset, interleaved, scale, inverse, stream)
     else:

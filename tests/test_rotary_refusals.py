@@ -1,0 +1,24 @@
+"""Calls of rotary whose results would silently lack something, refused on a
+machine without a GPU: a gradient or tangent of the frequencies."""
+
+import pytest
+import torch
+
+
+@pytest.mark.parametrize("needs", ["freqs", "both"])
+def test_no_gradient_of_the_frequencies(needs):
+    import newton_schulz_orthogonalized_amd as nso
+    q = torch.zeros(2, 5, 4, 16, requires_grad=needs == "both")
+    freqs = nso.rotary_frequencies(16, device="cpu").requires_grad_()
+    with pytest.raises(NotImplementedError, match="freqs"):
+        nso.rotary(q, freqs=freqs)
+    with torch.no_grad(), pytest.raises(ValueError, match="GPU"):     # nothing asked for: on to the next check
+        nso.rotary(q, freqs=freqs)
+
+
+def test_no_tangent_of_the_frequencies():
+    import newton_schulz_orthogonalized_amd as nso
+    with torch.autograd.forward_ad.dual_level():
+        f = nso.rotary_frequencies(16, device="cpu")
+        with pytest.raises(NotImplementedError):
+            nso.rotary(torch.zeros(2, 5, 4, 16), freqs=torch.autograd.forward_ad.make_dual(f, f))
