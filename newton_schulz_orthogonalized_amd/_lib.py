@@ -619,6 +619,8 @@ def rotary_args(xs, outs, freqs, positions, offset: int, interleaved: bool, inve
     if freqs.dtype != torch.float64 or freqs.dim() != 1:
         raise TypeError("freqs must be a float64 vector (rotary_frequencies)")
     _require(freqs, "freqs")
+    if not -1 << 52 <= offset <= 1 << 52:   # (the field would take its low 64 bits)
+        raise ValueError("offset is too large")
     a.batch, a.len = (1, shape[0]) if packed else shape[:2]
     if positions is not None:
         rows = shape[:-2]
