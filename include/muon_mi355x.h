@@ -524,8 +524,9 @@ int mu_residual_norm_grad(const mu_resnorm_grad* a, void* workspace, size_t work
  *   g = x w_gate^T,  u = x w_up^T,  h = act(g) * u
  * x [tokens, dim], w_gate and w_up [hidden, dim], h [tokens, hidden], all of
  * dtype; products accumulate in float32 and h is rounded once from unrounded g
- * and u. gate_out and up_out (both or neither) receive g and u, rounded, for
- * the gradient. activation: MU_ACT_SILU g / (1 + e^-g), MU_ACT_GELU (the normal
+ * and u. gate_out and up_out (both or neither) receive g and u for the
+ * gradient, rounded to dtype, or float32 where MU_GATES_F32 is added to the
+ * activation. activation: MU_ACT_SILU g / (1 + e^-g), MU_ACT_GELU (the normal
  * distribution's), MU_ACT_GELU_TANH (its tanh form), MU_ACT_RELU.
  * Outputs overlap neither each other nor an input. dim and hidden up to
  * MU_GATED_MAX_DIM; a product of more than 2^23 tiles (of 64 to 256 rows and 32
@@ -535,6 +536,7 @@ int mu_residual_norm_grad(const mu_resnorm_grad* a, void* workspace, size_t work
 #define MU_ACT_GELU 1
 #define MU_ACT_GELU_TANH 2
 #define MU_ACT_RELU 3
+#define MU_GATES_F32 0x100
 #define MU_GATED_MAX_DIM (1 << 20)
 typedef struct mu_gated {
     const void* x;
@@ -556,8 +558,9 @@ int mu_gated_mlp(const mu_gated* a, void* workspace, size_t workspace_bytes, voi
  * Its gradients from grad_h [tokens, hidden]:
  *   dg = grad_h * u * act'(g),  du = grad_h * act(g)     (rounded to dtype)
  *   dx = dg w_gate + du w_up,  d_gate = dg^T x,  d_up = du^T x
- * gate and up are the forward call's gate_out and up_out; both NULL: they are
- * computed again (unrounded) from x and the weights. dx [tokens, dim] of dtype;
+ * gate and up are the forward call's gate_out and up_out, float32 where
+ * MU_GATES_F32 is added to the activation; both NULL: they are computed again
+ * (unrounded) from x and the weights. dx [tokens, dim] of dtype;
  * d_gate and d_up [hidden, dim] of grad_dtype (dtype or float32; both or
  * neither), accumulate = 1: added to what they hold, in float32, rounded once.
  * dx, or d_gate and d_up, may be NULL. Results overlap neither each other nor an

@@ -771,12 +771,14 @@ def mu_residual_norm_grad(a: MuResnormGrad, workspace: Optional[torch.Tensor], s
 
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+MU_GATES_F32 = 0x100
 
 
-def _activation(name: str) -> int:
+def _activation(name: str, gates: Optional[torch.Tensor]) -> int:
+    """The activation's code, with the flag of float32 gates."""
     if name not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)} (got {name!r})")
-    return ACTIVATIONS[name]
+    return ACTIVATIONS[name] | (MU_GATES_F32 if gates is not None and gates.dtype == torch.float32 else 0)
 
 
 def _gated_sizes(x, w_gate, w_up):
@@ -799,12 +801,12 @@ def gated(x, w_gate, w_up, h, gates, activation: str) -> MuGated:
         raise ValueError("out must have x's dtype and shape with hidden in the last place")
     if gates is not None:
         _require(gates, "gates")
-        if gates.shape != (2,) + h.shape or gates.dtype != x.dtype:
-            raise ValueError("gates must be [2, *out's shape] of x's dtype")
+        if gates.shape != (2,) + h.shape or gates.dtype not in (x.dtype, torch.float32):
+            raise ValueError("gates must be [2, *out's shape] of x's dtype or float32")
     half = 0 if gates is None else tokens * hidden * gates.element_size()
     base = _ptr(gates)
     return MuGated(_ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(h), base, base + half if base else None, tokens, dim, hidden,
-                   _dtype_code(x), _activation(activation))
+                   _dtype_code(x), _activation(activation, gates))
 
 
 def mu_gated_mlp_workspace_size(a: MuGated) -> int:
@@ -826,8 +828,8 @@ def gated_grad(grad, x, w_gate, w_up, gates, dx, d_gate, d_up, accumulate: bool,
         raise ValueError("grad must have x's dtype and shape with hidden in the last place")
     if gates is not None:
         _require(gates, "gates")
-        if gates.shape != (2,) + grad.shape or gates.dtype != x.dtype:
-            raise ValueError("gates must be [2, *grad's shape] of x's dtype")
+        if gates.shape != (2,) + grad.shape or gates.dtype not in (x.dtype, torch.float32):
+            raise ValueError("gates must be [2, *grad's shape] of x's dtype or float32")
     if dx is not None:
         _require(dx, "dx")
         if dx.shape != x.shape or dx.dtype != x.dtype:
@@ -843,7 +845,7 @@ def gated_grad(grad, x, w_gate, w_up, gates, dx, d_gate, d_up, accumulate: bool,
     base = _ptr(gates)
     return MuGatedGrad(_ptr(grad), _ptr(x), _ptr(w_gate), _ptr(w_up), base, base + half if base else None, _ptr(dx),
                        _ptr(d_gate), _ptr(d_up), tokens, dim, hidden, _dtype_code(x),
-                       _dtype_code(x if d_gate is None else d_gate), 1 if accumulate else 0, _activation(activation))
+                       _dtype_code(x if d_gate is None else d_gate), 1 if accumulate else 0, _activation(activation, gates))
 
 
 def gated_backward(args: MuGatedGrad, saved, need, grad):
@@ -854,7 +856,7 @@ def gated_backward(args: MuGatedGrad, saved, need, grad):
     a.grad_h, a.x, a.w_gate, a.w_up = grad.data_ptr(), x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr()
     if gates is not None:
         a.gate = gates.data_ptr()
-        a.up = a.gate + grad.numel() * grad.element_size() if a.gate else None
+        a.up = a.gate + grad.numel() * gates.element_size() if a.gate else None
     dx = dg = du = None
     if need[0]:
         dx = torch.empty_like(x)

@@ -542,26 +542,37 @@ def _residual_norm_grad(dr, dn, r, update, gate, post_weight, pre_weight, post_n
 
 
 def gated_mlp(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, *, activation: str = "silu",
-              save_gates: bool = True, out: Optional[torch.Tensor] = None, gates_out: Optional[torch.Tensor] = None,
+              save_gates=torch.float32, out: Optional[torch.Tensor] = None, gates_out: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """act(x @ w_gate.T) * (x @ w_up.T), the input of a gated feed-forward
     block's last projection, in one kernel: x [..., dim], weights [hidden, dim],
     result [..., hidden], of one dtype. activation: "silu", "gelu", "gelu_tanh" or
-    "relu". gates_out [2, ..., hidden] receives both products, which gated_mlp_grad
-    reads. Differentiable in x and the weights unless buffers are given;
-    save_gates=False keeps no products for it and computes them again."""
+    "relu". gates_out [2, ..., hidden], of x's dtype or float32, receives both
+    products, which gated_mlp_grad reads. Differentiable in x and the weights unless
+    buffers are given. save_gates is what is kept of the products for that: float32,
+    as they are; True, rounded to x's dtype (half the memory beside a bfloat16 x, and
+    less exact gradients); False, nothing, they are computed again."""
+    keep = _kept_gates(save_gates, x)
     if _differentiable("gated_mlp", (x, w_gate, w_up), out, gates_out):
-        return _GatedMlp.apply(x, w_gate, w_up, activation, save_gates, workspace, stream)
+        return _GatedMlp.apply(x, w_gate, w_up, activation, keep, workspace, stream)
     return _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream)[0]
 
 
-def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, save=False):
+def _kept_gates(save_gates, x) -> Optional[torch.dtype]:
+    if not isinstance(save_gates, torch.dtype):
+        return x.dtype if save_gates else None
+    if save_gates not in (x.dtype, torch.float32):
+        raise TypeError("save_gates must be True, False, float32 or x's dtype")
+    return save_gates
+
+
+def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, keep=None):
     device = _lib.device_of((x, w_gate, w_up, out, gates_out, workspace), "x, weights and outputs")
 
     def call(st):
         shape = x.shape[:-1] + w_gate.shape[:1]
         h = _new(shape, x.dtype, device, stream) if out is None else out
-        gates = _new((2, *shape), x.dtype, device, stream) if save else gates_out
+        gates = gates_out if keep is None else _new((2, *shape), keep, device, stream)
         a = _lib.gated(x, w_gate, w_up, h, gates, activation)
         ws = _lib.scratch(_lib.mu_gated_mlp_workspace_size(a), device, stream) if workspace is None else workspace
         _lib.mu_gated_mlp(a, ws, st)
@@ -572,8 +583,8 @@ def _gated_mlp(x, w_gate, w_up, activation, out, gates_out, workspace, stream, s
 
 class _GatedMlp(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w_gate, w_up, activation, save_gates, workspace, stream):
-        h, gates, a = _gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream, save_gates)
+    def forward(ctx, x, w_gate, w_up, activation, keep, workspace, stream):
+        h, gates, a = _gated_mlp(x, w_gate, w_up, activation, None, None, workspace, stream, keep)
         ctx.args = _lib.MuGatedGrad(tokens=a.tokens, dim=a.dim, hidden=a.hidden, dtype=a.dtype, grad_dtype=a.dtype,
                                     activation=a.activation)
         ctx.save_for_backward(x, w_gate, w_up, gates)
@@ -594,7 +605,8 @@ def gated_mlp_grad(grad: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_
                    dtype: Optional[torch.dtype] = None, accumulate: bool = False,
                    workspace: Optional[torch.Tensor] = None, stream=None):
     """The gradients (dx, d_gate, d_up) of gated_mlp from its result's. gates is
-    the forward call's gates_out (None: both products are computed again). d_gate
+    the forward call's gates_out, of x's dtype or float32 (None: both products are
+    computed again). d_gate
     and d_up receive the weights' gradients, of x's dtype or float32
     (accumulate=True: added to them, over the micro-batches of a step); dtype is
     that of new ones (default: x's). The same call gives the same bits."""

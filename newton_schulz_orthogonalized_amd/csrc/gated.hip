@@ -18,6 +18,15 @@
 // transposed copy exists. Rows that do not start at 16-byte steps (odd dim) are
 // copied into the workspace with padded rows first.
 //
+// What is rounded to bfloat16 on the way to its gradients: dg and du, where they leave
+// k_slopes or RECOMP, because the matrix instructions that read them take bfloat16 (as two
+// halves each they would be twice the work), and every result. Two roundings leave a
+// gradient 0.0024 of its size off (2048 tokens of 4096 x 14336), one alone 0.0017. g and u
+// are not: the forward call leaves them in float32, which costs 8192 tokens of 4096 x 14336
+// 85 us forward (1435 -> 1520) and 70 in k_slopes against bfloat16. Those, which a caller
+// may choose for half the memory, are a third rounding: 0.0030. (The same block in a
+// library's bfloat16 operations, which round act(g) too: 0.0034 to 0.0039.)
+//
 // Slices of 128 bytes of k (64 bfloat16, 32 float32) move from memory to LDS with
 // direct loads, 1 KB each; what lies outside an operand reads as zero.
 //
@@ -233,8 +242,13 @@ __global__ __launch_bounds__(NTHR, 1) void k_tile(TileArgs A) {
             float o[8], s[8];
             if constexpr (MODE == FWD) {
                 if (A.gates[0]) {
-                    store_run<T, 8>((T*)A.gates[0] + at, cnt, v);
-                    store_run<T, 8>((T*)A.gates[1] + at, cnt, w);
+                    if (ES == 2 && A.gates_f32) {
+                        store_run<float, 8>((float*)A.gates[0] + at, cnt, v);
+                        store_run<float, 8>((float*)A.gates[1] + at, cnt, w);
+                    } else {
+                        store_run<T, 8>((T*)A.gates[0] + at, cnt, v);
+                        store_run<T, 8>((T*)A.gates[1] + at, cnt, w);
+                    }
                 }
                 act_run<FAST>(A.act, v, o);
 #pragma unroll
@@ -309,17 +323,18 @@ __global__ __launch_bounds__(NTHR) void k_join(JoinArgs A) {
     else store_run<bf16, 8>((bf16*)out + i, cnt, s);
 }
 
-// dg and du from the saved g and u: rows of `n`, into rows of `pitch`, zeros behind.
+// dg and du from the saved g and u, of type TG: rows of `n`, into rows of `pitch`, zeros behind.
 // Columns lie along blockIdx.x and rows along blockIdx.y (a division for each run took as
-// long as moving it; four rows a thread 238 us, one 204, for 8192 x 14336 bfloat16). HBM
-// bound: five elements moved for each, 5.8 TB/s there.
+// long as moving it; four rows a thread 238 us, one 204, for 8192 x 14336 bfloat16 with
+// bfloat16 gates). HBM bound: five elements moved for each, 5.8 TB/s there; with float32
+// gates 14 bytes for each, 5.2 TB/s.
 struct SlopeArgs {
     const void *dh, *g, *u;
     void *dg, *du;
     int64_t rows, n, pitch;
     int act;
 };
-template <typename T>
+template <typename T, typename TG>
 __global__ __launch_bounds__(NTHR) void k_slopes(SlopeArgs A) {
     constexpr int V = vec_of<T>();
     const int64_t c = ((int64_t)blockIdx.x * NTHR + threadIdx.x) * V;
@@ -329,8 +344,8 @@ __global__ __launch_bounds__(NTHR) void k_slopes(SlopeArgs A) {
         const int64_t at = row * A.n + c;
         float d[V], g[V], u[V], a[V], s[V];
         load_run<T, V>((const T*)A.dh + at, cnt, d);
-        load_run<T, V>((const T*)A.g + at, cnt, g);
-        load_run<T, V>((const T*)A.u + at, cnt, u);
+        load_run<TG, V>((const TG*)A.g + at, cnt, g);
+        load_run<TG, V>((const TG*)A.u + at, cnt, u);
         slope_run<sizeof(T) == 2>(A.act, g, a, s);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -369,6 +384,7 @@ __global__ __launch_bounds__(NTHR) void k_pack(PackArgs A) {
 // Host
 // ---------------------------------------------------------------------------
 size_t es_of(int dtype) { return dtype == MU_BF16 ? 2 : 4; }
+bool gates_f32(int dtype, int activation) { return dtype == MU_F32 || (activation & MU_GATES_F32); }
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -555,14 +571,15 @@ int run_fwd(const mu_gated* a, const Plan& p, char* ws, hipStream_t s) {
     t.m = a->tokens;
     t.n = a->hidden;
     t.k = a->dim;
-    t.act = a->activation;
+    t.act = a->activation & ~MU_GATES_F32;
     t.out[0] = a->h;
     t.ldo = a->hidden;
     t.gates[0] = a->gate_out;
     t.gates[1] = a->up_out;
+    t.gates_f32 = gates_f32(a->dtype, a->activation);
     const double n = (double)a->tokens, d = (double)a->dim, f = (double)a->hidden;
     return product<T, FWD>(MU_K_GATED, t, p.fwd, 4.0 * n * d * f,
-                           sizeof(T) * (n * d + 2 * d * f + (a->gate_out ? 3 : 1) * n * f), s);
+                           sizeof(T) * (n * d + 2 * d * f + n * f) + (a->gate_out ? (t.gates_f32 ? 8 : 4) * n * f : 0.0), s);
 }
 
 template <typename T>
@@ -581,18 +598,20 @@ int run_bwd(const mu_gated_grad* a, const Plan& p, char* ws, hipStream_t s) {
         t.m = a->tokens;
         t.n = a->hidden;
         t.k = a->dim;
-        t.act = a->activation;
+        t.act = a->activation & ~MU_GATES_F32;
         t.dh = a->grad_h;
         t.out[0] = dg;
         t.out[1] = du;
         t.ldo = p.pitch_h;
         rc = product<T, RECOMP>(MU_K_GATED_GRAD, t, p.fwd, 4.0 * n * d * f, sizeof(T) * (n * d + 2 * d * f + 3 * n * f), s);
     } else {
-        rc = timed_launch(MU_K_GATED_GRAD, 0.0, 5.0 * sizeof(T) * n * f, s, [&] {
+        const bool f32 = gates_f32(a->dtype, a->activation);
+        rc = timed_launch(MU_K_GATED_GRAD, 0.0, (3.0 * sizeof(T) + (f32 ? 8 : 4)) * n * f, s, [&] {
             const dim3 grid((unsigned)ceil_div(p.pitch_h, vec_of<T>() * NTHR),
                             (unsigned)std::min<int64_t>(a->tokens, 65535));
-            hipLaunchKernelGGL(k_slopes<T>, grid, dim3(NTHR), 0, s,
-                               SlopeArgs{a->grad_h, a->gate, a->up, dg, du, a->tokens, a->hidden, p.pitch_h, a->activation});
+            const SlopeArgs sa{a->grad_h, a->gate, a->up, dg, du, a->tokens, a->hidden, p.pitch_h, a->activation & ~MU_GATES_F32};
+            if (f32) hipLaunchKernelGGL((k_slopes<T, float>), grid, dim3(NTHR), 0, s, sa);
+            else hipLaunchKernelGGL((k_slopes<T, T>), grid, dim3(NTHR), 0, s, sa);
             return hipGetLastError();
         }, "gated feed-forward slopes launch");
     }
@@ -658,7 +677,8 @@ int check_buffers(const Buf (&in)[NI], const Buf (&out)[NO]) {
 
 int check_sizes(int64_t tokens, int64_t dim, int64_t hidden, int dtype, int act) {
     if (dtype != MU_F32 && dtype != MU_BF16) return fail(MU_ERR_DTYPE, "unknown dtype %d", dtype);
-    if (act < MU_ACT_SILU || act > MU_ACT_RELU) return fail(MU_ERR_INVALID_ARG, "unknown activation %d", act);
+    const int kind = act & ~MU_GATES_F32;
+    if (kind < MU_ACT_SILU || kind > MU_ACT_RELU) return fail(MU_ERR_INVALID_ARG, "unknown activation %d", act);
     if (tokens < 0 || tokens > 0x7fffffffLL) return fail(MU_ERR_INVALID_ARG, "bad token count");
     if (dim < 1 || dim > MU_GATED_MAX_DIM || hidden < 1 || hidden > MU_GATED_MAX_DIM)
         return fail(MU_ERR_INVALID_ARG, "dim and hidden must be in [1, %d]", MU_GATED_MAX_DIM);
@@ -672,10 +692,10 @@ int check_fwd(const mu_gated* a) {
     if (!a->gate_out != !a->up_out) return fail(MU_ERR_INVALID_ARG, "gate_out and up_out go together");
     if (a->tokens == 0) return MU_OK;
     if (!a->x || !a->w_gate || !a->w_up || !a->h) return fail(MU_ERR_INVALID_ARG, "null x, w_gate, w_up or h");
-    const size_t es = es_of(a->dtype);
+    const size_t es = es_of(a->dtype), ega = gates_f32(a->dtype, a->activation) ? 4 : 2;
     const int64_t nx = a->tokens * a->dim, nw = a->hidden * a->dim, nh = a->tokens * a->hidden;
     return check_buffers({Buf{a->x, nx, es}, Buf{a->w_gate, nw, es}, Buf{a->w_up, nw, es}},
-                         {Buf{a->h, nh, es}, Buf{a->gate_out, nh, es}, Buf{a->up_out, nh, es}});
+                         {Buf{a->h, nh, es}, Buf{a->gate_out, nh, ega}, Buf{a->up_out, nh, ega}});
 }
 
 int check_bwd(const mu_gated_grad* a) {
@@ -691,10 +711,10 @@ int check_bwd(const mu_gated_grad* a) {
         return fail(MU_ERR_INVALID_ARG, "null grad_h, x, w_gate or w_up");
     if (a->tokens == 0 && a->d_gate && !a->accumulate && ceil_div(a->hidden * a->dim, 8 * NTHR) > MAX_JOIN_WGS)
         return fail(MU_ERR_INVALID_ARG, "too many elements for one launch");
-    const size_t es = es_of(a->dtype), eg = es_of(a->grad_dtype);
+    const size_t es = es_of(a->dtype), eg = es_of(a->grad_dtype), ega = gates_f32(a->dtype, a->activation) ? 4 : 2;
     const int64_t nx = a->tokens * a->dim, nw = a->hidden * a->dim, nh = a->tokens * a->hidden;
     return check_buffers({Buf{a->grad_h, nh, es}, Buf{a->x, nx, es}, Buf{a->w_gate, nw, es}, Buf{a->w_up, nw, es},
-                          Buf{a->gate, nh, es}, Buf{a->up, nh, es}},
+                          Buf{a->gate, nh, ega}, Buf{a->up, nh, ega}},
                          {Buf{a->dx, nx, es}, Buf{a->d_gate, nw, eg}, Buf{a->d_up, nw, eg}});
 }
 

@@ -130,6 +130,7 @@ struct TileArgs {
     const void* dh;            // RECOMP
     float* part;               // DX, split: [splits][m][n] float32 sums
     bool out_f32;              // DW: float32 results
+    bool gates_f32;            // FWD: g and u leave as float32, unrounded
     bool accumulate;           // DW
     bool aligned;              // the wide kernel: results' rows start at 16-byte steps
 };

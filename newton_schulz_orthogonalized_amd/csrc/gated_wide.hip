@@ -412,8 +412,13 @@ __global__ __launch_bounds__(NTHR, 1) void k_wide(TileArgs A) {
                     run(2 * p, y);
                     run(2 * p + 1, z);
                     if (MODE == FWD && A.gates[0]) {
-                        put((bf16*)A.gates[0], A.ldo, p, cnt, y);
-                        put((bf16*)A.gates[1], A.ldo, p, cnt, z);
+                        if (A.gates_f32) {
+                            put32((float*)A.gates[0], A.ldo, p, y);
+                            put32((float*)A.gates[1], A.ldo, p, z);
+                        } else {
+                            put((bf16*)A.gates[0], A.ldo, p, cnt, y);
+                            put((bf16*)A.gates[1], A.ldo, p, cnt, z);
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) { v[8 * p + e] = y[e]; w[8 * p + e] = z[e]; }
