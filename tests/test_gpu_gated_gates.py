@@ -121,3 +121,32 @@ def test_what_autograd_keeps(t, d, f, dtype):
             assert torch.equal(nso.gated_mlp(*leaves, activation="gelu", gates_out=gates), h)
             want = nso.gated_mlp_grad(dh, *leaves, gates, activation="gelu")
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_gates_of_more_than_2_31_elements():
+    """Integers that bfloat16 holds: both types of gates hold the same values, at both
+    ends and around the places where 31- and 32-bit offsets would turn over, and give
+    the same gradients."""
+    import newton_schulz_orthogonalized_amd as nso
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 100 GB of device memory")
+    t, d, f = 150001, 64, 14336
+    g = torch.Generator(device="cuda")
+    g.manual_seed(99400)
+
+    def ints(shape, top, keep):
+        v = torch.randint(-top, top + 1, shape, generator=g, device="cuda", dtype=torch.int8)
+        return (v * (torch.rand(shape, generator=g, device="cuda") < keep)).to(BF)
+    x, wg, wu, dh = ints((t, d), 2, 1.0), ints((f, d), 2, 0.15), ints((f, d), 2, 0.15), ints((t, f), 1, 0.05)
+    gates = torch.empty((2, t, f), device="cuda")
+    nso.gated_mlp(x, wg, wu, activation="relu", gates_out=gates)
+    rows = torch.tensor(sorted({0, 1, t - 2, t - 1} | {e // f + i for e in (1 << 29, 1 << 30, 1 << 31) for i in (-1, 0, 1) if e // f + i < t}),
+                        device="cuda")
+    for v, w in zip(gates, (wg, wu)):
+        assert torch.equal(v[rows].double(), x[rows].double() @ w.double().t())
+    got = nso.gated_mlp_grad(dh, x, wg, wu, gates, activation="relu", dtype=FP)
+    small = gates.to(BF)
+    assert float(gates.abs().max()) <= 256
+    del gates
+    want = nso.gated_mlp_grad(dh, x, wg, wu, small, activation="relu", dtype=FP)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
